@@ -19,6 +19,7 @@ LIB_PATH = os.environ.get("CONV2D_LIBRARY") or os.path.join(_HERE, "libconv2d.so
 
 F32, BF16 = 0, 1
 EPI_NONE, EPI_BIAS, EPI_RELU = 0, 1, 2
+ACT_NONE, ACT_RELU, ACT_SILU = 0, 1, 2
 PATH_AUTO, PATH_DIRECT, PATH_DEPTHWISE, PATH_GEMM1X1, PATH_IGEMM = 0, 1, 2, 3, 4
 PATH_IGEMM_GATHER, PATH_IGEMM_HALO = 5, 6
 PATH_NAMES = {PATH_DIRECT: "direct", PATH_DEPTHWISE: "depthwise", PATH_GEMM1X1: "gemm1x1",
@@ -34,6 +35,9 @@ EXPORTS = ("conv2d_fwd", "conv2d_fwd_noalloc", "conv2d_fwd_nhwc_packed", "conv2d
            "conv2d_winograd_weight_bytes", "conv2d_winograd_transform_weights", "conv2d_fwd_winograd_nhwc",
            "conv2d_transpose_fwd", "conv2d_transpose_fwd_nhwc_packed", "conv2d_transpose_pack_weights",
            "conv2d_transpose_out_dim", "conv2d_transpose_check_args", "conv2d_transpose_select_path",
+           "conv2d_group_norm_workspace_bytes", "conv2d_group_norm_nhwc", "conv2d_group_norm_quant_nhwc",
+           "conv2d_group_norm_bwd_nhwc", "conv2d_quantize_rows", "conv2d_int8_matmul_workspace_bytes",
+           "conv2d_int8_matmul",
            "conv2d_packed_weight_bytes",
            "conv2d_pack_weights", "conv2d_nchw_to_nhwc", "conv2d_nhwc_to_nchw",
            "conv2d_out_dim", "conv2d_check_args", "conv2d_select_path",
@@ -80,6 +84,17 @@ def _load() -> ctypes.CDLL:
     lib.conv2d_transpose_check_args.argtypes = [P] * 4 + [I] * 14
     lib.conv2d_transpose_check_args.restype = I
     lib.conv2d_transpose_select_path.argtypes, lib.conv2d_transpose_select_path.restype = [I] * 13, I
+    Z, F = ctypes.c_size_t, ctypes.c_float
+    lib.conv2d_group_norm_workspace_bytes.argtypes, lib.conv2d_group_norm_workspace_bytes.restype = [I] * 6, Z
+    lib.conv2d_group_norm_nhwc.argtypes = [P] * 7 + [Z] + [I] * 7 + [F, I, I, P]
+    lib.conv2d_group_norm_quant_nhwc.argtypes = [P] * 8 + [Z] + [I] * 7 + [F, I, I, P]
+    lib.conv2d_group_norm_bwd_nhwc.argtypes = [P] * 10 + [Z] + [I] * 10 + [P]
+    lib.conv2d_quantize_rows.argtypes = [P] * 3 + [I] * 5 + [P]
+    lib.conv2d_int8_matmul_workspace_bytes.argtypes, lib.conv2d_int8_matmul_workspace_bytes.restype = [I] * 3, Z
+    lib.conv2d_int8_matmul.argtypes = [P] * 7 + [Z] + [I] * 8 + [P]
+    for name in ("conv2d_group_norm_nhwc", "conv2d_group_norm_quant_nhwc", "conv2d_group_norm_bwd_nhwc",
+                 "conv2d_quantize_rows", "conv2d_int8_matmul"):
+        getattr(lib, name).restype = I
     lib.conv2d_packed_weight_bytes.argtypes = [I] * 6
     lib.conv2d_packed_weight_bytes.restype = ctypes.c_size_t
     lib.conv2d_pack_weights.argtypes = [P, P] + [I] * 6 + [P]
@@ -238,6 +253,57 @@ def conv2d_transpose_select_path(N, Cin, H, W, Cout, Kh, Kw, stride, pad, output
                                  dtype) -> int:
     return _check(int(lib.conv2d_transpose_select_path(N, Cin, H, W, Cout, Kh, Kw, stride, pad, output_padding,
                                                        dilation, groups, dtype)), "conv2d_transpose_select_path")
+
+
+def conv2d_group_norm_workspace_bytes(N, C, H, W, G, backward=False) -> int:
+    return int(lib.conv2d_group_norm_workspace_bytes(N, C, H, W, G, int(backward)))
+
+
+def conv2d_group_norm_nhwc(x, gamma, beta, y, mean, rstd, workspace, workspace_bytes, N, C, H, W, G, ldx, ldy, eps,
+                           dtype, act, stream=None) -> None:
+    """Group norm and activation: NHWC x (ldx elements a pixel) -> NHWC y; fp32
+    gamma, beta [C] or None; mean, rstd fp32 [N][G] written, or None."""
+    _check(lib.conv2d_group_norm_nhwc(_ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), _ptr(mean), _ptr(rstd),
+                                      _ptr(workspace), workspace_bytes, N, C, H, W, G, ldx, ldy, eps, dtype, act,
+                                      _stream(stream)), "conv2d_group_norm_nhwc")
+
+
+def conv2d_group_norm_quant_nhwc(x, gamma, beta, q, q_scale, mean, rstd, workspace, workspace_bytes, N, C, H, W, G,
+                                 ldx, ldq, eps, dtype, act, stream=None) -> None:
+    """Group norm and activation, quantised for each pixel: int8 q and fp32
+    q_scale [N*H*W], the rows of conv2d_int8_matmul."""
+    _check(lib.conv2d_group_norm_quant_nhwc(_ptr(x), _ptr(gamma), _ptr(beta), _ptr(q), _ptr(q_scale), _ptr(mean),
+                                            _ptr(rstd), _ptr(workspace), workspace_bytes, N, C, H, W, G, ldx, ldq,
+                                            eps, dtype, act, _stream(stream)), "conv2d_group_norm_quant_nhwc")
+
+
+def conv2d_group_norm_bwd_nhwc(dy, x, gamma, beta, mean, rstd, dx, dgamma, dbeta, workspace, workspace_bytes, N, C,
+                               H, W, G, lddy, ldx, lddx, dtype, act, stream=None) -> None:
+    """Gradients of conv2d_group_norm_nhwc from dy, x and the saved mean and
+    rstd; dgamma, dbeta fp32 [C] or None."""
+    _check(lib.conv2d_group_norm_bwd_nhwc(_ptr(dy), _ptr(x), _ptr(gamma), _ptr(beta), _ptr(mean), _ptr(rstd),
+                                          _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), workspace_bytes, N,
+                                          C, H, W, G, lddy, ldx, lddx, dtype, act, _stream(stream)),
+           "conv2d_group_norm_bwd_nhwc")
+
+
+def conv2d_quantize_rows(x, q, scale, M, K, ldx, ldq, dtype, stream=None) -> None:
+    """fp32 or bf16 rows -> int8 rows and their fp32 scales [M]."""
+    _check(lib.conv2d_quantize_rows(_ptr(x), _ptr(q), _ptr(scale), M, K, ldx, ldq, dtype, _stream(stream)),
+           "conv2d_quantize_rows")
+
+
+def conv2d_int8_matmul_workspace_bytes(M, K, N) -> int:
+    return int(lib.conv2d_int8_matmul_workspace_bytes(M, K, N))
+
+
+def conv2d_int8_matmul(q, q_scale, w, w_scale, bias, y, workspace, workspace_bytes, M, K, N, ldq, ldw, ldy, dtype,
+                       epilogue, stream=None) -> None:
+    """int8 q [M][K] times int8 w [N][K], scaled by row and channel, fp32 bias
+    or None -> y [M][N] of dtype."""
+    _check(lib.conv2d_int8_matmul(_ptr(q), _ptr(q_scale), _ptr(w), _ptr(w_scale), _ptr(bias), _ptr(y),
+                                  _ptr(workspace), workspace_bytes, M, K, N, ldq, ldw, ldy, dtype, epilogue,
+                                  _stream(stream)), "conv2d_int8_matmul")
 
 
 def conv2d_packed_weight_bytes(Cout, Cin, Kh, Kw, groups, dtype) -> int:

@@ -454,6 +454,31 @@ int run_tnhwc(int path, const Shape& s, const void* x, const void* wp, const flo
     return e == hipSuccess ? CONV2D_OK : hip_fail(e, "transposed kernel launch");
 }
 
+// Checks shared by the group-norm entries; fills the sizes of `a`.
+int validate_norm(const NormArgs& a, int H, int W, int act, const void* ws, size_t ws_bytes, int backward) {
+    if (a.dtype != CONV2D_F32 && a.dtype != CONV2D_BF16) return set_error(CONV2D_ERR_DTYPE, "unknown dtype %d", a.dtype);
+    if (act < CONV2D_ACT_NONE || act > CONV2D_ACT_SILU)
+        return set_error(CONV2D_ERR_EPILOGUE, "unknown activation %d", act);
+    if (a.N < 1 || a.C < 1 || H < 1 || W < 1 || a.G < 1)
+        return set_error(CONV2D_ERR_ARG, "sizes must be >= 1 (N=%d C=%d H=%d W=%d G=%d)", a.N, a.C, H, W, a.G);
+    if (a.C % a.G) return set_error(CONV2D_ERR_GROUPS, "C=%d must be divisible by G=%d", a.C, a.G);
+    if (!a.x || !a.y) return set_error(CONV2D_ERR_NULL, "the activations and the output must be non-NULL");
+    if (a.ldx < a.C || a.ldy < a.C || (backward && a.lddy < a.C))
+        return set_error(CONV2D_ERR_ARG, "a pixel stride is below C=%d", a.C);
+    if (!(a.eps >= 0.0f) || a.eps > 3e38f) return set_error(CONV2D_ERR_ARG, "eps must be >= 0 and finite");
+    const size_t eb = a.dtype == CONV2D_F32 ? 4 : 2;
+    if ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.dy)) % eb ||
+        (!a.q_scale && reinterpret_cast<uintptr_t>(a.y) % eb))
+        return set_error(CONV2D_ERR_ALIGN, "a tensor is not aligned to its elements");
+    if (a.C > 4096 || sat_mul({a.N, H, W}) >= INT_MAX || !group_norm_supports(a.N, H * W, a.C))
+        return set_error(CONV2D_ERR_UNSUPPORTED, "group norm takes C <= 4096 and N*H*W < 2^31");
+    const size_t need = conv2d_group_norm_workspace_bytes(a.N, a.C, H, W, a.G, backward);
+    if (!ws) return set_error(CONV2D_ERR_NULL, "the workspace is NULL (%zu bytes needed)", need);
+    if (reinterpret_cast<uintptr_t>(ws) & 15u) return set_error(CONV2D_ERR_ALIGN, "the workspace must be 16-byte aligned");
+    if (ws_bytes < need) return set_error(CONV2D_ERR_ARG, "the workspace has %zu bytes, %zu are needed", ws_bytes, need);
+    return CONV2D_OK;
+}
+
 }  // namespace
 
 int conv2d::grid_limit() { return __atomic_load_n(&g_grid_limit, __ATOMIC_RELAXED); }
@@ -754,6 +779,109 @@ int conv2d_transpose_fwd(const void* x, const void* w, const float* bias, void* 
     rc = run_tnhwc(path, s, xn, wp, bias, yn, stream);
     if (rc) return rc;
     return conv2d_nhwc_to_nchw(yn, y, N, Cout, s.Ho, s.Wo, dtype, stream);
+}
+
+size_t conv2d_group_norm_workspace_bytes(int N, int C, int H, int W, int G, int backward) {
+    if (N < 1 || C < 1 || H < 1 || W < 1 || G < 1 || C % G || C > 4096 || sat_mul({N, H, W}) >= INT_MAX) return 0;
+    return round_up(group_norm_workspace(N, H * W, C, G, backward), 16);
+}
+
+int conv2d_group_norm_nhwc(const void* x, const float* gamma, const float* beta, void* y, float* mean, float* rstd,
+                           void* workspace, size_t workspace_bytes, int N, int C, int H, int W, int G, int ldx,
+                           int ldy, float eps, int dtype, int act, hipStream_t stream) {
+    NormArgs a = {};
+    a.x = x; a.gamma = gamma; a.beta = beta; a.y = y; a.mean = mean; a.rstd = rstd;
+    a.N = N; a.C = C; a.G = G; a.ldx = ldx; a.ldy = ldy; a.eps = eps; a.dtype = dtype;
+    const int rc = validate_norm(a, H, W, act, workspace, workspace_bytes, 0);
+    if (rc) return rc;
+    if (x == y && ldx != ldy) return set_error(CONV2D_ERR_ARG, "in place needs ldy == ldx");
+    a.P = H * W;
+    const hipError_t e = launch_group_norm(a, act, workspace, stream);
+    return e == hipSuccess ? CONV2D_OK : hip_fail(e, "group norm launch");
+}
+
+int conv2d_group_norm_quant_nhwc(const void* x, const float* gamma, const float* beta, void* q, float* q_scale,
+                                 float* mean, float* rstd, void* workspace, size_t workspace_bytes, int N, int C,
+                                 int H, int W, int G, int ldx, int ldq, float eps, int dtype, int act,
+                                 hipStream_t stream) {
+    NormArgs a = {};
+    a.x = x; a.gamma = gamma; a.beta = beta; a.y = q; a.q_scale = q_scale; a.mean = mean; a.rstd = rstd;
+    a.N = N; a.C = C; a.G = G; a.ldx = ldx; a.ldy = ldq; a.eps = eps; a.dtype = dtype;
+    if (!q_scale) return set_error(CONV2D_ERR_NULL, "q_scale must be non-NULL");
+    const int rc = validate_norm(a, H, W, act, workspace, workspace_bytes, 0);
+    if (rc) return rc;
+    a.P = H * W;
+    const hipError_t e = launch_group_norm_quant(a, act, workspace, stream);
+    return e == hipSuccess ? CONV2D_OK : hip_fail(e, "quantised group norm launch");
+}
+
+int conv2d_group_norm_bwd_nhwc(const void* dy, const void* x, const float* gamma, const float* beta,
+                               const float* mean, const float* rstd, void* dx, float* dgamma, float* dbeta,
+                               void* workspace, size_t workspace_bytes, int N, int C, int H, int W, int G, int lddy,
+                               int ldx, int lddx, int dtype, int act, hipStream_t stream) {
+    NormArgs a = {};
+    a.x = x; a.dy = dy; a.gamma = gamma; a.beta = beta; a.y = dx;
+    a.mean = const_cast<float*>(mean); a.rstd = const_cast<float*>(rstd);
+    a.dgamma = dgamma; a.dbeta = dbeta;
+    a.N = N; a.C = C; a.G = G; a.ldx = ldx; a.ldy = lddx; a.lddy = lddy; a.dtype = dtype;
+    if (!dy || !mean || !rstd) return set_error(CONV2D_ERR_NULL, "dy, mean and rstd must be non-NULL");
+    const int rc = validate_norm(a, H, W, act, workspace, workspace_bytes, 1);
+    if (rc) return rc;
+    if ((dx == dy && lddx != lddy) || (dx == x && lddx != ldx))
+        return set_error(CONV2D_ERR_ARG, "in place needs equal pixel strides");
+    a.P = H * W;
+    const hipError_t e = launch_group_norm_bwd(a, act, workspace, stream);
+    return e == hipSuccess ? CONV2D_OK : hip_fail(e, "group norm backward launch");
+}
+
+int conv2d_quantize_rows(const void* x, void* q, float* scale, int M, int K, int ldx, int ldq, int dtype,
+                         hipStream_t stream) {
+    if (dtype != CONV2D_F32 && dtype != CONV2D_BF16) return set_error(CONV2D_ERR_DTYPE, "unknown dtype %d", dtype);
+    if (M < 1 || K < 1) return set_error(CONV2D_ERR_ARG, "sizes must be >= 1 (M=%d K=%d)", M, K);
+    if (ldx < K || ldq < K) return set_error(CONV2D_ERR_ARG, "a row stride is below K=%d", K);
+    if (!x || !q || !scale) return set_error(CONV2D_ERR_NULL, "x, q and scale must be non-NULL");
+    if (reinterpret_cast<uintptr_t>(x) % elem_bytes(dtype))
+        return set_error(CONV2D_ERR_ALIGN, "x is not aligned to its elements");
+    const hipError_t e = launch_quantize_rows(x, q, scale, M, K, ldx, ldq, dtype, stream);
+    return e == hipSuccess ? CONV2D_OK : hip_fail(e, "quantize_rows launch");
+}
+
+size_t conv2d_int8_matmul_workspace_bytes(int M, int K, int N) {
+    if (M < 1 || K < 1 || N < 1) return 0;
+    return round_up(int8_matmul_workspace(M, K, N), 16);
+}
+
+int conv2d_int8_matmul(const void* q, const float* q_scale, const void* w, const float* w_scale, const float* bias,
+                       void* y, void* workspace, size_t workspace_bytes, int M, int K, int N, int ldq, int ldw,
+                       int ldy, int dtype, int epilogue, hipStream_t stream) {
+    if (dtype != CONV2D_F32 && dtype != CONV2D_BF16) return set_error(CONV2D_ERR_DTYPE, "unknown dtype %d", dtype);
+    if (epilogue < 0 || (epilogue & ~(CONV2D_EPI_BIAS | CONV2D_EPI_RELU)))
+        return set_error(CONV2D_ERR_EPILOGUE, "unknown epilogue bits 0x%x", epilogue);
+    if (M < 1 || K < 1 || N < 1) return set_error(CONV2D_ERR_ARG, "sizes must be >= 1 (M=%d K=%d N=%d)", M, K, N);
+    if (ldq < K || ldw < K || ldy < N) return set_error(CONV2D_ERR_ARG, "a row stride is below its row's length");
+    if (!q || !q_scale || !w || !w_scale || !y)
+        return set_error(CONV2D_ERR_NULL, "q, q_scale, w, w_scale and y must be non-NULL");
+    if ((epilogue & CONV2D_EPI_BIAS) && !bias)
+        return set_error(CONV2D_ERR_NULL, "bias is NULL but the epilogue asks for it");
+    if (reinterpret_cast<uintptr_t>(y) % elem_bytes(dtype))
+        return set_error(CONV2D_ERR_ALIGN, "y is not aligned to its elements");
+    if (!int8_matmul_supports(M, K, N, ldq, ldw))
+        return set_error(CONV2D_ERR_UNSUPPORTED, "int8 products take K <= 131071 and row strides up to 2^22");
+    const size_t need = conv2d_int8_matmul_workspace_bytes(M, K, N);
+    if (need) {
+        if (!workspace) return set_error(CONV2D_ERR_NULL, "the workspace is NULL (%zu bytes needed)", need);
+        if (!aligned16(workspace)) return set_error(CONV2D_ERR_ALIGN, "the workspace must be 16-byte aligned");
+        if (workspace_bytes < need)
+            return set_error(CONV2D_ERR_ARG, "the workspace has %zu bytes, %zu are needed", workspace_bytes, need);
+    }
+    Int8Args a;
+    a.q = static_cast<const int8_t*>(q); a.w = static_cast<const int8_t*>(w);
+    a.q_scale = q_scale; a.w_scale = w_scale;
+    a.bias = (epilogue & CONV2D_EPI_BIAS) ? bias : nullptr;
+    a.y = y; a.M = M; a.K = K; a.N = N; a.ldq = ldq; a.ldw = ldw; a.ldy = ldy;
+    a.relu = (epilogue & CONV2D_EPI_RELU) != 0;
+    const hipError_t e = launch_int8_matmul(a, dtype == CONV2D_F32, workspace, stream);
+    return e == hipSuccess ? CONV2D_OK : hip_fail(e, "int8 product launch");
 }
 
 void conv2d_release_scratch(void) {

@@ -1,0 +1,144 @@
+// rowvec.hpp -- device helpers shared by the group-norm and the int8 kernels:
+// vector loads of V fp32 or bf16 elements, the activations and the
+// quantisation of a row to 8 bits.
+#pragma once
+
+#include "common.hpp"
+
+namespace conv2d {
+
+// V consecutive elements of T in one load or store of V * sizeof(T) bytes
+// (2, 4, 8 or 16).
+template <int BYTES> struct RawBytes;
+template <> struct RawBytes<16> { typedef uint4 type; };
+template <> struct RawBytes<8> { typedef uint2 type; };
+template <> struct RawBytes<4> { typedef uint32_t type; };
+template <> struct RawBytes<2> { typedef uint16_t type; };
+template <> struct RawBytes<1> { typedef uint8_t type; };
+
+template <typename T, int V> struct Vec;
+
+template <int V> struct Vec<float, V> {
+    typedef typename RawBytes<4 * V>::type raw;
+    static __device__ __forceinline__ raw load(const float* p) { return *reinterpret_cast<const raw*>(p); }
+    static __device__ __forceinline__ void unpack(const raw& r, float (&v)[V]) {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = __uint_as_float(w[j]);
+    }
+    static __device__ __forceinline__ void store(float* p, const float (&v)[V]) {
+        raw r;
+        uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+        for (int j = 0; j < V; ++j) w[j] = __float_as_uint(v[j]);
+        *reinterpret_cast<raw*>(p) = r;
+    }
+};
+
+template <int V> struct Vec<bf16_t, V> {
+    typedef typename RawBytes<2 * V>::type raw;
+    static __device__ __forceinline__ raw load(const bf16_t* p) { return *reinterpret_cast<const raw*>(p); }
+    static __device__ __forceinline__ void unpack(const raw& r, float (&v)[V]) {
+        if constexpr (V == 1) {
+            v[0] = bf16_to_f32(r);
+        } else {
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) {
+                v[2 * j] = __uint_as_float(w[j] << 16);
+                v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+            }
+        }
+    }
+    // one rounding, to nearest even
+    static __device__ __forceinline__ void store(bf16_t* p, const float (&v)[V]) {
+        if constexpr (V == 1) {
+            *p = f32_to_bf16(v[0]);
+        } else {
+            raw r;
+            uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+            *reinterpret_cast<raw*>(p) = r;
+        }
+    }
+};
+
+// 1 / (1 + exp(-z)) from the hardware's exp2 and reciprocal (1 ulp each).
+__device__ __forceinline__ float sigmoid(float z) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
+}
+
+enum { kActNone = 0, kActRelu = 1, kActSilu = 2 };
+
+// ReLU by comparison: a NaN stays a NaN.
+template <int ACT> __device__ __forceinline__ float activate(float z) {
+    if (ACT == kActRelu) return z < 0.0f ? 0.0f : z;
+    if (ACT == kActSilu) return z * sigmoid(z);
+    return z;
+}
+
+// Sum (or unsigned maximum) over L consecutive lanes, L a power of two <= 64;
+// every lane gets the result.
+__device__ __forceinline__ float lanes_sum(float v, int L) {
+    for (int m = 1; m < L; m <<= 1) v += __shfl_xor(v, m);
+    return v;
+}
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v, int L) {
+    for (int m = 1; m < L; m <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, m));
+    return v;
+}
+
+// ---- a row in 8 bits: a = max(max |v|, 2^-100), q = round(v * (127 / a)),
+// scale = a / 127.  The maximum is taken over the bit patterns of |v|, whose
+// order is that of the values with infinities and NaN above all: a row that
+// holds one of them gets scale NaN and q = 0, so that every product with it
+// is NaN.
+constexpr uint32_t kInfBits = 0x7f800000u;
+
+struct RowScale {
+    float inv;    // 127 / a (0: the row is not finite)
+    float scale;  // a / 127
+};
+
+__device__ __forceinline__ RowScale row_scale(uint32_t amax_bits) {
+    if (amax_bits >= kInfBits) return {0.0f, __uint_as_float(0x7fc00000u)};
+    const float a = fmaxf(__uint_as_float(amax_bits), 0x1p-100f);
+    return {127.0f / a, a / 127.0f};
+}
+
+// The rounded value's low byte, by adding 1.5 * 2^23: the product is rounded
+// to fp32 first (no fused multiply-add), then the sum's rounding to integers
+// is to nearest even.  In a row that is not finite (inv = 0) the product may
+// be NaN: store_quantised writes 0 there.
+__device__ __forceinline__ uint32_t quant_bits(float v, float inv) {
+#pragma clang fp contract(off)
+    const float p = v * inv;
+    return __float_as_uint(p + 12582912.0f);
+}
+
+template <int V>
+__device__ __forceinline__ void store_quantised(int8_t* q, const float (&v)[V], float inv) {
+    typedef typename RawBytes<V>::type raw;
+    uint32_t b[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) b[j] = quant_bits(v[j], inv);
+    raw r;
+    if constexpr (V >= 4) {
+        uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+        for (int j = 0; j < V / 4; ++j) {
+            const uint32_t lo = __builtin_amdgcn_perm(b[4 * j + 1], b[4 * j], 0x0c0c0400u);
+            const uint32_t hi = __builtin_amdgcn_perm(b[4 * j + 3], b[4 * j + 2], 0x04000c0cu);
+            w[j] = inv == 0.0f ? 0u : (lo | hi);
+        }
+    } else {
+        uint32_t w = 0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) w |= (b[j] & 0xffu) << (8 * j);
+        r = (raw)(inv == 0.0f ? 0u : w);
+    }
+    *reinterpret_cast<raw*>(q) = r;
+}
+
+}  // namespace conv2d

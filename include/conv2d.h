@@ -303,6 +303,92 @@ int conv2d_transpose_select_path(int N, int Cin, int H, int W, int Cout, int Kh,
                                  int dtype);
 
 /*
+ * Group normalisation with an activation on channels-last activations: for
+ * image n and group g, over its H*W pixels and C/G channels,
+ *   mean = sum(x) / m,  var = sum((x - mean)^2) / m,  rstd = 1 / sqrt(var + eps)
+ *   z = (x - mean) * rstd * gamma[c] + beta[c],   y = act(z)
+ * with act none, ReLU or SiLU (z / (1 + exp(-z))), m = H*W*C/G.  x, y, dy and
+ * dx are fp32 or bf16 (dtype), [N][H][W] pixels of C channels; ldx, ldy, lddy,
+ * lddx: elements from one pixel to the next (>= C; images follow each other at
+ * H*W of them).  Everything in between is fp32, each output is rounded once.
+ *
+ * conv2d_group_norm_nhwc -- y, and mean and rstd (fp32 [N][G]; either may be
+ *   NULL when it is not wanted).  y may be x itself (ldy == ldx).
+ * conv2d_group_norm_quant_nhwc -- y in 8 bits instead, ready to be the rows of
+ *   conv2d_int8_matmul: q int8 [N][H][W] pixels of C (ldq apart) and q_scale
+ *   fp32 [N*H*W], quantised for each pixel as conv2d_quantize_rows does (the
+ *   unrounded fp32 activations).
+ * conv2d_group_norm_bwd_nhwc -- the gradients, from dy, x and the mean and
+ *   rstd of the forward pass (the pass recomputes z; nothing else is kept):
+ *     dz = dy * act'(z),  dbeta[c] = sum dz,  dgamma[c] = sum dz * xh
+ *     dx = rstd * (gamma dz - mean_m(gamma dz) - xh mean_m(gamma dz xh))
+ *   with xh = (x - mean) rstd and mean_m over the group's m values; ReLU's
+ *   derivative at 0 is 0.  dgamma, dbeta: fp32 [C], written (not added to);
+ *   either may be NULL.  dx may be dy or x (same ld).
+ *
+ * gamma, beta: fp32 [C]; NULL means 1 and 0.  eps >= 0 and finite.  C must be
+ * divisible by G, C <= 4096.  Any channel count, stride and alignment works;
+ * C, the strides and the pointers as multiples of 16 bytes are fastest.
+ * Sums have a fixed order (no atomics): equal calls give equal bits.  A NaN or
+ * infinity spreads through its own (image, group) and no further.
+ *
+ * workspace: device memory of at least conv2d_group_norm_workspace_bytes
+ * (backward: 0 for the two forward calls, 1 for the gradients), 16-byte
+ * aligned, used by the call alone until its work has ended on the stream; its
+ * contents need no clearing.  Too small a workspace returns CONV2D_ERR_ARG.
+ * The calls allocate nothing and may be captured into a graph.
+ */
+enum { CONV2D_ACT_NONE = 0, CONV2D_ACT_RELU = 1, CONV2D_ACT_SILU = 2 };
+
+/* 0 on bad arguments */
+size_t conv2d_group_norm_workspace_bytes(int N, int C, int H, int W, int G, int backward);
+int conv2d_group_norm_nhwc(const void* x, const float* gamma, const float* beta, void* y,
+                           float* mean, float* rstd, void* workspace, size_t workspace_bytes,
+                           int N, int C, int H, int W, int G, int ldx, int ldy, float eps,
+                           int dtype, int act, hipStream_t stream);
+int conv2d_group_norm_quant_nhwc(const void* x, const float* gamma, const float* beta, void* q, float* q_scale,
+                                 float* mean, float* rstd, void* workspace, size_t workspace_bytes,
+                                 int N, int C, int H, int W, int G, int ldx, int ldq, float eps,
+                                 int dtype, int act, hipStream_t stream);
+int conv2d_group_norm_bwd_nhwc(const void* dy, const void* x, const float* gamma, const float* beta,
+                               const float* mean, const float* rstd, void* dx, float* dgamma, float* dbeta,
+                               void* workspace, size_t workspace_bytes,
+                               int N, int C, int H, int W, int G, int lddy, int ldx, int lddx,
+                               int dtype, int act, hipStream_t stream);
+
+/*
+ * Products of 8-bit integers with a scale for every row (a token, or a pixel
+ * of a 1x1 convolution) and every output channel.
+ *
+ * conv2d_quantize_rows -- x [M][K] fp32 or bf16 (ldx elements apart) to
+ *   q int8 [M][K] (ldq apart) and scale fp32 [M]:
+ *     a = max(max_k |x|, 2^-100),  q = round(x * (127 / a)) (to nearest even),
+ *     scale = a / 127
+ *   A row that holds a NaN or an infinity gets scale NaN and q = 0, so every
+ *   product with it is NaN.  Also the way to quantise weights, whose rows are
+ *   output channels.
+ * conv2d_int8_matmul --
+ *     y[m][n] = epi( (sum_k q[m][k] * w[n][k]) * (q_scale[m] * w_scale[n]) )
+ *   q int8 [M][K] (ldq apart), w int8 [N][K] (ldw apart), q_scale fp32 [M],
+ *   w_scale fp32 [N], bias fp32 [N] (required iff CONV2D_EPI_BIAS), y fp32 or
+ *   bf16 (dtype) [M][N] (ldy apart).  The sums are exact (32-bit integers;
+ *   K <= 131071), the rest is fp32, rounded once.  ReLU keeps a NaN.
+ *   Any K, stride and alignment works; K, ldq and ldw as multiples of 16 with
+ *   16-byte aligned pointers run without repacking in registers.  ldq and ldw
+ *   up to 2^22.
+ * workspace as for the group norm, conv2d_int8_matmul_workspace_bytes(M, K, N)
+ * bytes (0: none is needed and workspace may be NULL).  Neither call allocates
+ * and both may be captured into a graph.
+ */
+int conv2d_quantize_rows(const void* x, void* q, float* scale, int M, int K, int ldx, int ldq,
+                         int dtype, hipStream_t stream);
+size_t conv2d_int8_matmul_workspace_bytes(int M, int K, int N);
+int conv2d_int8_matmul(const void* q, const float* q_scale, const void* w, const float* w_scale,
+                       const float* bias, void* y, void* workspace, size_t workspace_bytes,
+                       int M, int K, int N, int ldq, int ldw, int ldy,
+                       int dtype, int epilogue, hipStream_t stream);
+
+/*
  * Packed weight layout (the reduction order the NHWC kernels walk: tap
  * (kh, kw) outer, input channel inner; the row/column order of W_matrix,
  * lincklin.cn section 7, with K ordered to match channels-last input):

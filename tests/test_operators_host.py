@@ -1,0 +1,141 @@
+"""Refusals of the group-norm and int8 entries (no GPU: an invalid call
+returns its code before anything is enqueued), their workspace sizes, and the
+plain fp64 definitions against finite differences."""
+import numpy as np
+import pytest
+
+from helpers import ensure_built
+from oracle import operators as ref
+
+ensure_built()
+import cnn_convolution_conv2d_amd as c2  # noqa: E402
+
+P = 0x1000   # a non-NULL, aligned address; nothing is dereferenced by validation
+BIG = 1 << 40
+
+
+def _norm(entry, **over):
+    a = dict(N=2, C=32, H=5, W=7, G=4, ldx=32, ldy=32, lddy=32, eps=1e-5, dtype=c2.BF16, act=c2.ACT_SILU, x=P, y=P,
+             dy=P, gamma=P, beta=P, mean=P, rstd=P, q_scale=P, dgamma=P, dbeta=P, ws=P, bytes=BIG)
+    a.update(over)
+    size = (a["N"], a["C"], a["H"], a["W"], a["G"])
+    if entry == "bwd":
+        return c2.lib.conv2d_group_norm_bwd_nhwc(a["dy"], a["x"], a["gamma"], a["beta"], a["mean"], a["rstd"], a["y"],
+                                                 a["dgamma"], a["dbeta"], a["ws"], a["bytes"], *size, a["lddy"],
+                                                 a["ldx"], a["ldy"], a["dtype"], a["act"], None)
+    if entry == "quant":
+        return c2.lib.conv2d_group_norm_quant_nhwc(a["x"], a["gamma"], a["beta"], a["y"], a["q_scale"], a["mean"],
+                                                   a["rstd"], a["ws"], a["bytes"], *size, a["ldx"], a["ldy"], a["eps"],
+                                                   a["dtype"], a["act"], None)
+    return c2.lib.conv2d_group_norm_nhwc(a["x"], a["gamma"], a["beta"], a["y"], a["mean"], a["rstd"], a["ws"],
+                                         a["bytes"], *size, a["ldx"], a["ldy"], a["eps"], a["dtype"], a["act"], None)
+
+
+BAD_NORM = [
+    ({"N": 0}, c2.ERR_ARG), ({"C": 0}, c2.ERR_ARG), ({"H": -1}, c2.ERR_ARG), ({"W": 0}, c2.ERR_ARG),
+    ({"G": 0}, c2.ERR_ARG), ({"G": 5}, c2.ERR_GROUPS), ({"ldx": 31}, c2.ERR_ARG), ({"ldy": 31}, c2.ERR_ARG),
+    ({"dtype": 2}, c2.ERR_DTYPE), ({"act": 3}, c2.ERR_EPILOGUE), ({"act": -1}, c2.ERR_EPILOGUE),
+    ({"x": None}, c2.ERR_NULL), ({"y": None}, c2.ERR_NULL), ({"ws": None}, c2.ERR_NULL), ({"bytes": 0}, c2.ERR_ARG),
+    ({"ws": P + 8}, c2.ERR_ALIGN), ({"x": P + 1}, c2.ERR_ALIGN),
+    ({"C": 4100, "G": 4, "ldx": 4100, "ldy": 4100, "lddy": 4100}, c2.ERR_UNSUPPORTED),
+    ({"N": 1 << 16, "H": 1 << 10, "W": 1 << 10}, c2.ERR_UNSUPPORTED),
+    ({"H": 2 ** 31 - 1, "W": 2 ** 31 - 1}, c2.ERR_UNSUPPORTED),
+]
+
+
+@pytest.mark.parametrize("over,code", BAD_NORM, ids=str)
+@pytest.mark.parametrize("entry", ["fwd", "quant", "bwd"])
+def test_norm_refusals(entry, over, code):
+    assert _norm(entry, **over) == code
+    assert c2.last_error()
+
+
+@pytest.mark.parametrize("entry,over,code", [
+    ("fwd", {"eps": -1e-5}, c2.ERR_ARG), ("fwd", {"eps": float("nan")}, c2.ERR_ARG),
+    ("fwd", {"eps": float("inf")}, c2.ERR_ARG), ("fwd", {"ldy": 40}, c2.ERR_ARG),   # x == y needs one stride
+    ("fwd", {"y": P + 1}, c2.ERR_ALIGN), ("quant", {"q_scale": None}, c2.ERR_NULL),
+    ("bwd", {"dy": None}, c2.ERR_NULL), ("bwd", {"mean": None}, c2.ERR_NULL), ("bwd", {"rstd": None}, c2.ERR_NULL),
+    ("bwd", {"lddy": 31}, c2.ERR_ARG), ("bwd", {"dy": P + 1}, c2.ERR_ALIGN), ("bwd", {"ldy": 40}, c2.ERR_ARG),
+], ids=str)
+def test_norm_refusals_of_one_entry(entry, over, code):
+    assert _norm(entry, **over) == code
+
+
+def _product(**over):
+    a = dict(M=8, K=64, N=32, ldq=64, ldw=64, ldy=32, dtype=c2.BF16, epi=c2.EPI_BIAS, q=P, qs=P, w=P, ws=P, bias=P,
+             y=P, wk=P, bytes=BIG)
+    a.update(over)
+    return c2.lib.conv2d_int8_matmul(a["q"], a["qs"], a["w"], a["ws"], a["bias"], a["y"], a["wk"], a["bytes"], a["M"],
+                                     a["K"], a["N"], a["ldq"], a["ldw"], a["ldy"], a["dtype"], a["epi"], None)
+
+
+@pytest.mark.parametrize("over,code", [
+    ({"M": 0}, c2.ERR_ARG), ({"K": 0}, c2.ERR_ARG), ({"N": -3}, c2.ERR_ARG), ({"ldq": 63}, c2.ERR_ARG),
+    ({"ldw": 63}, c2.ERR_ARG), ({"ldy": 31}, c2.ERR_ARG), ({"dtype": 9}, c2.ERR_DTYPE), ({"epi": 4}, c2.ERR_EPILOGUE),
+    ({"q": None}, c2.ERR_NULL), ({"qs": None}, c2.ERR_NULL), ({"w": None}, c2.ERR_NULL), ({"ws": None}, c2.ERR_NULL),
+    ({"y": None}, c2.ERR_NULL), ({"bias": None}, c2.ERR_NULL), ({"y": P + 1}, c2.ERR_ALIGN),
+    ({"K": 131072, "ldq": 131072, "ldw": 131072}, c2.ERR_UNSUPPORTED),
+    ({"ldq": (1 << 22) + 1}, c2.ERR_UNSUPPORTED), ({"ldw": (1 << 22) + 1}, c2.ERR_UNSUPPORTED),
+    ({"M": 100, "K": 8192, "N": 64, "ldq": 8192, "ldw": 8192, "ldy": 64, "wk": None}, c2.ERR_NULL),
+    ({"M": 100, "K": 8192, "N": 64, "ldq": 8192, "ldw": 8192, "ldy": 64, "bytes": 16}, c2.ERR_ARG),
+    ({"M": 100, "K": 8192, "N": 64, "ldq": 8192, "ldw": 8192, "ldy": 64, "wk": P + 4}, c2.ERR_ALIGN),
+], ids=str)
+def test_product_refusals(over, code):
+    assert _product(**over) == code
+    assert c2.last_error()
+
+
+@pytest.mark.parametrize("over,code", [
+    ({"M": 0}, c2.ERR_ARG), ({"K": 0}, c2.ERR_ARG), ({"ldx": 63}, c2.ERR_ARG), ({"ldq": 63}, c2.ERR_ARG),
+    ({"dtype": 5}, c2.ERR_DTYPE), ({"x": None}, c2.ERR_NULL), ({"q": None}, c2.ERR_NULL), ({"s": None}, c2.ERR_NULL),
+    ({"x": P + 1}, c2.ERR_ALIGN),
+], ids=str)
+def test_quantize_refusals(over, code):
+    a = dict(x=P, q=P, s=P, M=8, K=64, ldx=64, ldq=64, dtype=c2.BF16)
+    a.update(over)
+    assert c2.lib.conv2d_quantize_rows(a["x"], a["q"], a["s"], a["M"], a["K"], a["ldx"], a["ldq"], a["dtype"],
+                                       None) == code
+
+
+def test_binding_raises_with_the_code():
+    with pytest.raises(c2.Conv2dError) as e:
+        c2.conv2d_quantize_rows(P, P, None, 1, 1, 1, 1, c2.BF16, stream=0)
+    assert e.value.code == c2.ERR_NULL
+
+
+def test_workspace_sizes():
+    assert c2.conv2d_group_norm_workspace_bytes(2, 32, 5, 7, 5) == 0     # C % G
+    assert c2.conv2d_group_norm_workspace_bytes(0, 32, 5, 7, 4) == 0
+    assert c2.conv2d_int8_matmul_workspace_bytes(0, 1, 1) == 0
+    assert c2.conv2d_int8_matmul_workspace_bytes(8192, 8192, 8192) == 0  # enough tiles without splitting k
+    for size in [(1, 1, 1, 1, 1), (64, 256, 56, 56, 32), (1, 4096, 300, 300, 4096), (3, 999, 17, 9, 27)]:
+        fwd = c2.conv2d_group_norm_workspace_bytes(*size)
+        bwd = c2.conv2d_group_norm_workspace_bytes(*size, backward=True)
+        assert 0 < fwd <= bwd and fwd % 16 == 0 and bwd % 16 == 0
+
+
+# ------------------------------------------------------------------ the definitions
+
+def test_definition_gradients_match_differences():
+    rng = np.random.default_rng(0)
+    N, P_, C, G, h = 2, 6, 12, 3, 1e-6
+    x, dy = rng.standard_normal((N, P_, C)), rng.standard_normal((N, P_, C))
+    gamma, beta = 1 + 0.2 * rng.standard_normal(C), 0.2 * rng.standard_normal(C)
+    for act in (0, 2):
+        y, mean, rstd = ref.group_norm(x, gamma, beta, G, 1e-5, act)
+        grads = dict(zip("xgb", ref.group_norm_bwd(dy, x, gamma, beta, mean, rstd, act)))
+        f = lambda **k: (ref.group_norm(k.get("x", x), k.get("g", gamma), k.get("b", beta), G, 1e-5, act)[0] * dy).sum()  # noqa: E731
+        for name, at in dict(x=x, g=gamma, b=beta).items():
+            v = rng.standard_normal(at.shape)
+            want = (f(**{name: at + h * v}) - f(**{name: at - h * v})) / (2 * h)
+            # central differences: h^2 of the third derivative, and 2^-52 / h of the values
+            assert abs((grads[name] * v).sum() - want) < 1e-6
+
+
+def test_definition_of_rows_and_products():
+    t, s = ref.quantise_rows(np.array([[1.0, -2.0, 0.5], [0.0, 0.0, 0.0]]))
+    np.testing.assert_allclose(t[0], [63.5, -127.0, 31.75], rtol=1e-15)
+    assert s[0] == 2.0 / 127 and s[1] == 2.0 ** -100 / 127 and (t[1] == 0).all()
+    y, size = ref.int8_matmul([[2, -3]], [0.5], [[4, 5], [1, 1]], [1.0, 2.0], bias=[1.0, 0.5], relu=True)
+    np.testing.assert_array_equal(y, [[0.0, 0.0]])
+    np.testing.assert_array_equal(size, [[4.5, 1.5]])
