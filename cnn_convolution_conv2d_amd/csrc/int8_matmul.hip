@@ -30,7 +30,6 @@ namespace conv2d {
 namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 // Descriptor of rows [r0, rows) of a row-major byte matrix, starting at row
@@ -136,73 +135,72 @@ __device__ __forceinline__ TileAt tile_at(int tm, int tn, int BM, int BN) {
     return t;
 }
 
-// The matrix products of a 32-byte step of k: TI x TJ blocks of 32 channels x
-// 32 rows.
+// The matrix products of a 64-byte step of k: TI x TJ blocks of 16 channels x
+// 16 rows.  The 16x16x64 form, not 32x32x32: on random bytes the matrix unit
+// is held back by power, not by issue, and the small form, which moves half
+// the accumulator bytes per product, sustains 3.8 against 3.3 POP/s (registers
+// only; on zeros 4.7 against 4.9).
 template <int TI, int TJ>
-__device__ __forceinline__ void products(i32x16 (&acc)[TI][TJ], const i32x4 (&w)[TI], const i32x4 (&q)[TJ]) {
+__device__ __forceinline__ void products(i32x4 (&acc)[TI][TJ], const i32x4 (&w)[TI], const i32x4 (&q)[TJ]) {
 #pragma unroll
     for (int j = 0; j < TJ; ++j)
 #pragma unroll
-        for (int i = 0; i < TI; ++i) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(w[i], q[j], acc[i][j], 0, 0, 0);
+        for (int i = 0; i < TI; ++i) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[i], q[j], acc[i][j], 0, 0, 0);
 }
 
-// Results of a wave's TI*32 channels x TJ*32 rows: block by block of 32 rows
-// through the wave's own piece of LDS (32 x TI*32 elements), so that whole
-// rows are written.  In the 32x32 result lane l holds, in register 4p + r,
-// channel 8p + 4 (l >> 5) + r of row l & 31.  sw, sb: the tile's channel
-// scales and biases in LDS, from the wave's first channel.  OUT int: the sums
-// themselves.
+// Results of a wave's TI*16 channels x TJ*16 rows: block by block of 16 rows
+// through the wave's own piece of LDS (16 x TI*16 elements), so that whole
+// rows are written.  In the 16x16 result lane l holds, in register r, channel
+// 4 (l >> 4) + r of row l & 15.  sw, sb: the tile's channel scales and biases
+// in LDS, from the wave's first channel.  OUT int: the sums themselves.
 template <int TI, int TJ, typename OUT>
-__device__ __forceinline__ void write_results(const Int8Args& a, i32x16 (&acc)[TI][TJ], char* lds, const float* sw,
+__device__ __forceinline__ void write_results(const Int8Args& a, i32x4 (&acc)[TI][TJ], char* lds, const float* sw,
                                               const float* sb, int m0, int n0, OUT* y, long long ldy, bool vec) {
     constexpr bool kSums = std::is_same_v<OUT, int>;
-    constexpr int ROW = TI * 32 * sizeof(OUT), PIECES = ROW / 16, MASK = (PIECES < 16 ? PIECES : 16) - 1;
-    const int lane = threadIdx.x & 63, r32 = lane & 31, half = lane >> 5;
+    constexpr int COLS = TI * 16, ROW = COLS * (int)sizeof(OUT), PIECES = ROW / 16;
+    constexpr int MASK = (PIECES < 16 ? PIECES : 16) - 1;
+    const int lane = threadIdx.x & 63, r16 = lane & 15;
+    char* const row = lds + r16 * ROW;
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
         float qs = 0.0f;
-        if constexpr (!kSums) qs = m0 + j * 32 + r32 < a.M ? a.q_scale[m0 + j * 32 + r32] : 0.0f;
-        char* row = lds + r32 * ROW;
+        if constexpr (!kSums) qs = m0 + j * 16 + r16 < a.M ? a.q_scale[m0 + j * 16 + r16] : 0.0f;
 #pragma unroll
-        for (int i = 0; i < TI; ++i)
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                const int c = i * 32 + 8 * p + 4 * half;
-                const int at = ((c * (int)sizeof(OUT) / 16) ^ (r32 & MASK)) * 16 + c * (int)sizeof(OUT) % 16;
-                if constexpr (kSums) {
-                    *reinterpret_cast<i32x4*>(row + at) = i32x4{acc[i][j][4 * p], acc[i][j][4 * p + 1],
-                                                                acc[i][j][4 * p + 2], acc[i][j][4 * p + 3]};
-                } else {
-                    const float4 ws = *reinterpret_cast<const float4*>(sw + c);
-                    const float4 bs = *reinterpret_cast<const float4*>(sb + c);
-                    const float v0 = finish(acc[i][j][4 * p], qs * ws.x, bs.x, a.relu);
-                    const float v1 = finish(acc[i][j][4 * p + 1], qs * ws.y, bs.y, a.relu);
-                    const float v2 = finish(acc[i][j][4 * p + 2], qs * ws.z, bs.z, a.relu);
-                    const float v3 = finish(acc[i][j][4 * p + 3], qs * ws.w, bs.w, a.relu);
-                    if constexpr (sizeof(OUT) == 4)
-                        *reinterpret_cast<float4*>(row + at) = make_float4(v0, v1, v2, v3);
-                    else
-                        *reinterpret_cast<uint2*>(row + at) = make_uint2(pack_bf16x2(v0, v1), pack_bf16x2(v2, v3));
-                }
+        for (int i = 0; i < TI; ++i) {
+            const int c = i * 16 + 4 * (lane >> 4), b = c * (int)sizeof(OUT);
+            char* const at = row + ((b / 16) ^ (r16 & MASK)) * 16 + b % 16;
+            if constexpr (kSums) {
+                *reinterpret_cast<i32x4*>(at) = acc[i][j];
+            } else {
+                const float4 ws = *reinterpret_cast<const float4*>(sw + c);
+                const float4 bs = *reinterpret_cast<const float4*>(sb + c);
+                const float v0 = finish(acc[i][j][0], qs * ws.x, bs.x, a.relu);
+                const float v1 = finish(acc[i][j][1], qs * ws.y, bs.y, a.relu);
+                const float v2 = finish(acc[i][j][2], qs * ws.z, bs.z, a.relu);
+                const float v3 = finish(acc[i][j][3], qs * ws.w, bs.w, a.relu);
+                if constexpr (sizeof(OUT) == 4)
+                    *reinterpret_cast<float4*>(at) = make_float4(v0, v1, v2, v3);
+                else
+                    *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16x2(v0, v1), pack_bf16x2(v2, v3));
             }
+        }
         // the wave's own LDS: its writes are done before its reads
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
         if (vec) {
 #pragma unroll
-            for (int it = 0; it < PIECES / 2; ++it) {
+            for (int it = 0; it < 16 * PIECES / 64; ++it) {
                 const int e = it * 64 + lane, r = e / PIECES, p = e % PIECES;
-                const int m = m0 + j * 32 + r, n = n0 + p * (16 / (int)sizeof(OUT));
+                const int m = m0 + j * 16 + r, n = n0 + p * (16 / (int)sizeof(OUT));
                 if (m < a.M && n < a.N)
                     *reinterpret_cast<uint4*>(y + m * ldy + n) =
                         *reinterpret_cast<const uint4*>(lds + r * ROW + (p ^ (r & MASK)) * 16);
             }
         } else {
-            for (int e = lane; e < 32 * TI * 32; e += 64) {
-                const int r = e / (TI * 32), c = e % (TI * 32);
-                const int b = c * (int)sizeof(OUT);
-                const int m = m0 + j * 32 + r, n = n0 + c;
+            for (int e = lane; e < 16 * COLS; e += 64) {
+                const int r = e / COLS, c = e % COLS, b = c * (int)sizeof(OUT);
+                const int m = m0 + j * 16 + r, n = n0 + c;
                 if (m < a.M && n < a.N)
                     y[m * ldy + n] = *reinterpret_cast<const OUT*>(lds + r * ROW + ((b / 16) ^ (r & MASK)) * 16 + b % 16);
             }
@@ -237,17 +235,18 @@ __device__ __forceinline__ void copy_kb(__amdgpu_buffer_rsrc_t r, char* dst, int
 // there is one barrier per stage.
 template <int BM, int BN, int WM, int WN, typename OUT>
 __global__ __launch_bounds__(WM * WN * 64) void int8_tile_kernel(Int8Args a, int tm, int tn, int stages, bool vec) {
-    constexpr int NW = WM * WN, TI = BN / WN / 32, TJ = BM / WM / 32;
+    constexpr int NW = WM * WN, TI = BN / WN / 16, TJ = BM / WM / 16;
     constexpr int STAGE = (BM + BN) * kStageK;
     constexpr int CW = BN / 8 / NW, CQ = BM / 8 / NW;   // 1 KB copies per wave and stage
     static_assert(CW * 8 * NW == BN && CQ * 8 * NW == BM, "copies split evenly");
-    static_assert(NW * 32 * TI * 32 * 4 <= STAGE, "results fit a stage");
+    static_assert(NW * 16 * TI * 16 * 4 <= STAGE, "results fit a stage");
     __shared__ uint4 lds0[STAGE / 16], lds1[STAGE / 16];
     __shared__ float sw[BN], sb[BN];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const TileAt t = tile_at(tm, tn, BM, BN);
     const int kbase = t.split * stages * kStageK;
     const int nk = min(stages, (a.K - kbase + kStageK - 1) / kStageK);
+    const int kend = min(kbase + nk * kStageK, a.K);
     const auto wr = rows_rsrc(a.w, a.ldw, t.n0, a.N, BN, a.K);
     const auto qr = rows_rsrc(a.q, a.ldq, t.m0, a.M, BM, a.K);
 
@@ -265,24 +264,23 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_tile_kernel(Int8Args a, int
     static_assert(NW % 2 == 0, "a wave's copies share their rows' bit 3");
     const int piece = ((lane & 7) ^ (((wave * 8 + lr) >> 1) & 7)) * 16;
 
-    const int half = lane >> 5, r32 = lane & 31;
     const int wm = wave / WN, wn = wave % WN;
-    int ro[4];  // a lane's slot in a 32-row block, for the 4 steps of a stage
+    int ro[2];  // a lane's slot in a 16-row block, for the 2 steps of a stage
 #pragma unroll
-    for (int j = 0; j < 4; ++j) ro[j] = slot_of(r32, 2 * j + half) * 16;
-    const int wbase = wn * (TI * 32) * kStageK, qbase = BN * kStageK + wm * (TJ * 32) * kStageK;
+    for (int j = 0; j < 2; ++j) ro[j] = slot_of(lane & 15, 4 * j + (lane >> 4)) * 16;
+    const int wbase = wn * (TI * 16) * kStageK, qbase = BN * kStageK + wm * (TJ * 16) * kStageK;
 
-    i32x16 acc[TI][TJ];
+    i32x4 acc[TI][TJ];
 #pragma unroll
     for (int i = 0; i < TI; ++i)
 #pragma unroll
-        for (int j = 0; j < TJ; ++j) acc[i][j] = i32x16{};
+        for (int j = 0; j < TJ; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
     i32x4 fw[2][TI], fq[2][TJ];
 
 #define I8_COPY(DST, S)                                                                                  \
     do {                                                                                                 \
         const int k_ = kbase + (S) * kStageK + piece;                                                    \
-        const bool in_ = k_ < a.K;                                                                       \
+        const bool in_ = k_ < kend;                                                                      \
         char* const w_ = (DST) + wave * 1024;                                                            \
         _Pragma("unroll") for (int c = 0; c < CW; ++c) copy_kb(wr, w_ + c * NW * 1024, in_ ? wo[c] + k_ : kOOB); \
         _Pragma("unroll") for (int c = 0; c < CQ; ++c)                                                   \
@@ -291,27 +289,38 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_tile_kernel(Int8Args a, int
 #define I8_READ(SRC, J, SET)                                                                                  \
     do {                                                                                                      \
         _Pragma("unroll") for (int i = 0; i < TI; ++i) fw[SET][i] =                                           \
-            *reinterpret_cast<const i32x4*>((SRC) + wbase + ro[J] + i * 32 * kStageK);                        \
+            *reinterpret_cast<const i32x4*>((SRC) + wbase + ro[J] + i * 16 * kStageK);                        \
         _Pragma("unroll") for (int j = 0; j < TJ; ++j) fq[SET][j] =                                           \
-            *reinterpret_cast<const i32x4*>((SRC) + qbase + ro[J] + j * 32 * kStageK);                        \
+            *reinterpret_cast<const i32x4*>((SRC) + qbase + ro[J] + j * 16 * kStageK);                        \
+    } while (0)
+// The products of set SET with the reads (and copies) issued before them in
+// the source spread between them: the compiler would otherwise sink the reads
+// below the products to save registers, and the next step would wait for them.
+#define I8_PRODUCTS(SET, COPIES)                                                                \
+    do {                                                                                        \
+        constexpr int PER = TI * TJ / (TI + TJ) > 0 ? TI * TJ / (TI + TJ) : 1;                  \
+        products<TI, TJ>(acc, fw[SET], fq[SET]);                                                \
+        _Pragma("unroll") for (int i = 0; i < TI + TJ; ++i) {                                   \
+            __builtin_amdgcn_sched_group_barrier(0x008, PER, 0);                                \
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                                  \
+            if (COPIES) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);                      \
+        }                                                                                       \
+        __builtin_amdgcn_sched_barrier(0);                                                      \
     } while (0)
 // One stage from CUR, whose step 0 is in set 0.  At the barrier this wave's
 // reads of CUR are complete and its copies of the next stage have landed.
+// Past the last stage the copies write zeros and the read is not used.
 #define I8_STAGE(CUR, NXT, S)                                                                   \
     do {                                                                                        \
         I8_READ(CUR, 1, 1);                                                                     \
-        products<TI, TJ>(acc, fw[0], fq[0]);                                                    \
-        I8_READ(CUR, 2, 0);                                                                     \
-        products<TI, TJ>(acc, fw[1], fq[1]);                                                    \
-        I8_READ(CUR, 3, 1);                                                                     \
-        products<TI, TJ>(acc, fw[0], fq[0]);                                                    \
+        I8_PRODUCTS(0, false);                                                                  \
         __atomic_signal_fence(__ATOMIC_SEQ_CST);                                                \
         __builtin_amdgcn_s_waitcnt(0x0070); /* vmcnt(0) lgkmcnt(0) */                           \
         __builtin_amdgcn_s_barrier();                                                           \
         __atomic_signal_fence(__ATOMIC_SEQ_CST);                                                \
-        if ((S) + 2 < nk) I8_COPY(CUR, (S) + 2);                                                \
-        if ((S) + 1 < nk) I8_READ(NXT, 0, 0);                                                   \
-        products<TI, TJ>(acc, fw[1], fq[1]);                                                    \
+        I8_READ(NXT, 0, 0);                                                                     \
+        I8_COPY(CUR, (S) + 2);                                                                  \
+        I8_PRODUCTS(1, true);                                                                   \
     } while (0)
 
     stage_scales<BN>(a, t.n0, sw, sb);
@@ -320,7 +329,7 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_tile_kernel(Int8Args a, int
         // does not make the reads of one wait for the copies into the other
         auto loop = [&](char* __restrict__ b0, char* __restrict__ b1) __attribute__((always_inline)) {
             I8_COPY(b0, 0);
-            if (nk > 1) I8_COPY(b1, 1);
+            I8_COPY(b1, 1);
             __builtin_amdgcn_s_waitcnt(0x0070);
             __builtin_amdgcn_s_barrier();
             __atomic_signal_fence(__ATOMIC_SEQ_CST);
@@ -334,10 +343,12 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_tile_kernel(Int8Args a, int
     }
 #undef I8_COPY
 #undef I8_READ
+#undef I8_PRODUCTS
 #undef I8_STAGE
+    __builtin_amdgcn_s_waitcnt(0x0070);   // no copy is in flight when the buffers take the results
     __syncthreads();
-    write_results<TI, TJ, OUT>(a, acc, reinterpret_cast<char*>(lds0) + wave * (32 * TI * 32 * (int)sizeof(OUT)),
-                               sw + wn * TI * 32, sb + wn * TI * 32, t.m0 + wm * TJ * 32, t.n0 + wn * TI * 32,
+    write_results<TI, TJ, OUT>(a, acc, reinterpret_cast<char*>(lds0) + wave * (16 * TI * 16 * (int)sizeof(OUT)),
+                               sw + wn * TI * 16, sb + wn * TI * 16, t.m0 + wm * TJ * 16, t.n0 + wn * TI * 16,
                                out_of<OUT>(a, t.split), a.ldy, vec);
 }
 
@@ -371,10 +382,10 @@ __device__ __forceinline__ uint4 shift_words(const Unaligned& u, int off, int le
 // the products of stage s.
 template <int BM, int BN, int WM, int WN, typename OUT>
 __global__ __launch_bounds__(WM * WN * 64) void int8_ragged_kernel(Int8Args a, int tm, int tn, int stages, bool vec) {
-    constexpr int NT = WM * WN * 64, TI = BN / WN / 32, TJ = BM / WM / 32;
+    constexpr int NT = WM * WN * 64, TI = BN / WN / 16, TJ = BM / WM / 16;
     constexpr int STAGE = (BM + BN) * kStageK, PER = (BM + BN) * 8 / NT;
     static_assert(BN * 8 % NT == 0 && BM * 8 % NT == 0, "pieces split evenly");
-    constexpr int OUTB = WM * WN * 32 * TI * 32 * 4;
+    constexpr int OUTB = WM * WN * 16 * TI * 16 * 4;
     __shared__ uint4 lds[(STAGE > OUTB ? STAGE : OUTB) / 16];
     __shared__ float sw[BN], sb[BN];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -396,12 +407,12 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_ragged_kernel(Int8Args a, i
         slot[c] = slot_of(row, e & 7);
     }
     const int piece = (tid & 7) * 16;
-    const int half = lane >> 5, r32 = lane & 31, wm = wave / WN, wn = wave % WN;
-    i32x16 acc[TI][TJ];
+    const int wm = wave / WN, wn = wave % WN;
+    i32x4 acc[TI][TJ];
 #pragma unroll
     for (int i = 0; i < TI; ++i)
 #pragma unroll
-        for (int j = 0; j < TJ; ++j) acc[i][j] = i32x16{};
+        for (int j = 0; j < TJ; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
     stage_scales<BN>(a, t.n0, sw, sb);
     Unaligned v[PER];
     auto fetch = [&](int s) {
@@ -420,21 +431,21 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_ragged_kernel(Int8Args a, i
         if (s + 1 < nk) fetch(s + 1);
         const char* base = reinterpret_cast<const char*>(lds);
 #pragma unroll
-        for (int j4 = 0; j4 < 4; ++j4) {
-            const int ro = slot_of(r32, 2 * j4 + half) * 16;
+        for (int step = 0; step < 2; ++step) {
+            const int ro = slot_of(lane & 15, 4 * step + (lane >> 4)) * 16;
             i32x4 fw[TI], fq[TJ];
 #pragma unroll
             for (int i = 0; i < TI; ++i)
-                fw[i] = *reinterpret_cast<const i32x4*>(base + (wn * TI + i) * 32 * kStageK + ro);
+                fw[i] = *reinterpret_cast<const i32x4*>(base + (wn * TI + i) * 16 * kStageK + ro);
 #pragma unroll
             for (int j = 0; j < TJ; ++j)
-                fq[j] = *reinterpret_cast<const i32x4*>(base + BN * kStageK + (wm * TJ + j) * 32 * kStageK + ro);
+                fq[j] = *reinterpret_cast<const i32x4*>(base + BN * kStageK + (wm * TJ + j) * 16 * kStageK + ro);
             products<TI, TJ>(acc, fw, fq);
         }
     }
     __syncthreads();
-    write_results<TI, TJ, OUT>(a, acc, reinterpret_cast<char*>(lds) + wave * (32 * TI * 32 * (int)sizeof(OUT)),
-                               sw + wn * TI * 32, sb + wn * TI * 32, t.m0 + wm * TJ * 32, t.n0 + wn * TI * 32,
+    write_results<TI, TJ, OUT>(a, acc, reinterpret_cast<char*>(lds) + wave * (16 * TI * 16 * (int)sizeof(OUT)),
+                               sw + wn * TI * 16, sb + wn * TI * 16, t.m0 + wm * TJ * 16, t.n0 + wn * TI * 16,
                                out_of<OUT>(a, t.split), a.ldy, vec);
 }
 
@@ -595,7 +606,7 @@ template <typename OUT> hipError_t tiled(const Int8Args& a, const Int8Plan& p, h
     const bool vec = a.ldy * es % 16 == 0 && a.N * (long long)es % 16 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
     const int blocks = p.tm * p.tn * p.splits;
     switch (p.kernel) {
-    case kTile256: int8_tile_kernel<256, 256, 2, 2, OUT><<<blocks, 256, 0, st>>>(a, p.tm, p.tn, p.stages, vec); break;
+    case kTile256: int8_tile_kernel<256, 256, 2, 4, OUT><<<blocks, 512, 0, st>>>(a, p.tm, p.tn, p.stages, vec); break;
     case kTile128: int8_tile_kernel<128, 128, 2, 2, OUT><<<blocks, 256, 0, st>>>(a, p.tm, p.tn, p.stages, vec); break;
     case kTile64: int8_tile_kernel<64, 64, 2, 2, OUT><<<blocks, 256, 0, st>>>(a, p.tm, p.tn, p.stages, vec); break;
     case kRagged128: int8_ragged_kernel<128, 128, 2, 2, OUT><<<blocks, 256, 0, st>>>(a, p.tm, p.tn, p.stages, vec); break;
