@@ -116,6 +116,31 @@ def _load() -> ctypes.CDLL:
 lib = _load()
 
 
+def _load_binding():
+    """The C extension that calls the operator entries (a few microseconds of
+    GPU time, less than ctypes takes to marshal their arguments)."""
+    import importlib.util
+    path = os.path.join(_HERE, "_binding.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is not built; run `python -m cnn_convolution_conv2d_amd.build`")
+    spec = importlib.util.spec_from_file_location("_binding", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
+def _address(name: str) -> int:
+    return ctypes.cast(getattr(lib, name), ctypes.c_void_p).value
+
+
+_binding = _load_binding()
+_group_norm = _address("conv2d_group_norm_nhwc")
+_group_norm_quant = _address("conv2d_group_norm_quant_nhwc")
+_group_norm_bwd = _address("conv2d_group_norm_bwd_nhwc")
+_quantize_rows = _address("conv2d_quantize_rows")
+_int8_matmul = _address("conv2d_int8_matmul")
+
+
 def _ptr(t) -> int | None:
     if t is None:
         return None
@@ -131,6 +156,12 @@ def _stream(stream) -> int | None:
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _raw_stream() -> int:
+    """torch's current stream on the current device, without building a Stream object."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _check(rc: int, where: str) -> int:
@@ -263,34 +294,40 @@ def conv2d_group_norm_nhwc(x, gamma, beta, y, mean, rstd, workspace, workspace_b
                            dtype, act, stream=None) -> None:
     """Group norm and activation: NHWC x (ldx elements a pixel) -> NHWC y; fp32
     gamma, beta [C] or None; mean, rstd fp32 [N][G] written, or None."""
-    _check(lib.conv2d_group_norm_nhwc(_ptr(x), _ptr(gamma), _ptr(beta), _ptr(y), _ptr(mean), _ptr(rstd),
-                                      _ptr(workspace), workspace_bytes, N, C, H, W, G, ldx, ldy, eps, dtype, act,
-                                      _stream(stream)), "conv2d_group_norm_nhwc")
+    rc = _binding.group_norm(_group_norm, x, gamma, beta, y, mean, rstd, workspace, workspace_bytes, N, C, H, W, G,
+                             ldx, ldy, eps, dtype, act, _raw_stream() if stream is None else _stream(stream))
+    if rc < 0:
+        raise Conv2dError(rc, "conv2d_group_norm_nhwc")
 
 
 def conv2d_group_norm_quant_nhwc(x, gamma, beta, q, q_scale, mean, rstd, workspace, workspace_bytes, N, C, H, W, G,
                                  ldx, ldq, eps, dtype, act, stream=None) -> None:
     """Group norm and activation, quantised for each pixel: int8 q and fp32
     q_scale [N*H*W], the rows of conv2d_int8_matmul."""
-    _check(lib.conv2d_group_norm_quant_nhwc(_ptr(x), _ptr(gamma), _ptr(beta), _ptr(q), _ptr(q_scale), _ptr(mean),
-                                            _ptr(rstd), _ptr(workspace), workspace_bytes, N, C, H, W, G, ldx, ldq,
-                                            eps, dtype, act, _stream(stream)), "conv2d_group_norm_quant_nhwc")
+    rc = _binding.group_norm_quant(_group_norm_quant, x, gamma, beta, q, q_scale, mean, rstd, workspace,
+                                   workspace_bytes, N, C, H, W, G, ldx, ldq, eps, dtype, act,
+                                   _raw_stream() if stream is None else _stream(stream))
+    if rc < 0:
+        raise Conv2dError(rc, "conv2d_group_norm_quant_nhwc")
 
 
 def conv2d_group_norm_bwd_nhwc(dy, x, gamma, beta, mean, rstd, dx, dgamma, dbeta, workspace, workspace_bytes, N, C,
                                H, W, G, lddy, ldx, lddx, dtype, act, stream=None) -> None:
     """Gradients of conv2d_group_norm_nhwc from dy, x and the saved mean and
     rstd; dgamma, dbeta fp32 [C] or None."""
-    _check(lib.conv2d_group_norm_bwd_nhwc(_ptr(dy), _ptr(x), _ptr(gamma), _ptr(beta), _ptr(mean), _ptr(rstd),
-                                          _ptr(dx), _ptr(dgamma), _ptr(dbeta), _ptr(workspace), workspace_bytes, N,
-                                          C, H, W, G, lddy, ldx, lddx, dtype, act, _stream(stream)),
-           "conv2d_group_norm_bwd_nhwc")
+    rc = _binding.group_norm_bwd(_group_norm_bwd, dy, x, gamma, beta, mean, rstd, dx, dgamma, dbeta, workspace,
+                                 workspace_bytes, N, C, H, W, G, lddy, ldx, lddx, dtype, act,
+                                 _raw_stream() if stream is None else _stream(stream))
+    if rc < 0:
+        raise Conv2dError(rc, "conv2d_group_norm_bwd_nhwc")
 
 
 def conv2d_quantize_rows(x, q, scale, M, K, ldx, ldq, dtype, stream=None) -> None:
     """fp32 or bf16 rows -> int8 rows and their fp32 scales [M]."""
-    _check(lib.conv2d_quantize_rows(_ptr(x), _ptr(q), _ptr(scale), M, K, ldx, ldq, dtype, _stream(stream)),
-           "conv2d_quantize_rows")
+    rc = _binding.quantize_rows(_quantize_rows, x, q, scale, M, K, ldx, ldq, dtype,
+                                _raw_stream() if stream is None else _stream(stream))
+    if rc < 0:
+        raise Conv2dError(rc, "conv2d_quantize_rows")
 
 
 def conv2d_int8_matmul_workspace_bytes(M, K, N) -> int:
@@ -301,9 +338,10 @@ def conv2d_int8_matmul(q, q_scale, w, w_scale, bias, y, workspace, workspace_byt
                        epilogue, stream=None) -> None:
     """int8 q [M][K] times int8 w [N][K], scaled by row and channel, fp32 bias
     or None -> y [M][N] of dtype."""
-    _check(lib.conv2d_int8_matmul(_ptr(q), _ptr(q_scale), _ptr(w), _ptr(w_scale), _ptr(bias), _ptr(y),
-                                  _ptr(workspace), workspace_bytes, M, K, N, ldq, ldw, ldy, dtype, epilogue,
-                                  _stream(stream)), "conv2d_int8_matmul")
+    rc = _binding.int8_matmul(_int8_matmul, q, q_scale, w, w_scale, bias, y, workspace, workspace_bytes, M, K, N, ldq,
+                              ldw, ldy, dtype, epilogue, _raw_stream() if stream is None else _stream(stream))
+    if rc < 0:
+        raise Conv2dError(rc, "conv2d_int8_matmul")
 
 
 def conv2d_packed_weight_bytes(Cout, Cin, Kh, Kw, groups, dtype) -> int:

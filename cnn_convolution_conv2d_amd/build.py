@@ -1,10 +1,12 @@
-"""Build libconv2d.so for gfx950 with hipcc (in-tree, no JIT cache).
+"""Build libconv2d.so for gfx950 with hipcc, and the C extension that calls its
+operator entries from Python (in-tree, no JIT cache).
 
     python -m cnn_convolution_conv2d_amd.build
 
 Every ``csrc/*.hip`` file is compiled to an object under ``_build/`` at the
 repository root, in parallel, then linked into
-``cnn_convolution_conv2d_amd/libconv2d.so``.
+``cnn_convolution_conv2d_amd/libconv2d.so``; ``csrc/binding.c`` becomes
+``cnn_convolution_conv2d_amd/_binding.so``.
 """
 from __future__ import annotations
 
@@ -14,11 +16,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libconv2d.so")
+BINDING = os.path.join(PKG, "_binding.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 ARCH = os.environ.get("CONV2D_OFFLOAD_ARCH", "gfx950")
 
@@ -53,6 +57,17 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_binding() -> None:
+    tmp = BINDING + ".tmp"
+    cc = shutil.which("gcc") or shutil.which("cc") or hipcc()
+    cmd = [cc, "-O2", "-Wall", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "binding.c"), "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cc} failed on binding.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = True) -> str:
     """Compile every HIP source and link libconv2d.so; returns its path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -66,6 +81,7 @@ def build(verbose: bool = True) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _build_binding()
     os.replace(tmp, OUT)
     if verbose:
         print(f"built {OUT}")
@@ -73,9 +89,9 @@ def build(verbose: bool = True) -> str:
 
 
 def sources() -> list[str]:
-    """Every file the library is built from: the HIP sources, their headers and
-    the public header."""
-    pats = ("*.hip", "*.hpp", "*.h")
+    """Every file the library and the extension are built from: the HIP sources,
+    their headers, the extension's source and the public header."""
+    pats = ("*.hip", "*.hpp", "*.h", "*.c")
     found = [p for pat in pats for p in glob.glob(os.path.join(CSRC, pat))]
     found += glob.glob(os.path.join(ROOT, "include", "*.h"))
     found.append(os.path.abspath(__file__))
@@ -83,8 +99,9 @@ def sources() -> list[str]:
 
 
 def stale() -> bool:
-    """True when libconv2d.so is missing or older than any file it is built from."""
-    if not os.path.exists(OUT):
+    """True when libconv2d.so is missing or older than any file it is built from,
+    or the extension is missing."""
+    if not os.path.exists(OUT) or not os.path.exists(BINDING):
         return True
     built = os.path.getmtime(OUT)
     return any(os.path.getmtime(p) > built for p in sources())
