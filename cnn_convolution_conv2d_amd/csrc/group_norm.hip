@@ -9,110 +9,131 @@
 //     s1 = sum(gamma * dz) / m,  s2 = sum(gamma * dz * xh) / m   (over the group)
 //     dx = rstd * (gamma * dz - s1 - xh * s2)
 //
-// Two launches each.  The first reads the activations once and leaves partial
-// statistics per image, chunk of pixels and group in the workspace; the
-// second combines an image's partials (a few KB, from L2) in every workgroup,
-// then reads the activations again and writes the result.  No atomics: every
-// sum has a fixed order.
+// Two forms.
+//
+// Streaming, two launches.  The first reads the activations once and leaves
+// partial statistics per image, chunk of pixels and group in the workspace;
+// the second combines an image's partials (a few KB, from L2) in every
+// workgroup, then reads the activations again and writes the result.
+//
+// Resident, one launch: a workgroup loads one (image, group) whole into
+// registers, takes its statistics there and writes the result, so memory is
+// read once.  Forward and backward take it where a group fits and is either
+// small (latency counts) or has whole 64-byte pieces of every pixel.
+//
+// No atomics: every sum has a fixed order.
 //
 // Every thread keeps V consecutive channels (16 bytes where the channel count
 // and the alignment allow) and walks down the pixels of its chunk, R rows of
 // threads side by side, so its per-channel constants stay in registers and a
 // row of threads reads whole consecutive lines.
 //
-// Statistics in fp32: a thread sums x - k and (x - k)^2 with k its first
-// value of the channel, which bounds the cancellation in M2 = ss - s^2/n by
-// the (small) count of its values whatever the mean is; partial means and M2
-// are then merged by the exact identity
+// Statistics in fp32.  Streaming: a thread sums x - k and (x - k)^2 with k its
+// first value of the channel, which bounds the cancellation in
+// M2 = ss - s^2/n by the (small) count of its values whatever the mean is;
+// partial means and M2 are then merged by the exact identity
 //   M2 = sum(M2_i) + sum(n_i * (mean_i - mean)^2).
+// Resident: the deviations from the mean itself, in a second pass over the
+// registers.
+#include "mfma.hpp"
 #include "rowvec.hpp"
 
 namespace conv2d {
 
 namespace {
 
-constexpr int kUnroll = 8;      // vector loads in flight per thread
-constexpr int kTargetBlocks = 2048;
+constexpr int kBatch = 8;       // vector loads in flight per thread (forward)
+constexpr int kBatchBwd = 4;    // of x and of dy each (backward)
+constexpr int kTargetBlocks = 1024;
 constexpr int kMaxChunks = 128; // partials that the second launch combines per image
 
 // Values of row r of R in a chunk of np pixels.
-__device__ __forceinline__ int row_count(int np, int R, int r) { return np / R + (r < np % R ? 1 : 0); }
+__device__ __forceinline__ int row_count(int np, int R, int r) { return r < np ? (np - r - 1) / R + 1 : 0; }
 
-// Lanes that work on one group together: a power of two, at most 64, such
-// that the block covers all G groups in one go where it can.
-__device__ __forceinline__ int lanes_per_group(int G) {
+// Lanes that work on one of `count` things together: a power of two, at most
+// 64, such that the block covers all of them in one go where it can.
+__device__ __forceinline__ int lanes_per(int count) {
     int L = 64;
-    while (L > 1 && (int)blockDim.x / L < G) L >>= 1;
+    while (L > 1 && (int)blockDim.x / L < count) L >>= 1;
     return L;
 }
 
-// Combines an image's chunk partials (mean, M2) into mean and rstd in LDS.
+// B vectors of a thread, `step` elements apart, from value i of cnt on.
+template <typename T, int V, int B> struct Batch {
+    typename Vec<T, V>::raw raw[B];
+    __device__ __forceinline__ void load(const T* p, long long step, int i, int cnt) {
+        if (i + B <= cnt) {
+#pragma unroll
+            for (int u = 0; u < B; ++u) raw[u] = Vec<T, V>::load(p + (i + u) * step);
+        } else {
+#pragma unroll
+            for (int u = 0; u < B; ++u)
+                if (i + u < cnt) raw[u] = Vec<T, V>::load(p + (i + u) * step);
+        }
+    }
+};
+
+// Combines an image's chunk partials (mean, M2) into mean and rstd in LDS, in
+// one pass: with d = mean_i - mean_0, M2 = sum(M2_i) + sum(n d^2) - sum(n d)^2 / N.
+// Chunk 0's own distance from the mean is part of M2, which bounds the
+// cancellation by the number of chunks.
 __device__ __forceinline__ void combine_stats(const float2* part, const NormArgs& a, int n, int chunks, int pix,
                                               float2* stat) {
-    const int cg = a.C / a.G, L = lanes_per_group(a.G), lane = threadIdx.x % L;
+    const int cg = a.C / a.G, L = lanes_per(a.G), lane = threadIdx.x % L;
     const float last = (float)(a.P - (chunks - 1) * pix) * cg, full = (float)pix * cg;
     const float total = (float)a.P * cg;
     for (int g = threadIdx.x / L; g < a.G; g += blockDim.x / L) {
         const float2* p = part + (long long)n * chunks * a.G + g;
-        float s = 0.0f;
-        for (int j = lane; j < chunks; j += L) s += (j == chunks - 1 ? last : full) * p[(long long)j * a.G].x;
-        const float mean = lanes_sum(s, L) / total;
-        float m2 = 0.0f;
+        const float base = p[0].x;
+        float s = 0.0f, ss = 0.0f;
+#pragma unroll 4
         for (int j = lane; j < chunks; j += L) {
             const float2 e = p[(long long)j * a.G];
-            const float d = e.x - mean;
-            m2 += e.y + (j == chunks - 1 ? last : full) * d * d;
+            const float w = j == chunks - 1 ? last : full, d = e.x - base;
+            s = fmaf(w, d, s);
+            ss += fmaf(w * d, d, e.y);
         }
-        m2 = lanes_sum(m2, L);
-        if (lane == 0) stat[g] = make_float2(mean, 1.0f / sqrtf(m2 / total + a.eps));
+        s = lanes_sum(s, L);
+        ss = lanes_sum(ss, L);
+        const float shift = s / total, m2 = ss - s * shift;
+        if (lane == 0)
+            stat[g] = make_float2(base + shift, 1.0f / sqrtf((m2 < 0.0f ? 0.0f : m2) / total + a.eps));  // a NaN stays
     }
     __syncthreads();
 }
 
-// First launch of the forward pass: (mean, M2) of every group of one chunk.
-// One workgroup per image and chunk; LDS: R * C pairs.
+// First launch of the streaming forward pass: (mean, M2) of every group of
+// one chunk.  One workgroup per image and chunk; LDS: R * C pairs.
 template <typename T, int V>
 __global__ __launch_bounds__(512) void gn_stats_kernel(NormArgs a, int TX, int R, int chunks, int pix, float2* part) {
     extern __shared__ float2 lds[];
-    const int n = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
-    const int tx = threadIdx.x % TX, r = threadIdx.x / TX;
+    const int n = blockIdx.x / chunks, chunk = blockIdx.x - n * chunks;
+    const int r = threadIdx.x / TX, tx = threadIdx.x - r * TX;
     const int p0 = chunk * pix, np = min(pix, a.P - p0);
-    const T* x = static_cast<const T*>(a.x) + ((long long)n * a.P + p0) * a.ldx;
     const long long step = (long long)R * a.ldx;
     if (r < R) {
         const int cnt = row_count(np, R, r);
         for (int c = tx * V; c < a.C; c += TX * V) {
-            const T* p = x + r * (long long)a.ldx + c;
+            const T* p = static_cast<const T*>(a.x) + ((long long)n * a.P + p0 + r) * a.ldx + c;
             float k[V], s[V], ss[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) k[j] = s[j] = ss[j] = 0.0f;
-            if (cnt > 0) Vec<T, V>::unpack(Vec<T, V>::load(p), k);
-            int i = 0;
-            for (; i + kUnroll <= cnt; i += kUnroll) {
-                typename Vec<T, V>::raw raw[kUnroll];
+            Batch<T, V, kBatch> b;
+            b.load(p, step, 0, cnt);
+            if (cnt > 0) Vec<T, V>::unpack(b.raw[0], k);
+            for (int i = 0; i < cnt; i += kBatch) {
+                if (i > 0) b.load(p, step, i, cnt);
 #pragma unroll
-                for (int u = 0; u < kUnroll; ++u) raw[u] = Vec<T, V>::load(p + u * step);
-                p += kUnroll * step;
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
+                for (int u = 0; u < kBatch; ++u) {
+                    if (i + u >= cnt) break;
                     float v[V];
-                    Vec<T, V>::unpack(raw[u], v);
+                    Vec<T, V>::unpack(b.raw[u], v);
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
                         const float d = v[j] - k[j];
                         s[j] += d;
                         ss[j] = fmaf(d, d, ss[j]);
                     }
-                }
-            }
-            for (; i < cnt; ++i, p += step) {
-                float v[V];
-                Vec<T, V>::unpack(Vec<T, V>::load(p), v);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float d = v[j] - k[j];
-                    s[j] += d;
-                    ss[j] = fmaf(d, d, ss[j]);
                 }
             }
             const float inv = cnt > 0 ? 1.0f / cnt : 0.0f;
@@ -124,41 +145,76 @@ __global__ __launch_bounds__(512) void gn_stats_kernel(NormArgs a, int TX, int R
         }
     }
     __syncthreads();
-    const int cg = a.C / a.G, L = lanes_per_group(a.G), lane = threadIdx.x % L;
+    // a group's R x C/G entries, by `row` and channel; a row's entries all
+    // count row_count values
+    const int cg = a.C / a.G, L = lanes_per(a.G), lane = threadIdx.x % L;
+    const int few = np / R, more = np - few * R;   // rows below `more` have one value more
     for (int g = threadIdx.x / L; g < a.G; g += blockDim.x / L) {
+        const float2* e = lds + g * cg;
         float s = 0.0f;
-        for (int e = lane; e < R * cg; e += L) {
-            const int er = e / cg;
-            s += row_count(np, R, er) * lds[er * a.C + g * cg + e % cg].x;
+        for (int k = lane, row = lane / cg, c = lane - row * cg; k < R * cg; k += L) {
+            s += (few + (row < more)) * e[row * a.C + c].x;
+            for (c += L; c >= cg; c -= cg) ++row;
         }
         const float mean = lanes_sum(s, L) / ((float)np * cg);
         float m2 = 0.0f;
-        for (int e = lane; e < R * cg; e += L) {
-            const int er = e / cg;
-            const float2 v = lds[er * a.C + g * cg + e % cg];
+        for (int k = lane, row = lane / cg, c = lane - row * cg; k < R * cg; k += L) {
+            const float2 v = e[row * a.C + c];
             const float d = v.x - mean;
-            m2 += v.y + row_count(np, R, er) * d * d;
+            m2 += v.y + (few + (row < more)) * d * d;
+            for (c += L; c >= cg; c -= cg) ++row;
         }
         m2 = lanes_sum(m2, L);
         if (lane == 0) part[(long long)blockIdx.x * a.G + g] = make_float2(mean, m2);
     }
 }
 
-// A thread's constants for its V channels.
-template <int V> struct Affine {
-    float mean[V], rg[V], beta[V];   // z = (x - mean) * (rstd * gamma) + beta
-    __device__ __forceinline__ void load(const NormArgs& a, const float2* stat, int c) {
-        const int cg = a.C / a.G;
+// A thread's constants for its V channels.  bf16 activations carry 8 bits, so
+// z = x * (rstd gamma) + (beta - mean rstd gamma), whose error is 2^-24 of
+// |mean| rstd, cannot lose what their own rounding kept; fp32 ones subtract
+// the mean first.
+template <typename T, int V> struct Affine;
+template <int V> struct Affine<float, V> {
+    float mean[V], rg[V], beta[V];
+    __device__ __forceinline__ void prepare(const NormArgs& a, int c) {
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const float2 s = stat[(c + j) / cg];
-            mean[j] = s.x;
-            rg[j] = s.y * (a.gamma ? a.gamma[c + j] : 1.0f);
+            rg[j] = a.gamma ? a.gamma[c + j] : 1.0f;
             beta[j] = a.beta ? a.beta[c + j] : 0.0f;
         }
     }
+    __device__ __forceinline__ void finish(float m, float r, int j) {
+        mean[j] = m;
+        rg[j] *= r;
+    }
     __device__ __forceinline__ float z(float x, int j) const { return fmaf(x - mean[j], rg[j], beta[j]); }
 };
+template <int V> struct Affine<bf16_t, V> {
+    float rg[V], shift[V];
+    __device__ __forceinline__ void prepare(const NormArgs& a, int c) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            rg[j] = a.gamma ? a.gamma[c + j] : 1.0f;
+            shift[j] = a.beta ? a.beta[c + j] : 0.0f;
+        }
+    }
+    __device__ __forceinline__ void finish(float m, float r, int j) {
+        rg[j] *= r;
+        shift[j] = fmaf(-m, rg[j], shift[j]);
+    }
+    __device__ __forceinline__ float z(float x, int j) const { return fmaf(x, rg[j], shift[j]); }
+};
+// the same from the groups' (mean, rstd)
+template <typename A, int V> __device__ __forceinline__ void finish_affine(A& f, const float2* stat, int c, int cg) {
+    int g = c / cg, left = (g + 1) * cg - c;   // channels of group g from c on
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        if (left == 0) ++g, left = cg;
+        --left;
+        const float2 s = stat[g];
+        f.finish(s.x, s.y, j);
+    }
+}
 
 __device__ __forceinline__ void save_stats(const NormArgs& a, const float2* stat, int n) {
     for (int g = threadIdx.x; g < a.G; g += blockDim.x) {
@@ -167,55 +223,104 @@ __device__ __forceinline__ void save_stats(const NormArgs& a, const float2* stat
     }
 }
 
-// Second launch of the forward pass: one workgroup per image and piece of
-// opix pixels.  LDS: G pairs.
+// Second launch of the streaming forward pass: one workgroup per image and
+// chunk.  The first loads are under way while the partials are combined.
+// LDS: G pairs.
 template <typename T, int V, int ACT>
-__global__ __launch_bounds__(512) void gn_apply_kernel(NormArgs a, int TX, int R, int chunks, int pix, int pieces, int opix,
-                                const float2* part) {
+__global__ __launch_bounds__(512) void gn_apply_kernel(NormArgs a, int TX, int R, int chunks, int pix,
+                                                       const float2* part) {
     extern __shared__ float2 lds[];
-    const int n = blockIdx.x / pieces, piece = blockIdx.x % pieces;
+    const int n = blockIdx.x / chunks, piece = blockIdx.x - n * chunks;
+    const int r = threadIdx.x / TX, tx = threadIdx.x - r * TX;
+    const int p0 = piece * pix, np = min(pix, a.P - p0);
+    const long long first = (long long)n * a.P + p0 + r;
+    const int cnt = r < R ? row_count(np, R, r) : 0, c0 = tx * V;
+    const long long xs = (long long)R * a.ldx, ys = (long long)R * a.ldy;
+    Batch<T, V, kBatch> b;
+    b.load(static_cast<const T*>(a.x) + first * a.ldx + c0, xs, 0, cnt);
+    Affine<T, V> f;
+    f.prepare(a, c0);
     combine_stats(part, a, n, chunks, pix, lds);
     if (piece == 0) save_stats(a, lds, n);
-    const int tx = threadIdx.x % TX, r = threadIdx.x / TX;
-    if (r >= R) return;
-    const int p0 = piece * opix, np = min(opix, a.P - p0);
-    const long long first = (long long)n * a.P + p0 + r;
-    const int cnt = row_count(np, R, r);
-    const long long xs = (long long)R * a.ldx, ys = (long long)R * a.ldy;
-    for (int c = tx * V; c < a.C; c += TX * V) {
-        Affine<V> f;
-        f.load(a, lds, c);
+    for (int c = c0; c < a.C; c += TX * V) {
         const T* p = static_cast<const T*>(a.x) + first * a.ldx + c;
         T* q = static_cast<T*>(a.y) + first * a.ldy + c;
-        for (int i = 0; i < cnt; i += 4) {
-            typename Vec<T, V>::raw raw[4];
+        if (c > c0) f.prepare(a, c);
+        finish_affine<Affine<T, V>, V>(f, lds, c, a.C / a.G);
+        for (int i = 0; i < cnt; i += kBatch) {
+            if (i > 0 || c > c0) b.load(p, xs, i, cnt);
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                if (i + u < cnt) raw[u] = Vec<T, V>::load(p + u * xs);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < kBatch; ++u) {
                 if (i + u >= cnt) break;
                 float v[V];
-                Vec<T, V>::unpack(raw[u], v);
+                Vec<T, V>::unpack(b.raw[u], v);
 #pragma unroll
                 for (int j = 0; j < V; ++j) v[j] = activate<ACT>(f.z(v[j], j));
-                Vec<T, V>::store(q + u * ys, v);
+                Vec<T, V>::store(q + (i + u) * ys, v);
             }
-            p += 4 * xs;
-            q += 4 * ys;
         }
     }
 }
 
 // Second launch of the quantised forward pass.  LPP lanes (a power of two)
-// share a pixel, lane l holds the vectors l, l + LPP, ... of it, J of them at
-// most; with J = 0 a pixel's vectors do not fit the registers and are read
-// twice.  LDS: G pairs, then mean, rstd * gamma and beta of every channel.
-template <typename T, int V, int ACT, int J>
-__global__ __launch_bounds__(256) void gn_quant_kernel(NormArgs a, int LPP, int chunks, int pix, int pieces, int opix,
-                                                       const float2* part) {
+// share a pixel, lane l holds the vectors l, l + LPP, ... of it.  LDS: G pairs.
+// One vector a lane: four pixels at a time, constants in registers.
+template <typename T, int V, int ACT>
+__global__ __launch_bounds__(256) void gn_quant_kernel(NormArgs a, int LPP, int chunks, int pix, const float2* part) {
     extern __shared__ float2 lds[];
-    const int n = blockIdx.x / pieces, piece = blockIdx.x % pieces;
+    constexpr int B = 4;
+    const int n = blockIdx.x / chunks, piece = blockIdx.x - n * chunks;
+    const int sub = threadIdx.x / LPP, l = threadIdx.x - sub * LPP, subs = blockDim.x / LPP;
+    const int p0 = piece * pix, np = min(pix, a.P - p0), c = l * V;
+    const long long first = (long long)n * a.P + p0 + sub;
+    const bool in = c < a.C;
+    const int cnt = row_count(np, subs, sub);
+    const T* p = static_cast<const T*>(a.x) + first * a.ldx + c;
+    int8_t* q = static_cast<int8_t*>(a.y) + first * a.ldy + c;
+    const long long xs = (long long)subs * a.ldx, qs = (long long)subs * a.ldy;
+    Batch<T, V, B> b;
+    b.load(p, xs, 0, in ? cnt : 0);
+    Affine<T, V> f;
+    if (in) f.prepare(a, c);
+    combine_stats(part, a, n, chunks, pix, lds);
+    if (piece == 0) save_stats(a, lds, n);
+    if (in) finish_affine<Affine<T, V>, V>(f, lds, c, a.C / a.G);
+    for (int i = 0; i < cnt; i += B) {
+        if (i > 0) b.load(p, xs, i, in ? cnt : 0);
+        float v[B][V];
+        uint32_t top[B];
+#pragma unroll
+        for (int u = 0; u < B; ++u) {
+            top[u] = 0;
+            if (in && i + u < cnt) {
+                Vec<T, V>::unpack(b.raw[u], v[u]);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    v[u][j] = activate<ACT>(f.z(v[u][j], j));
+                    top[u] = max(top[u], __float_as_uint(v[u][j]) & 0x7fffffffu);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < B; ++u) top[u] = lanes_max(top[u], LPP);
+#pragma unroll
+        for (int u = 0; u < B; ++u) {
+            if (i + u < cnt) {
+                const RowScale s = row_scale(top[u]);
+                if (in) store_quantised<V>(q + (i + u) * qs, v[u], s.inv);
+                if (l == 0) a.q_scale[first + (long long)(i + u) * subs] = s.scale;
+            }
+        }
+    }
+}
+
+// The same for pixels of more than 64 vectors: a wave per pixel, constants
+// from LDS (after the G pairs: mean, rstd gamma and beta of every channel),
+// the pixel read a second time (from the cache) when it is stored.
+template <typename T, int V, int ACT>
+__global__ __launch_bounds__(256) void gn_quant_wide_kernel(NormArgs a, int chunks, int pix, const float2* part) {
+    extern __shared__ float2 lds[];
+    const int n = blockIdx.x / chunks, piece = blockIdx.x - n * chunks;
     combine_stats(part, a, n, chunks, pix, lds);
     if (piece == 0) save_stats(a, lds, n);
     float* mean = reinterpret_cast<float*>(lds + a.G);
@@ -229,154 +334,144 @@ __global__ __launch_bounds__(256) void gn_quant_kernel(NormArgs a, int LPP, int 
         beta[c] = a.beta ? a.beta[c] : 0.0f;
     }
     __syncthreads();
-    const int l = threadIdx.x % LPP, sub = threadIdx.x / LPP, subs = blockDim.x / LPP;
-    const int p0 = piece * opix, np = min(opix, a.P - p0);
-    auto value = [&](float x, int c) { return activate<ACT>(fmaf(x - mean[c], rg[c], beta[c])); };
-    for (int i = sub; i < np; i += subs) {
+    const int l = threadIdx.x & 63;
+    const int p0 = piece * pix, np = min(pix, a.P - p0);
+    auto values = [&](const T* p, int c, float (&v)[V]) {
+        Vec<T, V>::unpack(Vec<T, V>::load(p + c), v);
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = activate<ACT>(fmaf(v[e] - mean[c + e], rg[c + e], beta[c + e]));
+    };
+    for (int i = threadIdx.x >> 6; i < np; i += 4) {
         const long long pixel = (long long)n * a.P + p0 + i;
         const T* p = static_cast<const T*>(a.x) + pixel * a.ldx;
-        int8_t* q = static_cast<int8_t*>(a.y) + pixel * a.ldy;
         uint32_t top = 0;
-        if constexpr (J > 0) {
-            float v[J][V];
+#pragma unroll 4
+        for (int c = l * V; c < a.C; c += 64 * V) {
+            float v[V];
+            values(p, c, v);
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const int c = (l + j * LPP) * V;
-                if (c < a.C) Vec<T, V>::unpack(Vec<T, V>::load(p + c), v[j]);
-            }
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const int c = (l + j * LPP) * V;
-                if (c >= a.C) break;
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    v[j][e] = value(v[j][e], c + e);
-                    top = max(top, __float_as_uint(v[j][e]) & 0x7fffffffu);
-                }
-            }
-            const RowScale s = row_scale(lanes_max(top, LPP));
-#pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const int c = (l + j * LPP) * V;
-                if (c < a.C) store_quantised<V>(q + c, v[j], s.inv);
-            }
-            if (l == 0) a.q_scale[pixel] = s.scale;
-        } else {
-            for (int c = l * V; c < a.C; c += LPP * V) {
-                float v[V];
-                Vec<T, V>::unpack(Vec<T, V>::load(p + c), v);
-#pragma unroll
-                for (int e = 0; e < V; ++e) top = max(top, __float_as_uint(value(v[e], c + e)) & 0x7fffffffu);
-            }
-            const RowScale s = row_scale(lanes_max(top, LPP));
-            for (int c = l * V; c < a.C; c += LPP * V) {
-                float v[V];
-                Vec<T, V>::unpack(Vec<T, V>::load(p + c), v);
-#pragma unroll
-                for (int e = 0; e < V; ++e) v[e] = value(v[e], c + e);
-                store_quantised<V>(q + c, v, s.inv);
-            }
-            if (l == 0) a.q_scale[pixel] = s.scale;
+            for (int e = 0; e < V; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
         }
+        const RowScale s = row_scale(lanes_max(top, 64));
+#pragma unroll 4
+        for (int c = l * V; c < a.C; c += 64 * V) {
+            float v[V];
+            values(p, c, v);
+            store_quantised<V>(static_cast<int8_t*>(a.y) + pixel * a.ldy + c, v, s.inv);
+        }
+        if (l == 0) a.q_scale[pixel] = s.scale;
     }
 }
 
-// dz = dy * act'(z).  ReLU's derivative at 0 is 0.
-template <int ACT> __device__ __forceinline__ float act_grad(float dy, float z) {
-    if (ACT == kActRelu) return z > 0.0f ? dy : z <= 0.0f ? 0.0f : z;  // a NaN stays
-    if (ACT == kActSilu) {
-        const float e = sigmoid(z);
-        return dy * (e * fmaf(z, 1.0f - e, 1.0f));
-    }
-    return dy;
-}
-
-template <int V> struct BwdCoef {
-    float mean[V], rstd[V], gamma[V], beta[V];
+// A thread's constants of the backward pass, and an element's dz and xh.  ONE:
+// its channels are of one group.  ReLU's derivative at 0 is 0; a NaN stays.
+template <int V, bool ONE = false> struct Slope {
+    float mean[ONE ? 1 : V], rstd[ONE ? 1 : V], gamma[V], beta[V];
+    static constexpr __device__ __forceinline__ int at(int j) { return ONE ? 0 : j; }
     __device__ __forceinline__ void load(const NormArgs& a, int n, int c) {
         const int cg = a.C / a.G;
+        int g = c / cg, left = (g + 1) * cg - c;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const long long g = (long long)n * a.G + (c + j) / cg;
-            mean[j] = a.mean[g];
-            rstd[j] = a.rstd[g];
+            if (left == 0) ++g, left = cg;
+            --left;
+            if (!ONE || j == 0) {
+                mean[at(j)] = a.mean[(long long)n * a.G + g];
+                rstd[at(j)] = a.rstd[(long long)n * a.G + g];
+            }
             gamma[j] = a.gamma ? a.gamma[c + j] : 1.0f;
             beta[j] = a.beta ? a.beta[c + j] : 0.0f;
         }
     }
+    __device__ __forceinline__ float xh(float x, int j) const { return (x - mean[at(j)]) * rstd[at(j)]; }
+    template <int ACT> __device__ __forceinline__ float dz(float dy, float xh, int j) const {
+        if (ACT == kActNone) return dy;
+        const float z = fmaf(xh, gamma[j], beta[j]);
+        if (ACT == kActRelu) return z > 0.0f ? dy : z <= 0.0f ? 0.0f : z;
+        const float e = sigmoid(z);
+        return dy * fmaf(z * e, 1.0f - e, e);
+    }
 };
 
-// First launch of the backward pass: for every image and chunk the sums of dz
-// and dz * xh per channel (pc: [block][2][C]) and, weighted with gamma, per
-// group (pg).  LDS: R * C pairs.
+// Sums of a workgroup's channels over its R rows of threads (pairs in LDS:
+// R * cols) into row 0, L lanes to a channel.
+__device__ __forceinline__ void sum_rows(float2* lds, int R, int cols) {
+    const int L = lanes_per(cols), lane = threadIdx.x % L;
+    for (int c = threadIdx.x / L; c < cols; c += blockDim.x / L) {
+        float s = 0.0f, t = 0.0f;
+        for (int k = lane; k < R; k += L) {
+            s += lds[k * cols + c].x;
+            t += lds[k * cols + c].y;
+        }
+        s = lanes_sum(s, L);
+        t = lanes_sum(t, L);
+        if (lane == 0) lds[c] = make_float2(s, t);
+    }
+    __syncthreads();
+}
+
+// First launch of the streaming backward pass: for every image and chunk the
+// sums of dz and dz * xh per channel (pc: [block][2][C]) and, weighted with
+// gamma, per group (pg).  LDS: R * C pairs.
 template <typename T, int V, int ACT>
-__global__ __launch_bounds__(512) void gn_bwd_sums_kernel(NormArgs a, int TX, int R, int chunks, int pix, float* pc, float2* pg) {
+__global__ __launch_bounds__(512) void gn_bwd_sums_kernel(NormArgs a, int TX, int R, int chunks, int pix, float* pc,
+                                                          float2* pg) {
     extern __shared__ float2 lds[];
-    const int n = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
-    const int tx = threadIdx.x % TX, r = threadIdx.x / TX;
+    const int n = blockIdx.x / chunks, chunk = blockIdx.x - n * chunks;
+    const int r = threadIdx.x / TX, tx = threadIdx.x - r * TX;
     const int p0 = chunk * pix, np = min(pix, a.P - p0);
     if (r < R) {
         const int cnt = row_count(np, R, r);
         const long long first = (long long)n * a.P + p0 + r;
         const long long xs = (long long)R * a.ldx, ds = (long long)R * a.lddy;
         for (int c = tx * V; c < a.C; c += TX * V) {
-            BwdCoef<V> f;
-            f.load(a, n, c);
             const T* px = static_cast<const T*>(a.x) + first * a.ldx + c;
             const T* pd = static_cast<const T*>(a.dy) + first * a.lddy + c;
+            Batch<T, V, kBatchBwd> bx, bd;
+            bx.load(px, xs, 0, cnt);
+            bd.load(pd, ds, 0, cnt);
+            Slope<V> f;
+            f.load(a, n, c);
             float A[V], B[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) A[j] = B[j] = 0.0f;
-            for (int i = 0; i < cnt; i += 4) {
-                typename Vec<T, V>::raw rx[4], rd[4];
+            for (int i = 0; i < cnt; i += kBatchBwd) {
+                if (i > 0) {
+                    bx.load(px, xs, i, cnt);
+                    bd.load(pd, ds, i, cnt);
+                }
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    if (i + u < cnt) {
-                        rx[u] = Vec<T, V>::load(px + u * xs);
-                        rd[u] = Vec<T, V>::load(pd + u * ds);
-                    }
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
+                for (int u = 0; u < kBatchBwd; ++u) {
                     if (i + u >= cnt) break;
                     float x[V], d[V];
-                    Vec<T, V>::unpack(rx[u], x);
-                    Vec<T, V>::unpack(rd[u], d);
+                    Vec<T, V>::unpack(bx.raw[u], x);
+                    Vec<T, V>::unpack(bd.raw[u], d);
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
-                        const float xh = (x[j] - f.mean[j]) * f.rstd[j];
-                        const float dz = act_grad<ACT>(d[j], fmaf(xh, f.gamma[j], f.beta[j]));
+                        const float xh = f.xh(x[j], j), dz = f.template dz<ACT>(d[j], xh, j);
                         A[j] += dz;
                         B[j] = fmaf(dz, xh, B[j]);
                     }
                 }
-                px += 4 * xs;
-                pd += 4 * ds;
             }
 #pragma unroll
             for (int j = 0; j < V; ++j) lds[r * a.C + c + j] = make_float2(A[j], B[j]);
         }
     }
     __syncthreads();
-    // rows into row 0: the sums of the channels
+    sum_rows(lds, R, a.C);
     float* out = pc + (long long)blockIdx.x * 2 * a.C;
     for (int c = threadIdx.x; c < a.C; c += blockDim.x) {
-        float2 s = lds[c];
-        for (int k = 1; k < R; ++k) {
-            s.x += lds[k * a.C + c].x;
-            s.y += lds[k * a.C + c].y;
-        }
-        out[c] = s.x;
-        out[a.C + c] = s.y;
-        const float g = a.gamma ? a.gamma[c] : 1.0f;
-        lds[c] = make_float2(s.x * g, s.y * g);
+        out[c] = lds[c].x;
+        out[a.C + c] = lds[c].y;
     }
-    __syncthreads();
-    const int cg = a.C / a.G, L = lanes_per_group(a.G), lane = threadIdx.x % L;
+    const int cg = a.C / a.G, L = lanes_per(a.G), lane = threadIdx.x % L;
     for (int g = threadIdx.x / L; g < a.G; g += blockDim.x / L) {
         float s = 0.0f, t = 0.0f;
-        for (int e = lane; e < cg; e += L) {
-            s += lds[g * cg + e].x;
-            t += lds[g * cg + e].y;
+        for (int c = g * cg + lane; c < (g + 1) * cg; c += L) {
+            const float w = a.gamma ? a.gamma[c] : 1.0f;
+            s = fmaf(w, lds[c].x, s);
+            t = fmaf(w, lds[c].y, t);
         }
         s = lanes_sum(s, L);
         t = lanes_sum(t, L);
@@ -386,47 +481,63 @@ __global__ __launch_bounds__(512) void gn_bwd_sums_kernel(NormArgs a, int TX, in
 
 constexpr int kParamChannels = 32;  // channels of one workgroup that sums dgamma and dbeta
 
-// Second launch of the backward pass.  The first `sums` workgroups add the
-// channels' partials into dgamma and dbeta, the others write dx, one per
-// image and piece of opix pixels.  LDS: max(G, blockDim.x) pairs.
+// Adds `count` partials of kParamChannels channels into dgamma and dbeta.
+// LDS: blockDim.x pairs.
+__device__ __forceinline__ void sum_params(const NormArgs& a, const float* pc, long long count, int block, float2* lds) {
+    const int c = block * kParamChannels + threadIdx.x % kParamChannels;
+    const int row = threadIdx.x / kParamChannels, rows = blockDim.x / kParamChannels;
+    float s = 0.0f, t = 0.0f;
+    if (c < a.C) {
+        const float* p = pc + c;
+#pragma unroll 8
+        for (long long i = row; i < count; i += rows) {
+            s += p[i * 2 * a.C];
+            t += p[i * 2 * a.C + a.C];
+        }
+    }
+    lds[threadIdx.x] = make_float2(s, t);
+    __syncthreads();
+    if (row == 0 && c < a.C) {
+        for (int k = 1; k < rows; ++k) {
+            s += lds[k * kParamChannels + threadIdx.x].x;
+            t += lds[k * kParamChannels + threadIdx.x].y;
+        }
+        if (a.dbeta) a.dbeta[c] = s;
+        if (a.dgamma) a.dgamma[c] = t;
+    }
+}
+
+// Second launch of the streaming backward pass.  The first `sums` workgroups
+// add the channels' partials into dgamma and dbeta, the others write dx, one
+// per image and chunk.  LDS: max(G, blockDim.x) pairs.
 template <typename T, int V, int ACT>
-__global__ __launch_bounds__(512) void gn_bwd_apply_kernel(NormArgs a, int TX, int R, int chunks, int pieces, int opix, int sums,
-                                    const float* pc, const float2* pg) {
+__global__ __launch_bounds__(512) void gn_bwd_apply_kernel(NormArgs a, int TX, int R, int chunks, int pix, int sums,
+                                                           const float* pc, const float2* pg) {
     extern __shared__ float2 lds[];
     if ((int)blockIdx.x < sums) {
-        const int c = blockIdx.x * kParamChannels + threadIdx.x % kParamChannels;
-        const int row = threadIdx.x / kParamChannels, rows = blockDim.x / kParamChannels;
-        const long long count = (long long)a.N * chunks;
-        float s = 0.0f, t = 0.0f;
-        if (c < a.C) {
-            const float* p = pc + c;
-#pragma unroll 4
-            for (long long i = row; i < count; i += rows) {
-                s += p[i * 2 * a.C];
-                t += p[i * 2 * a.C + a.C];
-            }
-        }
-        lds[threadIdx.x] = make_float2(s, t);
-        __syncthreads();
-        if (row == 0 && c < a.C) {
-            for (int k = 1; k < rows; ++k) {
-                s += lds[k * kParamChannels + threadIdx.x].x;
-                t += lds[k * kParamChannels + threadIdx.x].y;
-            }
-            if (a.dbeta) a.dbeta[c] = s;
-            if (a.dgamma) a.dgamma[c] = t;
-        }
+        sum_params(a, pc, (long long)a.N * chunks, blockIdx.x, lds);
         return;
     }
     const int b = blockIdx.x - sums;
-    const int n = b / pieces, piece = b % pieces;
+    const int n = b / chunks, piece = b - n * chunks;
     const int cg = a.C / a.G;
+    const int r = threadIdx.x / TX, tx = threadIdx.x - r * TX;
+    const int p0 = piece * pix, np = min(pix, a.P - p0);
+    const long long first = (long long)n * a.P + p0 + r;
+    const int cnt = r < R ? row_count(np, R, r) : 0, c0 = tx * V;
+    const long long xs = (long long)R * a.ldx, ds = (long long)R * a.lddy, os = (long long)R * a.ldy;
+    Batch<T, V, kBatchBwd> bx, bd;
+    bx.load(static_cast<const T*>(a.x) + first * a.ldx + c0, xs, 0, cnt);
+    bd.load(static_cast<const T*>(a.dy) + first * a.lddy + c0, ds, 0, cnt);
+    Slope<V> f;
+    f.load(a, n, c0);
     {
-        const int L = lanes_per_group(a.G), lane = threadIdx.x % L;
+        const int L = lanes_per(a.G), lane = threadIdx.x % L;
         const float inv = 1.0f / ((float)a.P * cg);
         for (int g = threadIdx.x / L; g < a.G; g += blockDim.x / L) {
             const float2* p = pg + (long long)n * chunks * a.G + g;
             float s = 0.0f, t = 0.0f;
+#pragma unroll 4
             for (int j = lane; j < chunks; j += L) {
                 const float2 e = p[(long long)j * a.G];
                 s += e.x;
@@ -438,74 +549,210 @@ __global__ __launch_bounds__(512) void gn_bwd_apply_kernel(NormArgs a, int TX, i
         }
         __syncthreads();
     }
-    const int tx = threadIdx.x % TX, r = threadIdx.x / TX;
-    if (r >= R) return;
-    const int p0 = piece * opix, np = min(opix, a.P - p0);
-    const long long first = (long long)n * a.P + p0 + r;
-    const int cnt = row_count(np, R, r);
-    const long long xs = (long long)R * a.ldx, ds = (long long)R * a.lddy, os = (long long)R * a.ldy;
-    for (int c = tx * V; c < a.C; c += TX * V) {
-        BwdCoef<V> f;
-        f.load(a, n, c);
-        float s1[V], s2[V];
+    for (int c = c0; c < a.C; c += TX * V) {
+        if (c > c0) f.load(a, n, c);
+        float s1[V], s2[V];   // rstd * s1, rstd * s2
+        int g = c / cg, left = (g + 1) * cg - c;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const float2 s = lds[(c + j) / cg];
-            s1[j] = s.x;
-            s2[j] = s.y;
+            if (left == 0) ++g, left = cg;
+            --left;
+            const float2 s = lds[g];
+            s1[j] = s.x * f.rstd[j];
+            s2[j] = s.y * f.rstd[j];
         }
         const T* px = static_cast<const T*>(a.x) + first * a.ldx + c;
         const T* pd = static_cast<const T*>(a.dy) + first * a.lddy + c;
         T* po = static_cast<T*>(a.y) + first * a.ldy + c;
-        for (int i = 0; i < cnt; i += 2) {
-            typename Vec<T, V>::raw rx[2], rd[2];
+        for (int i = 0; i < cnt; i += kBatchBwd) {
+            if (i > 0 || c > c0) {
+                bx.load(px, xs, i, cnt);
+                bd.load(pd, ds, i, cnt);
+            }
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-                if (i + u < cnt) {
-                    rx[u] = Vec<T, V>::load(px + u * xs);
-                    rd[u] = Vec<T, V>::load(pd + u * ds);
-                }
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < kBatchBwd; ++u) {
                 if (i + u >= cnt) break;
                 float x[V], d[V];
-                Vec<T, V>::unpack(rx[u], x);
-                Vec<T, V>::unpack(rd[u], d);
+                Vec<T, V>::unpack(bx.raw[u], x);
+                Vec<T, V>::unpack(bd.raw[u], d);
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const float xh = (x[j] - f.mean[j]) * f.rstd[j];
-                    const float dz = act_grad<ACT>(d[j], fmaf(xh, f.gamma[j], f.beta[j]));
-                    d[j] = f.rstd[j] * (fmaf(f.gamma[j], dz, -s1[j]) - xh * s2[j]);
+                    const float xh = f.xh(x[j], j), dz = f.template dz<ACT>(d[j], xh, j);
+                    d[j] = fmaf(dz, f.rstd[j] * f.gamma[j], -fmaf(xh, s2[j], s1[j]));
                 }
-                Vec<T, V>::store(po + u * os, d);
+                Vec<T, V>::store(po + (i + u) * os, d);
             }
-            px += 2 * xs;
-            pd += 2 * ds;
-            po += 2 * os;
         }
     }
 }
 
+// ------------------------------------------------------------------ resident
+
+// Sums over the workgroup; every thread gets them.  LDS: 2 * 16 floats, not
+// in use by an earlier call.
+__device__ __forceinline__ float2 block_sum(float s, float t, float* lds) {
+    s = lanes_sum(s, 64);
+    t = lanes_sum(t, 64);
+    const int waves = blockDim.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+        lds[threadIdx.x >> 6] = s;
+        lds[16 + (threadIdx.x >> 6)] = t;
+    }
+    __syncthreads();
+    s = t = 0.0f;
+    for (int w = 0; w < waves; ++w) {
+        s += lds[w];
+        t += lds[16 + w];
+    }
+    return make_float2(s, t);
+}
+
+// Forward: one workgroup per (image, group), NV vectors of it in each thread.
+template <typename T, int V, int ACT, int NV>
+__global__ __launch_bounds__(1024) void gn_resident_kernel(NormArgs a, int TX, int R) {
+    __shared__ float lds[3][32];
+    const int b = xcd_tile_index(), n = b / a.G, g = b - n * a.G, cg = a.C / a.G;
+    const int r = threadIdx.x / TX, tx = threadIdx.x - r * TX, c = g * cg + tx * V;
+    const long long first = (long long)n * a.P + r;
+    const int cnt = r < R ? row_count(a.P, R, r) : 0;
+    Batch<T, V, NV> x;
+    x.load(static_cast<const T*>(a.x) + first * a.ldx + c, (long long)R * a.ldx, 0, cnt);
+    Affine<T, V> f;
+    f.prepare(a, c);
+    float s = 0.0f;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        if (u >= cnt) break;
+        float v[V];
+        Vec<T, V>::unpack(x.raw[u], v);
+#pragma unroll
+        for (int j = 0; j < V; ++j) s += v[j];
+    }
+    const float m = (float)a.P * cg, mean = block_sum(s, 0.0f, lds[0]).x / m;
+    s = 0.0f;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        if (u >= cnt) break;
+        float v[V];
+        Vec<T, V>::unpack(x.raw[u], v);
+#pragma unroll
+        for (int j = 0; j < V; ++j) s = fmaf(v[j] - mean, v[j] - mean, s);
+    }
+    const float rstd = 1.0f / sqrtf(block_sum(s, 0.0f, lds[1]).x / m + a.eps);
+    if (threadIdx.x == 0) {
+        if (a.mean) a.mean[b] = mean;
+        if (a.rstd) a.rstd[b] = rstd;
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) f.finish(mean, rstd, j);
+    T* q = static_cast<T*>(a.y) + first * a.ldy + c;
+    const long long ys = (long long)R * a.ldy;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        if (u >= cnt) break;
+        float v[V];
+        Vec<T, V>::unpack(x.raw[u], v);
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = activate<ACT>(f.z(v[j], j));
+        Vec<T, V>::store(q + u * ys, v);
+    }
+}
+
+// Backward: the same, with the channels' sums of this image to pc
+// ([image][2][C]), or, for a single image, to dgamma and dbeta themselves.
+// LDS: R * C/G pairs.
+template <typename T, int V, int ACT, int NV>
+__global__ __launch_bounds__(1024) void gn_bwd_resident_kernel(NormArgs a, int TX, int R, float* pc) {
+    extern __shared__ float2 rows[];
+    __shared__ float lds[32];
+    const int b = xcd_tile_index(), n = b / a.G, g = b - n * a.G, cg = a.C / a.G;
+    const int r = threadIdx.x / TX, tx = threadIdx.x - r * TX, c = g * cg + tx * V;
+    const long long first = (long long)n * a.P + r;
+    const int cnt = r < R ? row_count(a.P, R, r) : 0;
+    Batch<T, V, NV> bx, bd;
+    bx.load(static_cast<const T*>(a.x) + first * a.ldx + c, (long long)R * a.ldx, 0, cnt);
+    bd.load(static_cast<const T*>(a.dy) + first * a.lddy + c, (long long)R * a.lddy, 0, cnt);
+    Slope<V, true> f;
+    f.load(a, n, c);
+    float A[V], B[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) A[j] = B[j] = 0.0f;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        if (u >= cnt) break;
+        float x[V], d[V];
+        Vec<T, V>::unpack(bx.raw[u], x);
+        Vec<T, V>::unpack(bd.raw[u], d);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float xh = f.xh(x[j], j), dz = f.template dz<ACT>(d[j], xh, j);
+            A[j] += dz;
+            B[j] = fmaf(dz, xh, B[j]);
+        }
+    }
+    float s = 0.0f, t = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        if (r < R) rows[r * cg + tx * V + j] = make_float2(A[j], B[j]);
+        s = fmaf(f.gamma[j], A[j], s);
+        t = fmaf(f.gamma[j], B[j], t);
+    }
+    const float2 sum = block_sum(s, t, lds);   // and the rows are in LDS
+    const float m = (float)a.P * cg, s1 = sum.x / m * f.rstd[0], s2 = sum.y / m * f.rstd[0];
+    T* po = static_cast<T*>(a.y) + first * a.ldy + c;
+    const long long os = (long long)R * a.ldy;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        if (u >= cnt) break;
+        float x[V], d[V];
+        Vec<T, V>::unpack(bx.raw[u], x);
+        Vec<T, V>::unpack(bd.raw[u], d);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float xh = f.xh(x[j], j), dz = f.template dz<ACT>(d[j], xh, j);
+            d[j] = fmaf(dz, f.rstd[0] * f.gamma[j], -fmaf(xh, s2, s1));
+        }
+        Vec<T, V>::store(po + u * os, d);
+    }
+    if (!a.dgamma && !a.dbeta) return;
+    sum_rows(rows, R, cg);
+    for (int k = threadIdx.x; k < cg; k += blockDim.x) {
+        if (a.N == 1) {
+            if (a.dbeta) a.dbeta[g * cg + k] = rows[k].x;
+            if (a.dgamma) a.dgamma[g * cg + k] = rows[k].y;
+        } else {
+            pc[(long long)n * 2 * a.C + g * cg + k] = rows[k].x;
+            pc[(long long)n * 2 * a.C + a.C + g * cg + k] = rows[k].y;
+        }
+    }
+}
+
+__global__ __launch_bounds__(256) void gn_params_kernel(NormArgs a, const float* pc) {
+    __shared__ float2 lds[256];
+    sum_params(a, pc, a.N, blockIdx.x, lds);
+}
+
 // ------------------------------------------------------------------ host
 
-// Elements of one vector access: the most that divides the channel count and
-// every row stride, up to 16 bytes, with every pointer aligned to it.
-int vector_width(const NormArgs& a, int elem, int out_elem) {
+// Elements of one vector access: the most that divides `unit` (the channel
+// count, or a group's) and every row stride, up to 16 bytes, with every
+// pointer aligned to it.
+int vector_width(const NormArgs& a, int unit, int elem, int out_elem) {
     int v = 16 / elem;
     auto ok = [&](const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; };
-    while (v > 1 && !(a.C % v == 0 && a.ldx % v == 0 && a.ldy % v == 0 && (!a.dy || a.lddy % v == 0) &&
+    while (v > 1 && !(unit % v == 0 && a.ldx % v == 0 && a.ldy % v == 0 && (!a.dy || a.lddy % v == 0) &&
                       ok(a.x, v * elem) && ok(a.y, v * out_elem) && ok(a.dy, v * elem)))
         v >>= 1;
     return v;
 }
 
 struct Plan {
-    int TX, R, block, chunks, pix, pieces, opix;
+    int TX, R, block, chunks, pix;
 };
 
 // Threads: TX across the channel vectors, R rows of them, the block size of
 // 256 to 512 that leaves the fewest idle.  Chunks: about kTargetBlocks
-// workgroups in all, at most kMaxChunks per image, at least 4 pixels a thread.
+// workgroups in all, at most kMaxChunks per image, of whole batches of loads.
 Plan make_plan(int N, int P, int C, int V) {
     Plan p;
     const int cv = C / V;
@@ -517,19 +764,52 @@ Plan make_plan(int N, int P, int C, int V) {
         if (used > best) best = used, p.block = b;
     }
     p.R = p.block / p.TX;
-    auto split = [&](int target, int most, int least, int* count, int* size) {
-        long long k = (target + (long long)N - 1) / N;
-        const long long cap = (P + (long long)p.R * least - 1) / ((long long)p.R * least);
-        k = k < cap ? k : cap;
-        k = k < most ? k : most;
-        k = k < 1 ? 1 : k;
-        const long long each = (P + k - 1) / k;
-        *size = (int)((each + p.R - 1) / p.R * p.R);
-        *count = (int)((P + (long long)*size - 1) / *size);
-    };
-    split(kTargetBlocks, kMaxChunks, 4, &p.chunks, &p.pix);
-    split(kTargetBlocks, 1 << 20, 4, &p.pieces, &p.opix);
+    long long k = (kTargetBlocks + (long long)N - 1) / N;
+    k = k < kMaxChunks ? k : kMaxChunks;
+    // a chunk has at least one vector per thread; more than a batch, and it is
+    // rounded to whole batches
+    const long long batch = (long long)p.R * kBatch;
+    long long each = (P + k - 1) / k;
+    each = each > batch ? (each + batch - 1) / batch * batch : (each + p.R - 1) / p.R * p.R;
+    p.pix = (int)(each < 0x7fffffff ? each : 0x7fffffff);
+    p.chunks = (int)((P + (long long)p.pix - 1) / p.pix);
     return p;
+}
+
+// The resident form: threads and the vectors of each, or nv = 0 where the
+// group does not fit (most: the largest nv) or is not worth it.  Each
+// workgroup reads C/G channels of every pixel: below 64 bytes that splits the
+// memory's lines over several workgroups, which costs more than the second
+// read once the tensor is large.
+struct Resident {
+    int TX, R, block, nv;
+};
+
+constexpr long long kResidentBytes = 8 << 20;
+
+Resident make_resident(const NormArgs& a, int V, int elem, int most) {
+    Resident p = {0, 0, 0, 0};
+    const int cg = a.C / a.G;
+    p.TX = cg / V;
+    const long long bytes = (long long)a.N * a.P * a.C * elem;
+    if (p.TX > 256 || (bytes > kResidentBytes && cg * elem < 64) || (long long)a.N * a.G >= 0x7fffffffLL) return p;
+    for (p.block = 256; p.block <= 1024; p.block *= 2) {
+        p.R = p.block / p.TX;
+        const long long nv = (a.P + (long long)p.R - 1) / p.R;
+        const int limit = p.block == 1024 ? most : 4;
+        if (nv <= limit) {
+            p.nv = nv <= 2 ? 2 : nv <= 4 ? 4 : most <= 6 || nv <= 8 ? (most <= 6 ? 6 : 8) : 16;
+            return p;
+        }
+    }
+    return p;
+}
+
+template <typename T, int V, int ACT> hipError_t forward_resident(const NormArgs& a, const Resident& p, hipStream_t st) {
+    auto k = p.nv == 2 ? gn_resident_kernel<T, V, ACT, 2> : p.nv == 4 ? gn_resident_kernel<T, V, ACT, 4>
+             : p.nv == 8 ? gn_resident_kernel<T, V, ACT, 8> : gn_resident_kernel<T, V, ACT, 16>;
+    k<<<a.N * a.G, p.block, 0, st>>>(a, p.TX, p.R);
+    return hipGetLastError();
 }
 
 template <typename T, int V> hipError_t forward(const NormArgs& a, int act, void* ws, hipStream_t st) {
@@ -538,20 +818,25 @@ template <typename T, int V> hipError_t forward(const NormArgs& a, int act, void
     gn_stats_kernel<T, V><<<a.N * p.chunks, p.block, (size_t)p.R * a.C * 8, st>>>(a, p.TX, p.R, p.chunks, p.pix, part);
     auto k = act == kActSilu ? gn_apply_kernel<T, V, kActSilu>
              : act == kActRelu ? gn_apply_kernel<T, V, kActRelu> : gn_apply_kernel<T, V, kActNone>;
-    k<<<a.N * p.pieces, p.block, (size_t)a.G * 8, st>>>(a, p.TX, p.R, p.chunks, p.pix, p.pieces, p.opix, part);
+    k<<<a.N * p.chunks, p.block, (size_t)a.G * 8, st>>>(a, p.TX, p.R, p.chunks, p.pix, part);
     return hipGetLastError();
 }
 
 template <typename T, int V, int ACT> hipError_t quantised_apply(const NormArgs& a, const Plan& p, const float2* part,
                                                                  hipStream_t st) {
     const int cv = a.C / V;
+    if (cv > 64) {
+        const size_t lds = (size_t)a.G * 8 + (size_t)a.C * 12;
+        int dev = 0;
+        hipError_t e = hipGetDevice(&dev);
+        if (e == hipSuccess && lds > 65536) e = ensure_dynamic_lds<gn_quant_wide_kernel<T, V, ACT>>((int)lds, dev);
+        if (e != hipSuccess) return e;
+        gn_quant_wide_kernel<T, V, ACT><<<a.N * p.chunks, 256, lds, st>>>(a, p.chunks, p.pix, part);
+        return hipGetLastError();
+    }
     int lpp = 1;
-    while (lpp < cv && lpp < 64) lpp <<= 1;
-    const int j = (cv + lpp - 1) / lpp;
-    auto k = j == 1 ? gn_quant_kernel<T, V, ACT, 1> : j == 2 ? gn_quant_kernel<T, V, ACT, 2>
-             : j <= 4 ? gn_quant_kernel<T, V, ACT, 4> : gn_quant_kernel<T, V, ACT, 0>;
-    const size_t lds = (size_t)a.G * 8 + (size_t)a.C * 12;
-    k<<<a.N * p.pieces, 256, lds, st>>>(a, lpp, p.chunks, p.pix, p.pieces, p.opix, part);
+    while (lpp < cv) lpp <<= 1;
+    gn_quant_kernel<T, V, ACT><<<a.N * p.chunks, 256, (size_t)a.G * 8, st>>>(a, lpp, p.chunks, p.pix, part);
     return hipGetLastError();
 }
 
@@ -564,6 +849,29 @@ template <typename T, int V> hipError_t quantised(const NormArgs& a, int act, vo
                              : quantised_apply<T, V, kActNone>(a, p, part, st);
 }
 
+template <typename T, int V, int ACT> hipError_t backward_resident(const NormArgs& a, const Resident& p, float* pc,
+                                                                   hipStream_t st) {
+    const size_t lds = (size_t)p.R * (a.C / a.G) * 8;
+    auto run = [&](auto kernel_of) {
+        constexpr auto kernel = kernel_of();
+        hipError_t e = hipSuccess;
+        if (lds > 60000) {   // 64 KB with the kernel's own few bytes
+            int dev = 0;
+            e = hipGetDevice(&dev);
+            if (e == hipSuccess) e = ensure_dynamic_lds<kernel>((int)lds, dev);
+        }
+        if (e == hipSuccess) kernel<<<a.N * a.G, p.block, lds, st>>>(a, p.TX, p.R, pc);
+        return e;
+    };
+    const hipError_t e = p.nv == 2 ? run([] { return gn_bwd_resident_kernel<T, V, ACT, 2>; })
+                         : p.nv == 4 ? run([] { return gn_bwd_resident_kernel<T, V, ACT, 4>; })
+                                     : run([] { return gn_bwd_resident_kernel<T, V, ACT, 6>; });
+    if (e != hipSuccess) return e;
+    if (a.N > 1 && (a.dgamma || a.dbeta))
+        gn_params_kernel<<<(a.C + kParamChannels - 1) / kParamChannels, 256, 0, st>>>(a, pc);
+    return hipGetLastError();
+}
+
 template <typename T, int V, int ACT> hipError_t backward_act(const NormArgs& a, void* ws, hipStream_t st) {
     const Plan p = make_plan(a.N, a.P, a.C, V);
     const long long blocks = (long long)a.N * p.chunks;
@@ -573,8 +881,7 @@ template <typename T, int V, int ACT> hipError_t backward_act(const NormArgs& a,
                                                                                       pc, pg);
     const int sums = a.dgamma || a.dbeta ? (a.C + kParamChannels - 1) / kParamChannels : 0;
     const size_t lds = (size_t)(a.G > p.block ? a.G : p.block) * 8;
-    gn_bwd_apply_kernel<T, V, ACT><<<sums + a.N * p.pieces, p.block, lds, st>>>(a, p.TX, p.R, p.chunks, p.pieces,
-                                                                               p.opix, sums, pc, pg);
+    gn_bwd_apply_kernel<T, V, ACT><<<sums + (int)blocks, p.block, lds, st>>>(a, p.TX, p.R, p.chunks, p.pix, sums, pc, pg);
     return hipGetLastError();
 }
 
@@ -586,7 +893,8 @@ template <typename T, int V> hipError_t backward(const NormArgs& a, int act, voi
 }  // namespace
 
 // The most partials that any vector width plans, so that one figure holds for
-// every alignment.
+// every alignment (the resident backward pass keeps at most a pair per image
+// and channel, which is less).
 size_t group_norm_workspace(int N, int P, int C, int G, int backward) {
     size_t most = 0;
     for (int v = 1; v <= 8; v <<= 1) {
@@ -602,32 +910,53 @@ size_t group_norm_workspace(int N, int P, int C, int G, int backward) {
 bool group_norm_supports(int N, int P, int C) {
     for (int v = 1; v <= 8; v <<= 1) {
         if (C % v) break;
-        const Plan p = make_plan(N, P, C, v);
-        if ((long long)N * p.chunks + C >= 0x7fffffffLL || (long long)N * p.pieces + C >= 0x7fffffffLL) return false;
+        if ((long long)N * make_plan(N, P, C, v).chunks + C >= 0x7fffffffLL) return false;
     }
     return true;
 }
 
-#define CONV2D_NORM_DISPATCH(FN, OUT_ELEM)                                            \
-    if (a.dtype == 0 /* CONV2D_F32 */) {                                              \
-        const int v = vector_width(a, 4, OUT_ELEM ? OUT_ELEM : 4);                    \
-        return v == 4 ? FN<float, 4>(a, act, ws, st)                                  \
-               : v == 2 ? FN<float, 2>(a, act, ws, st) : FN<float, 1>(a, act, ws, st); \
-    }                                                                                 \
-    const int v = vector_width(a, 2, OUT_ELEM ? OUT_ELEM : 2);                        \
-    return v == 8 ? FN<bf16_t, 8>(a, act, ws, st) : v == 4 ? FN<bf16_t, 4>(a, act, ws, st) \
-           : v == 2 ? FN<bf16_t, 2>(a, act, ws, st) : FN<bf16_t, 1>(a, act, ws, st)
+#define CONV2D_NORM_WIDTH(FN, UNIT, OUT_ELEM, ...)                                                  \
+    if (a.dtype == 0 /* CONV2D_F32 */) {                                                            \
+        const int v = vector_width(a, UNIT, 4, OUT_ELEM ? OUT_ELEM : 4);                            \
+        return v == 4 ? FN<float, 4>(__VA_ARGS__) : v == 2 ? FN<float, 2>(__VA_ARGS__) : FN<float, 1>(__VA_ARGS__); \
+    }                                                                                               \
+    const int v = vector_width(a, UNIT, 2, OUT_ELEM ? OUT_ELEM : 2);                                \
+    return v == 8 ? FN<bf16_t, 8>(__VA_ARGS__) : v == 4 ? FN<bf16_t, 4>(__VA_ARGS__)                \
+           : v == 2 ? FN<bf16_t, 2>(__VA_ARGS__) : FN<bf16_t, 1>(__VA_ARGS__)
+
+template <typename T, int V>
+static hipError_t forward_group(const NormArgs& a, int act, const Resident& p, hipStream_t st) {
+    return act == kActSilu ? forward_resident<T, V, kActSilu>(a, p, st)
+           : act == kActRelu ? forward_resident<T, V, kActRelu>(a, p, st) : forward_resident<T, V, kActNone>(a, p, st);
+}
+template <typename T, int V>
+static hipError_t backward_group(const NormArgs& a, int act, const Resident& p, float* pc,
+                                                              hipStream_t st) {
+    return act == kActSilu ? backward_resident<T, V, kActSilu>(a, p, pc, st)
+           : act == kActRelu ? backward_resident<T, V, kActRelu>(a, p, pc, st)
+                             : backward_resident<T, V, kActNone>(a, p, pc, st);
+}
 
 hipError_t launch_group_norm(const NormArgs& a, int act, void* ws, hipStream_t st) {
-    CONV2D_NORM_DISPATCH(forward, 0);
+    const int elem = a.dtype == 0 ? 4 : 2, cg = a.C / a.G;
+    const Resident p = make_resident(a, vector_width(a, cg, elem, elem), elem, 16);
+    if (p.nv) {
+        CONV2D_NORM_WIDTH(forward_group, cg, 0, a, act, p, st);
+    }
+    CONV2D_NORM_WIDTH(forward, a.C, 0, a, act, ws, st);
 }
 
 hipError_t launch_group_norm_quant(const NormArgs& a, int act, void* ws, hipStream_t st) {
-    CONV2D_NORM_DISPATCH(quantised, 1);
+    CONV2D_NORM_WIDTH(quantised, a.C, 1, a, act, ws, st);
 }
 
 hipError_t launch_group_norm_bwd(const NormArgs& a, int act, void* ws, hipStream_t st) {
-    CONV2D_NORM_DISPATCH(backward, 0);
+    const int elem = a.dtype == 0 ? 4 : 2, cg = a.C / a.G;
+    const Resident p = make_resident(a, vector_width(a, cg, elem, elem), elem, 6);
+    if (p.nv) {
+        CONV2D_NORM_WIDTH(backward_group, cg, 0, a, act, p, static_cast<float*>(ws), st);
+    }
+    CONV2D_NORM_WIDTH(backward, a.C, 0, a, act, ws, st);
 }
 
 }  // namespace conv2d

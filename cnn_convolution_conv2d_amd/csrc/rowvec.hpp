@@ -78,15 +78,46 @@ template <int ACT> __device__ __forceinline__ float activate(float z) {
     return z;
 }
 
-// Sum (or unsigned maximum) over L consecutive lanes, L a power of two <= 64;
-// every lane gets the result.
-__device__ __forceinline__ float lanes_sum(float v, int L) {
-    for (int m = 1; m < L; m <<= 1) v += __shfl_xor(v, m);
+// One step of a reduction over neighbouring lanes: the value of a lane of the
+// other half of a group of 2, 4, 8, 16, 32 or 64 lanes, where both halves
+// already hold one value each (so a mirrored lane serves as well as the
+// exchanged one).  Register moves only; no LDS.
+template <int STEP> __device__ __forceinline__ uint32_t other_half(uint32_t v) {
+    if constexpr (STEP == 1) return __builtin_amdgcn_mov_dpp(v, 0xB1, 0xf, 0xf, false);        // quad_perm 1 0 3 2
+    else if constexpr (STEP == 2) return __builtin_amdgcn_mov_dpp(v, 0x4E, 0xf, 0xf, false);   // quad_perm 2 3 0 1
+    else if constexpr (STEP == 4) return __builtin_amdgcn_mov_dpp(v, 0x141, 0xf, 0xf, false);  // row_half_mirror
+    else return __builtin_amdgcn_mov_dpp(v, 0x140, 0xf, 0xf, false);                           // row_mirror
+}
+// The last two steps exchange whole rows of 16 (or halves of 32) lanes: both
+// sides come back, in the order (lower, upper) on every lane.
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ u32x2_t rows_of_16(uint32_t v) { return __builtin_amdgcn_permlane16_swap(v, v, false, false); }
+__device__ __forceinline__ u32x2_t halves_of_32(uint32_t v) { return __builtin_amdgcn_permlane32_swap(v, v, false, false); }
+
+// Sum (or unsigned maximum) over L consecutive lanes, L a power of two <= 64
+// and the same on every lane; every lane gets the result.
+template <typename OP> __device__ __forceinline__ uint32_t lanes_reduce(uint32_t v, int L, OP op) {
+    if (L > 1) v = op(v, other_half<1>(v));
+    if (L > 2) v = op(v, other_half<2>(v));
+    if (L > 4) v = op(v, other_half<4>(v));
+    if (L > 8) v = op(v, other_half<8>(v));
+    if (L > 16) {
+        const u32x2_t p = rows_of_16(v);
+        v = op(p.x, p.y);
+    }
+    if (L > 32) {
+        const u32x2_t p = halves_of_32(v);
+        v = op(p.x, p.y);
+    }
     return v;
 }
+__device__ __forceinline__ float lanes_sum(float v, int L) {
+    return __uint_as_float(lanes_reduce(__float_as_uint(v), L, [](uint32_t a, uint32_t b) {
+        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+    }));
+}
 __device__ __forceinline__ uint32_t lanes_max(uint32_t v, int L) {
-    for (int m = 1; m < L; m <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, m));
-    return v;
+    return lanes_reduce(v, L, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
 
 // ---- a row in 8 bits: a = max(max |v|, 2^-100), q = round(v * (127 / a)),
