@@ -152,46 +152,60 @@ __device__ __forceinline__ void products(i32x4 (&acc)[TI][TJ], const i32x4 (&w)[
         }
 }
 
+// The wave's accesses to its own piece of LDS before this are done before
+// those after it.
+__device__ __forceinline__ void wave_lds_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Four channels of a row: scaled, biased, ReLU.
+__device__ __forceinline__ float4 finish4(const Int8Args& a, const i32x4& acc, float qs, const float* sw,
+                                          const float* sb) {
+    const float4 ws = *reinterpret_cast<const float4*>(sw), bs = *reinterpret_cast<const float4*>(sb);
+    return make_float4(finish(acc[0], qs * ws.x, bs.x, a.relu), finish(acc[1], qs * ws.y, bs.y, a.relu),
+                       finish(acc[2], qs * ws.z, bs.z, a.relu), finish(acc[3], qs * ws.w, bs.w, a.relu));
+}
+
+// Block j of 16 rows of a wave's results, finished, into its piece of LDS (16
+// x TI*16 elements).  In the 16x16 result lane l holds, in register r, channel
+// 4 (l >> 4) + r of row l & 15.  The 16-byte pieces of a row are permuted with
+// the row.  OUT int: the sums themselves.
+template <int TI, typename OUT, int TJ>
+__device__ __forceinline__ void results_to_lds(const Int8Args& a, const i32x4 (&acc)[TI][TJ], int j, float qs, char* lds,
+                                               const float* sw, const float* sb) {
+    constexpr int ROW = TI * 16 * (int)sizeof(OUT), PIECES = ROW / 16, MASK = (PIECES < 16 ? PIECES : 16) - 1;
+    const int lane = threadIdx.x & 63, r16 = lane & 15;
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+        const int c = i * 16 + 4 * (lane >> 4), b = c * (int)sizeof(OUT);
+        char* const at = lds + r16 * ROW + ((b / 16) ^ (r16 & MASK)) * 16 + b % 16;
+        if constexpr (std::is_same_v<OUT, int>) {
+            *reinterpret_cast<i32x4*>(at) = acc[i][j];
+        } else {
+            const float4 v = finish4(a, acc[i][j], qs, sw + c, sb + c);
+            if constexpr (sizeof(OUT) == 4) *reinterpret_cast<float4*>(at) = v;
+            else *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        }
+    }
+    wave_lds_fence();
+}
+
 // Results of a wave's TI*16 channels x TJ*16 rows: block by block of 16 rows
-// through the wave's own piece of LDS (16 x TI*16 elements), so that whole
-// rows are written.  In the 16x16 result lane l holds, in register r, channel
-// 4 (l >> 4) + r of row l & 15.  sw, sb: the tile's channel scales and biases
-// in LDS, from the wave's first channel.  OUT int: the sums themselves.
+// through the wave's own piece of LDS, so that whole rows are written.  sq, sw,
+// sb: the row scales, channel scales and biases in LDS, from the wave's first.
 template <int TI, int TJ, typename OUT>
-__device__ __forceinline__ void write_results(const Int8Args& a, i32x4 (&acc)[TI][TJ], char* lds, const float* sw,
-                                              const float* sb, int m0, int n0, OUT* y, long long ldy, bool vec) {
+__device__ __forceinline__ void write_results(const Int8Args& a, i32x4 (&acc)[TI][TJ], char* lds, const float* sq,
+                                              const float* sw, const float* sb, int m0, int n0, OUT* y, long long ldy,
+                                              bool vec) {
     constexpr bool kSums = std::is_same_v<OUT, int>;
     constexpr int COLS = TI * 16, ROW = COLS * (int)sizeof(OUT), PIECES = ROW / 16;
     constexpr int MASK = (PIECES < 16 ? PIECES : 16) - 1;
-    const int lane = threadIdx.x & 63, r16 = lane & 15;
-    char* const row = lds + r16 * ROW;
+    const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
-        float qs = 0.0f;
-        if constexpr (!kSums) qs = m0 + j * 16 + r16 < a.M ? a.q_scale[m0 + j * 16 + r16] : 0.0f;
-#pragma unroll
-        for (int i = 0; i < TI; ++i) {
-            const int c = i * 16 + 4 * (lane >> 4), b = c * (int)sizeof(OUT);
-            char* const at = row + ((b / 16) ^ (r16 & MASK)) * 16 + b % 16;
-            if constexpr (kSums) {
-                *reinterpret_cast<i32x4*>(at) = acc[i][j];
-            } else {
-                const float4 ws = *reinterpret_cast<const float4*>(sw + c);
-                const float4 bs = *reinterpret_cast<const float4*>(sb + c);
-                const float v0 = finish(acc[i][j][0], qs * ws.x, bs.x, a.relu);
-                const float v1 = finish(acc[i][j][1], qs * ws.y, bs.y, a.relu);
-                const float v2 = finish(acc[i][j][2], qs * ws.z, bs.z, a.relu);
-                const float v3 = finish(acc[i][j][3], qs * ws.w, bs.w, a.relu);
-                if constexpr (sizeof(OUT) == 4)
-                    *reinterpret_cast<float4*>(at) = make_float4(v0, v1, v2, v3);
-                else
-                    *reinterpret_cast<uint2*>(at) = make_uint2(pack_bf16x2(v0, v1), pack_bf16x2(v2, v3));
-            }
-        }
-        // the wave's own LDS: its writes are done before its reads
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        results_to_lds<TI, OUT>(a, acc, j, kSums ? 0.0f : sq[j * 16 + (lane & 15)], lds, sw, sb);
         if (vec) {
 #pragma unroll
             for (int it = 0; it < 16 * PIECES / 64; ++it) {
@@ -209,19 +223,32 @@ __device__ __forceinline__ void write_results(const Int8Args& a, i32x4 (&acc)[TI
                     y[m * ldy + n] = *reinterpret_cast<const OUT*>(lds + r * ROW + ((b / 16) ^ (r & MASK)) * 16 + b % 16);
             }
         }
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        wave_lds_fence();
     }
 }
 
-// The tile's channel scales and biases into LDS (zero past the last channel).
-template <int BN> __device__ __forceinline__ void stage_scales(const Int8Args& a, int n0, float* sw, float* sb) {
-    for (int c = threadIdx.x; c < BN; c += blockDim.x) {
-        sw[c] = n0 + c < a.N ? a.w_scale[n0 + c] : 0.0f;
-        sb[c] = a.bias && n0 + c < a.N ? a.bias[n0 + c] : 0.0f;
+// The tile's scales and biases, one of each kind per thread: loaded before the
+// first copies are issued, put into LDS behind them (zero past the last row
+// and channel).
+template <int BM, int BN> struct Scales {
+    float q, w, b;
+    __device__ __forceinline__ void load(const Int8Args& a, int m0, int n0) {
+        const int m = m0 + threadIdx.x, n = n0 + threadIdx.x;
+        q = w = b = 0.0f;
+        if (threadIdx.x < BM && m < a.M) q = a.q_scale[m];
+        if (threadIdx.x < BN && n < a.N) {
+            w = a.w_scale[n];
+            if (a.bias) b = a.bias[n];
+        }
     }
-}
+    __device__ __forceinline__ void store(float* sq, float* sw, float* sb) const {
+        if (threadIdx.x < BM) sq[threadIdx.x] = q;
+        if (threadIdx.x < BN) {
+            sw[threadIdx.x] = w;
+            sb[threadIdx.x] = b;
+        }
+    }
+};
 
 template <typename OUT> __device__ __forceinline__ OUT* out_of(const Int8Args& a, int split) {
     return static_cast<OUT*>(a.y) + (std::is_same_v<OUT, int> ? (long long)split * a.M * a.N : 0);
@@ -233,6 +260,10 @@ __device__ __forceinline__ void copy_kb(__amdgpu_buffer_rsrc_t r, char* dst, int
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)dst, 16, off, 0, 0, 0);
 }
 
+__device__ __forceinline__ void copy_words(__amdgpu_buffer_rsrc_t r, char* dst, int off) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)dst, 4, off, 0, 0, 0);
+}
+
 // Aligned operands.  Stage s + 2 is copied into the buffer that stage s has
 // just been read from, a whole stage ahead of its use; the reads of a step
 // are issued one step before its products, across the stages' border too, so
@@ -242,10 +273,12 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_tile_kernel(Int8Args a, int
     constexpr int NW = WM * WN, TI = BN / WN / 16, TJ = BM / WM / 16;
     constexpr int STAGE = (BM + BN) * kStageK;
     constexpr int CW = BN / 8 / NW, CQ = BM / 8 / NW;   // 1 KB copies per wave and stage
+    constexpr bool kScaled = !std::is_same_v<OUT, int>;
+    static_assert(BM <= NW * 64 && BN <= NW * 64, "one row and one channel per thread");
     static_assert(CW * 8 * NW == BN && CQ * 8 * NW == BM, "copies split evenly");
     static_assert(NW * 16 * TI * 16 * 4 <= STAGE, "results fit a stage");
     __shared__ uint4 lds0[STAGE / 16], lds1[STAGE / 16];
-    __shared__ float sw[BN], sb[BN];
+    __shared__ float sq[BM], sw[BN], sb[BN];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const TileAt t = tile_at(tm, tn, BM, BN);
     const int kbase = t.split * stages * kStageK;
@@ -280,6 +313,8 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_tile_kernel(Int8Args a, int
 #pragma unroll
         for (int j = 0; j < TJ; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
     i32x4 fw[2][TI], fq[2][TJ];
+    Scales<BM, BN> scales;
+    if constexpr (kScaled) scales.load(a, t.m0, t.n0);
 
 #define I8_COPY(DST, S)                                                                                  \
     do {                                                                                                 \
@@ -327,13 +362,13 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_tile_kernel(Int8Args a, int
         I8_PRODUCTS(1, true);                                                                   \
     } while (0)
 
-    stage_scales<BN>(a, t.n0, sw, sb);
     {
         // every buffer a restrict argument of one function: the compiler then
         // does not make the reads of one wait for the copies into the other
         auto loop = [&](char* __restrict__ b0, char* __restrict__ b1) __attribute__((always_inline)) {
             I8_COPY(b0, 0);
             I8_COPY(b1, 1);
+            if constexpr (kScaled) scales.store(sq, sw, sb);
             __builtin_amdgcn_s_waitcnt(0x0070);
             __builtin_amdgcn_s_barrier();
             __atomic_signal_fence(__ATOMIC_SEQ_CST);
@@ -352,8 +387,189 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_tile_kernel(Int8Args a, int
     __builtin_amdgcn_s_waitcnt(0x0070);   // no copy is in flight when the buffers take the results
     __syncthreads();
     write_results<TI, TJ, OUT>(a, acc, reinterpret_cast<char*>(lds0) + wave * (16 * TI * 16 * (int)sizeof(OUT)),
-                               sw + wn * TI * 16, sb + wn * TI * 16, t.m0 + wm * TJ * 16, t.n0 + wn * TI * 16,
+                               sq + wm * TJ * 16, sw + wn * TI * 16, sb + wn * TI * 16, t.m0 + wm * TJ * 16, t.n0 + wn * TI * 16,
                                out_of<OUT>(a, t.split), a.ldy, vec);
+}
+
+// ------------------------------------------------------------------ streaming
+
+// Short rows (k up to 512): memory bounds them, so the weights stay in
+// registers and the rows stream past.  A workgroup of 8 waves owns BN = WN * 64
+// channels, a wave 64 of them and every WM-th group of 16 * TJ rows; row tiles
+// of BM rows come through three LDS buffers, two tiles ahead of their use, and
+// results leave as whole 128-byte lines while the next tiles arrive.  The tile
+// kernel at one or two workgroups per compute unit loads, then stores: 28.2 us
+// where this takes 20.5 (100352 x 256 rows, 256 channels, bf16 results).
+template <int KS, int WN, int TJ, typename OUT> struct StreamShape {
+    static constexpr int WM = 8 / WN, BM = WM * 16 * TJ, BN = WN * 64;
+    static constexpr int PR = KS * 4;                 // 16-byte pieces of a row
+    static constexpr int ROWS = BM * KS * 64;         // bytes of a tile
+    static constexpr int BUF = ROWS + 8 * 64 * 4;     // and of its scales, 64 from every wave
+    static constexpr int COPIES = BM * PR / 512;      // of rows, per wave and tile
+    static_assert(COPIES * 512 == BM * PR && BM <= 512, "copies split evenly");
+};
+
+// Slot of a row's 16-byte piece: 16 rows read at one piece hit all banks.
+template <int PR> __device__ __forceinline__ int stream_swizzle(int row) {
+    if constexpr (PR >= 16) return row & 15;
+    else return (row / (16 / PR)) & (PR - 1);
+}
+
+// This wave's LDS operations complete, then the workgroup barrier; copies in
+// flight are not waited for.
+__device__ __forceinline__ void stream_barrier() {
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_waitcnt(0xc07f);
+    __builtin_amdgcn_s_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
+constexpr int vmcnt_of(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0f70; }  // lgkmcnt, expcnt: no wait
+
+// Block j of 16 rows of a wave's results to memory, straight from registers:
+// fp32 lanes hold 16 bytes already; bf16 ones hold 8, and the exchange of
+// neighbouring groups of 16 lanes between two blocks of channels makes them 16.
+// Every store writes 64 contiguous bytes of 16 rows; rows and channels past
+// the end get an offset that drops them.
+template <int TI, typename OUT, int TJ>
+__device__ __forceinline__ void store_rows(const Int8Args& a, const i32x4 (&acc)[TI][TJ], int j, float qs,
+                                           const float* sw, const float* sb, __amdgpu_buffer_rsrc_t y, int row, int n0) {
+    const int lane = threadIdx.x & 63, group = lane >> 4;
+    const int at = (int)((row + (lane & 15)) * a.ldy);
+    if constexpr (sizeof(OUT) == 4) {
+#pragma unroll
+        for (int i = 0; i < TI; ++i) {
+            const int c = i * 16 + group * 4;
+            const float4 v = finish4(a, acc[i][j], qs, sw + c, sb + c);
+            store16<kStoreStream>(y, n0 + c < a.N ? (at + n0 + c) * 4 : kOOB, __builtin_bit_cast(uint4, v));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < TI; i += 2) {
+            uint32_t x[2], z[2];
+            const int c = group * 4;
+            const float4 u = finish4(a, acc[i][j], qs, sw + i * 16 + c, sb + i * 16 + c);
+            const float4 v = finish4(a, acc[i + 1][j], qs, sw + i * 16 + 16 + c, sb + i * 16 + 16 + c);
+            x[0] = pack_bf16x2(u.x, u.y), x[1] = pack_bf16x2(u.z, u.w);
+            z[0] = pack_bf16x2(v.x, v.y), z[1] = pack_bf16x2(v.z, v.w);
+            // groups 0 .. 3 then hold channels 0-7 of block i, 0-7 of i + 1,
+            // 8-15 of i, 8-15 of i + 1
+            const u32x2_t p = __builtin_amdgcn_permlane16_swap(x[0], z[0], false, false);
+            const u32x2_t q = __builtin_amdgcn_permlane16_swap(x[1], z[1], false, false);
+            const int n = n0 + (i + (group & 1)) * 16 + (group >> 1) * 8;
+            store16<kStoreStream>(y, n < a.N ? (at + n) * 2 : kOOB, make_uint4(p.x, q.x, p.y, q.y));
+        }
+    }
+}
+
+template <int KS, int WN, int TJ, typename OUT>
+__global__ __launch_bounds__(512) void int8_stream_kernel(Int8Args a, int tiles, int cols) {
+    using S = StreamShape<KS, WN, TJ, OUT>;
+    constexpr int TI = 4, D = S::COPIES + 1;
+    __shared__ uint4 lds0[S::BUF / 16], lds1[S::BUF / 16], lds2[S::BUF / 16];
+    __shared__ float scales[2 * S::BN];   // of the channels, then their biases
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const int index = xcd_tile_index(), col = index % cols, first = index / cols, stride = gridDim.x / cols;
+    const int n0 = col * S::BN;
+    const int count = first < tiles ? (tiles - first - 1) / stride + 1 : 0;
+
+    // the wave's weights: lane l holds channel l & 15 of a block at k 16 (l >> 4)
+    i32x4 w[KS][TI];
+    {
+        const auto wr = rows_rsrc(a.w, a.ldw, n0, a.N, S::BN, a.K);
+#pragma unroll
+        for (int i = 0; i < TI; ++i) {
+            const int c = wn * 64 + i * 16 + (lane & 15);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                const int k = ks * 64 + (lane >> 4) * 16;
+                w[ks][i] = __builtin_bit_cast(i32x4, load16(wr, n0 + c < a.N && k < a.K ? (int)(c * a.ldw) + k : kOOB));
+            }
+        }
+    }
+    for (int c = threadIdx.x; c < S::BN; c += 512) {
+        scales[c] = n0 + c < a.N ? a.w_scale[n0 + c] : 0.0f;
+        scales[S::BN + c] = a.bias && n0 + c < a.N ? a.bias[n0 + c] : 0.0f;
+    }
+    // before the function below, whose reads of its restrict argument the
+    // compiler may move up to its start, past the barriers inside
+    __syncthreads();
+    int qo[S::COPIES];
+#pragma unroll
+    for (int c = 0; c < S::COPIES; ++c) {
+        const int s = (c * 8 + wave) * 64 + lane, row = s / S::PR, k = (s % S::PR ^ stream_swizzle<S::PR>(row)) * 16;
+        qo[c] = k < a.K ? (int)(row * a.ldq) + k : kOOB;
+    }
+    int ro[KS];   // the lane's slot for each 64 bytes of k, in a block of 16 rows
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+        ro[ks] = ((lane & 15) * S::PR + ((ks * 4 + (lane >> 4)) ^ stream_swizzle<S::PR>(lane & 15))) * 16;
+
+// Tile T (of this workgroup's) into DST: the rows, and 64 scales from every
+// wave.  Past the last tile it writes zeros: the number of copies in flight
+// is always the same.
+#define I8_FETCH(DST, T)                                                                                   \
+    do {                                                                                                   \
+        const int m_ = (T) < count ? (first + (T) * stride) * S::BM : a.M;                                 \
+        const int left_ = min(a.M - m_, S::BM);                                                            \
+        const auto qr_ = make_rsrc(a.q + (long long)m_ * a.ldq,                                            \
+                                   left_ > 0 ? (uint32_t)((long long)(left_ - 1) * a.ldq + a.K) : 0u);     \
+        const auto sr_ = make_rsrc(a.q_scale + m_, (uint32_t)max(left_, 0) * 4u);                          \
+        _Pragma("unroll") for (int c = 0; c < S::COPIES; ++c)                                              \
+            copy_kb(qr_, (DST) + (c * 8 + wave) * 1024, qo[c]);                                            \
+        copy_words(sr_, (DST) + S::ROWS + wave * 256, wave * 256 + lane * 4);                              \
+    } while (0)
+// One tile from CUR, which has landed; the tile after the next goes to DST,
+// which the barrier has freed.  Before the tile's stores are issued, all but
+// the D youngest operations (the copies of tile T + 2) are waited for: the next
+// tile's copies and the last tile's stores, both a whole tile old.
+#define I8_TILE(CUR, DST, T)                                                                               \
+    do {                                                                                                   \
+        stream_barrier();                                                                                  \
+        I8_FETCH(DST, (T) + 2);                                                                            \
+        i32x4 acc[TI][TJ];                                                                                 \
+        _Pragma("unroll") for (int i = 0; i < TI; ++i)                                                     \
+            _Pragma("unroll") for (int j = 0; j < TJ; ++j) acc[i][j] = i32x4{0, 0, 0, 0};                  \
+        _Pragma("unroll") for (int ks = 0; ks < KS; ++ks) {                                                \
+            i32x4 q[TJ];                                                                                   \
+            _Pragma("unroll") for (int j = 0; j < TJ; ++j) q[j] = *reinterpret_cast<const i32x4*>(         \
+                (CUR) + (wm * TJ + j) * 16 * KS * 64 + ro[ks]);                                            \
+            products<TI, TJ>(acc, w[ks], q);                                                               \
+        }                                                                                                  \
+        const int m_ = (first + (T) * stride) * S::BM;                                                     \
+        const auto yr_ = make_rsrc(static_cast<OUT*>(a.y) + m_ * a.ldy,                                    \
+                                   (uint32_t)(((long long)(min(a.M - m_, S::BM) - 1) * a.ldy + a.N) * sizeof(OUT))); \
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);                                                           \
+        __builtin_amdgcn_s_waitcnt(vmcnt_of(D));                                                           \
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);                                                           \
+        _Pragma("unroll") for (int j = 0; j < TJ; ++j) {                                                   \
+            const int row_ = (wm * TJ + j) * 16;                                                           \
+            const float qs_ = reinterpret_cast<const float*>((CUR) + S::ROWS)[row_ + (lane & 15)];         \
+            store_rows<TI, OUT>(a, acc, j, qs_, sc, sc + S::BN, yr_, row_, n0 + wn * 64);                  \
+        }                                                                                                  \
+    } while (0)
+
+    // every piece of LDS a restrict argument of one function: the compiler then
+    // does not make the reads of one wait for the copies into another
+    auto run = [&](char* __restrict__ b0, char* __restrict__ b1, char* __restrict__ b2,
+                   const float* __restrict__ sc) __attribute__((always_inline)) {
+        I8_FETCH(b0, 0);
+        I8_FETCH(b1, 1);
+        __builtin_amdgcn_s_waitcnt(vmcnt_of(D));
+        for (int t = 0; t < count; t += 3) {
+            I8_TILE(b0, b2, t);
+            if (t + 1 >= count) break;
+            I8_TILE(b1, b0, t + 1);
+            if (t + 2 >= count) break;
+            I8_TILE(b2, b1, t + 2);
+        }
+    };
+    run(reinterpret_cast<char*>(lds0), reinterpret_cast<char*>(lds1), reinterpret_cast<char*>(lds2),
+        scales + wn * 64);
+#undef I8_FETCH
+#undef I8_TILE
+    __builtin_amdgcn_s_waitcnt(0x0070);   // no copy outlives the workgroup's LDS
 }
 
 // 16 bytes from any byte offset: two loads of whole words, shifted.  Bytes
@@ -388,10 +604,12 @@ template <int BM, int BN, int WM, int WN, typename OUT>
 __global__ __launch_bounds__(WM * WN * 64) void int8_ragged_kernel(Int8Args a, int tm, int tn, int stages, bool vec) {
     constexpr int NT = WM * WN * 64, TI = BN / WN / 16, TJ = BM / WM / 16;
     constexpr int STAGE = (BM + BN) * kStageK, PER = (BM + BN) * 8 / NT;
+    constexpr bool kScaled = !std::is_same_v<OUT, int>;
+    static_assert(BM <= NT && BN <= NT, "one row and one channel per thread");
     static_assert(BN * 8 % NT == 0 && BM * 8 % NT == 0, "pieces split evenly");
     constexpr int OUTB = WM * WN * 16 * TI * 16 * 4;
     __shared__ uint4 lds[(STAGE > OUTB ? STAGE : OUTB) / 16];
-    __shared__ float sw[BN], sb[BN];
+    __shared__ float sq[BM], sw[BN], sb[BN];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const TileAt t = tile_at(tm, tn, BM, BN);
     const int kbase = t.split * stages * kStageK;
@@ -417,7 +635,11 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_ragged_kernel(Int8Args a, i
     for (int i = 0; i < TI; ++i)
 #pragma unroll
         for (int j = 0; j < TJ; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-    stage_scales<BN>(a, t.n0, sw, sb);
+    Scales<BM, BN> scales;
+    if constexpr (kScaled) {
+        scales.load(a, t.m0, t.n0);
+        scales.store(sq, sw, sb);
+    }
     Unaligned v[PER];
     auto fetch = [&](int s) {
         const int k = kbase + s * kStageK + piece;
@@ -449,7 +671,7 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_ragged_kernel(Int8Args a, i
     }
     __syncthreads();
     write_results<TI, TJ, OUT>(a, acc, reinterpret_cast<char*>(lds) + wave * (16 * TI * 16 * (int)sizeof(OUT)),
-                               sw + wn * TI * 16, sb + wn * TI * 16, t.m0 + wm * TJ * 16, t.n0 + wn * TI * 16,
+                               sq + wm * TJ * 16, sw + wn * TI * 16, sb + wn * TI * 16, t.m0 + wm * TJ * 16, t.n0 + wn * TI * 16,
                                out_of<OUT>(a, t.split), a.ldy, vec);
 }
 
@@ -553,7 +775,7 @@ bool aligned_operands(const Int8Args& a) {
     return a.K % 16 == 0 && a.ldq % 16 == 0 && a.ldw % 16 == 0 && al(a.q) && al(a.w);
 }
 
-enum { kSkinny, kTile256, kTile128, kTile64, kRagged128, kRagged64 };
+enum { kSkinny, kStream, kTile256, kTile128, kTile64, kRagged128, kRagged64 };
 
 struct Int8Plan {
     int kernel, bm, bn, tm, tn, splits, stages;
@@ -566,8 +788,39 @@ struct Int8Plan {
 constexpr int kSkinnyRows = 64;
 constexpr int kUnits = 256;
 
-Int8Plan make_int8_plan(int M, int K, int N, bool aligned) {
+// `stream`: y takes 16-byte stores, which the streaming kernel needs.
+// The streaming kernel's instance for a K and N: ks of 64 bytes of k, wn of 64
+// channels, tj blocks of 16 rows a wave.
+constexpr int kStreamK = 512;
+constexpr long long kStreamStride = 1 << 20;  // a tile of y is addressed with 31 bits
+
+struct StreamTile {
+    int ks, wn, tj, bm, bn;
+};
+
+StreamTile stream_tile(int K, int N) {
+    StreamTile t;
+    t.ks = K <= 64 ? 1 : K <= 128 ? 2 : K <= 256 ? 4 : 8;
+    t.wn = N > 128 ? 4 : N > 64 || t.ks == 8 ? 2 : 1;
+    // at least one 16-byte copy per thread and tile, and no more than 32 KB
+    t.tj = t.wn == 4 ? (t.ks == 1 ? 4 : t.ks == 8 ? 1 : 2) : t.wn == 2 && t.ks == 1 ? 2 : 1;
+    t.bm = 8 / t.wn * 16 * t.tj;
+    t.bn = t.wn * 64;
+    return t;
+}
+
+Int8Plan make_int8_plan(int M, int K, int N, bool aligned, bool stream) {
     Int8Plan p;
+    p.stages = p.splits = 1;
+    if (aligned && stream && M > kSkinnyRows && K <= kStreamK) {
+        const StreamTile t = stream_tile(K, N);
+        p.kernel = kStream;
+        p.bm = t.bm;
+        p.bn = t.bn;
+        p.tm = (M + p.bm - 1) / p.bm;
+        p.tn = (N + p.bn - 1) / p.bn;
+        if ((long long)p.tm * p.tn >= kUnits) return p;
+    }
     auto tiles = [&](int b) { return (long long)((M + b - 1) / b) * ((N + b - 1) / b); };
     if (aligned && M <= kSkinnyRows) {
         p.kernel = kSkinny;
@@ -605,9 +858,38 @@ template <typename OUT> hipError_t skinny(const Int8Args& a, const Int8Plan& p, 
     return hipGetLastError();
 }
 
+template <int KS, int WN, int TJ, typename OUT>
+hipError_t stream_instance(const Int8Args& a, const Int8Plan& p, hipStream_t st) {
+    int dev = 0;
+    const hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    constexpr auto kernel = int8_stream_kernel<KS, WN, TJ, OUT>;
+    const long long slots = (long long)cu_count(dev) * blocks_per_cu<kernel>(512, dev);
+    long long rows = slots / p.tn;   // workgroups per block of channels
+    rows = rows < 1 ? 1 : rows > p.tm ? p.tm : rows;
+    kernel<<<(unsigned)(rows * p.tn), 512, 0, st>>>(a, p.tm, p.tn);
+    return hipGetLastError();
+}
+
+template <typename OUT> hipError_t stream(const Int8Args& a, const Int8Plan& p, hipStream_t st) {
+    const StreamTile t = stream_tile(a.K, a.N);
+    if (t.wn == 4)
+        return t.ks == 1 ? stream_instance<1, 4, 4, OUT>(a, p, st) : t.ks == 2 ? stream_instance<2, 4, 2, OUT>(a, p, st)
+               : t.ks == 4 ? stream_instance<4, 4, 2, OUT>(a, p, st) : stream_instance<8, 4, 1, OUT>(a, p, st);
+    if (t.wn == 2)
+        return t.ks == 1 ? stream_instance<1, 2, 2, OUT>(a, p, st) : t.ks == 2 ? stream_instance<2, 2, 1, OUT>(a, p, st)
+               : t.ks == 4 ? stream_instance<4, 2, 1, OUT>(a, p, st) : stream_instance<8, 2, 1, OUT>(a, p, st);
+    return t.ks == 1 ? stream_instance<1, 1, 1, OUT>(a, p, st) : t.ks == 2 ? stream_instance<2, 1, 1, OUT>(a, p, st)
+                                                                           : stream_instance<4, 1, 1, OUT>(a, p, st);
+}
+
+// y takes 16-byte stores
+bool vector_stores(const Int8Args& a, int es) {
+    return a.ldy * es % 16 == 0 && a.N * (long long)es % 16 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
+}
+
 template <typename OUT> hipError_t tiled(const Int8Args& a, const Int8Plan& p, hipStream_t st) {
-    const int es = (int)sizeof(OUT);
-    const bool vec = a.ldy * es % 16 == 0 && a.N * (long long)es % 16 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
+    const bool vec = vector_stores(a, (int)sizeof(OUT));
     const int blocks = p.tm * p.tn * p.splits;
     switch (p.kernel) {
     case kTile256: int8_tile_kernel<256, 256, 2, 4, OUT><<<blocks, 512, 0, st>>>(a, p.tm, p.tn, p.stages, vec); break;
@@ -627,8 +909,8 @@ size_t split_bytes(const Int8Plan& p, int M, int N) {
 
 // One figure for either alignment.
 size_t int8_matmul_workspace(int M, int K, int N) {
-    const size_t u = split_bytes(make_int8_plan(M, K, N, false), M, N);
-    const size_t v = K % 16 ? 0 : split_bytes(make_int8_plan(M, K, N, true), M, N);
+    const size_t u = split_bytes(make_int8_plan(M, K, N, false, false), M, N);
+    const size_t v = K % 16 ? 0 : split_bytes(make_int8_plan(M, K, N, true, false), M, N);
     return u > v ? u : v;
 }
 
@@ -636,14 +918,16 @@ bool int8_matmul_supports(int M, int K, int N, long long ldq, long long ldw) {
     // sums stay below 2^31; a tile's rows are addressed with 31 bits; the grid
     if (K > 131071 || ldq > (1 << 22) || ldw > (1 << 22)) return false;
     for (int al = 0; al < 2; ++al) {
-        const Int8Plan p = make_int8_plan(M, K, N, al);
+        const Int8Plan p = make_int8_plan(M, K, N, al, false);
         if ((long long)p.tm * p.tn * p.splits >= 0x7fffffffLL) return false;
     }
     return true;
 }
 
 hipError_t launch_int8_matmul(const Int8Args& a, int out_f32, void* ws, hipStream_t st) {
-    const Int8Plan p = make_int8_plan(a.M, a.K, a.N, aligned_operands(a));
+    const bool wide = vector_stores(a, out_f32 ? 4 : 2) && a.ldy <= kStreamStride;
+    const Int8Plan p = make_int8_plan(a.M, a.K, a.N, aligned_operands(a), wide);
+    if (p.kernel == kStream) return out_f32 ? stream<float>(a, p, st) : stream<bf16_t>(a, p, st);
     if (p.kernel == kSkinny) return out_f32 ? skinny<float>(a, p, st) : skinny<bf16_t>(a, p, st);
     if (p.splits == 1) return out_f32 ? tiled<float>(a, p, st) : tiled<bf16_t>(a, p, st);
     Int8Args part = a;

@@ -127,6 +127,17 @@ def test_large_tiles(M, K, N):
         run_product(M, K, N, dtype)
 
 
+# many short rows: the weights stay in registers and the rows stream past, in
+# every combination of k (up to 64, 128, 256, 512) and channels (up to 64, 128,
+# 256, more), with tiles and channels that end inside a block
+@pytest.mark.parametrize("K", [16, 64, 80, 128, 192, 256, 336, 512])
+def test_short_rows_stream(K):
+    for M, N in [(40001, 24), (33000, 64), (20011, 72), (16500, 128), (9001, 136), (9000, 256), (5003, 520)]:
+        run_product(M, K, N, "bf16", bias=M % 2 == 0, relu=N % 3 == 0)
+    for M, N in [(40001, 60), (20011, 100), (9001, 252), (5003, 516)]:
+        run_product(M, K, N, "f32", padq=16, pady=4, bias=M % 2 == 1)
+
+
 @pytest.mark.parametrize("M", [1, 64, 70])
 def test_extreme_sums_are_exact(M):
     """-128 * -128 over the longest row: 2147467264, just below 2^31."""
