@@ -786,12 +786,14 @@ struct Resident {
 };
 
 constexpr long long kResidentBytes = 8 << 20;
+constexpr long long kResidentUnitBytes = 48 << 10;
 
 Resident make_resident(const NormArgs& a, int V, int elem, int most) {
     Resident p = {0, 0, 0, 0};
     const int cg = a.C / a.G;
     p.TX = cg / V;
     const long long bytes = (long long)a.N * a.P * a.C * elem;
+    if ((long long)a.N * a.G < 256 && (long long)a.P * cg * elem > kResidentUnitBytes) return p;
     if (p.TX > 256 || (bytes > kResidentBytes && cg * elem < 64) || (long long)a.N * a.G >= 0x7fffffffLL) return p;
     for (p.block = 256; p.block <= 1024; p.block *= 2) {
         p.R = p.block / p.TX;

@@ -30,6 +30,8 @@ namespace conv2d {
 namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_unaligned __attribute__((aligned(2)));
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 // Descriptor of rows [r0, rows) of a row-major byte matrix, starting at row
@@ -160,6 +162,23 @@ __device__ __forceinline__ void wave_lds_fence() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// 16 bytes of results (8 bf16, 4 fp32 or int) to channels n .. of a row, fewer
+// at the row's end.  The address is aligned to an element only (a row may have
+// any length): one store all the same.
+template <typename OUT> __device__ __forceinline__ void store_piece(OUT* row, int n, int N, const uint4& v) {
+    constexpr int E = 16 / (int)sizeof(OUT);
+    if (n + E <= N) {
+        *reinterpret_cast<u32x4_unaligned*>(row + n) = __builtin_bit_cast(u32x4, v);
+    } else {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (n + e < N)
+                row[n + e] = sizeof(OUT) == 4 ? __builtin_bit_cast(OUT, (typename RawBytes<sizeof(OUT)>::type)w[e * (int)sizeof(OUT) / 4])
+                                              : __builtin_bit_cast(OUT, (typename RawBytes<sizeof(OUT)>::type)(w[e / 2] >> (16 * (e & 1))));
+    }
+}
+
 // Four channels of a row: scaled, biased, ReLU.
 __device__ __forceinline__ float4 finish4(const Int8Args& a, const i32x4& acc, float qs, const float* sw,
                                           const float* sb) {
@@ -197,31 +216,20 @@ __device__ __forceinline__ void results_to_lds(const Int8Args& a, const i32x4 (&
 // sb: the row scales, channel scales and biases in LDS, from the wave's first.
 template <int TI, int TJ, typename OUT>
 __device__ __forceinline__ void write_results(const Int8Args& a, i32x4 (&acc)[TI][TJ], char* lds, const float* sq,
-                                              const float* sw, const float* sb, int m0, int n0, OUT* y, long long ldy,
-                                              bool vec) {
+                                              const float* sw, const float* sb, int m0, int n0, OUT* y, long long ldy) {
     constexpr bool kSums = std::is_same_v<OUT, int>;
-    constexpr int COLS = TI * 16, ROW = COLS * (int)sizeof(OUT), PIECES = ROW / 16;
+    constexpr int ROW = TI * 16 * (int)sizeof(OUT), PIECES = ROW / 16;
     constexpr int MASK = (PIECES < 16 ? PIECES : 16) - 1;
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int j = 0; j < TJ; ++j) {
         results_to_lds<TI, OUT>(a, acc, j, kSums ? 0.0f : sq[j * 16 + (lane & 15)], lds, sw, sb);
-        if (vec) {
 #pragma unroll
-            for (int it = 0; it < 16 * PIECES / 64; ++it) {
-                const int e = it * 64 + lane, r = e / PIECES, p = e % PIECES;
-                const int m = m0 + j * 16 + r, n = n0 + p * (16 / (int)sizeof(OUT));
-                if (m < a.M && n < a.N)
-                    *reinterpret_cast<uint4*>(y + m * ldy + n) =
-                        *reinterpret_cast<const uint4*>(lds + r * ROW + (p ^ (r & MASK)) * 16);
-            }
-        } else {
-            for (int e = lane; e < 16 * COLS; e += 64) {
-                const int r = e / COLS, c = e % COLS, b = c * (int)sizeof(OUT);
-                const int m = m0 + j * 16 + r, n = n0 + c;
-                if (m < a.M && n < a.N)
-                    y[m * ldy + n] = *reinterpret_cast<const OUT*>(lds + r * ROW + ((b / 16) ^ (r & MASK)) * 16 + b % 16);
-            }
+        for (int it = 0; it < 16 * PIECES / 64; ++it) {
+            const int e = it * 64 + lane, r = e / PIECES, p = e % PIECES;
+            const int m = m0 + j * 16 + r, n = n0 + p * (16 / (int)sizeof(OUT));
+            if (m < a.M)
+                store_piece<OUT>(y + m * ldy, n, a.N, *reinterpret_cast<const uint4*>(lds + r * ROW + (p ^ (r & MASK)) * 16));
         }
         wave_lds_fence();
     }
@@ -269,7 +277,7 @@ __device__ __forceinline__ void copy_words(__amdgpu_buffer_rsrc_t r, char* dst, 
 // are issued one step before its products, across the stages' border too, so
 // there is one barrier per stage.
 template <int BM, int BN, int WM, int WN, typename OUT>
-__global__ __launch_bounds__(WM * WN * 64) void int8_tile_kernel(Int8Args a, int tm, int tn, int stages, bool vec) {
+__global__ __launch_bounds__(WM * WN * 64) void int8_tile_kernel(Int8Args a, int tm, int tn, int stages) {
     constexpr int NW = WM * WN, TI = BN / WN / 16, TJ = BM / WM / 16;
     constexpr int STAGE = (BM + BN) * kStageK;
     constexpr int CW = BN / 8 / NW, CQ = BM / 8 / NW;   // 1 KB copies per wave and stage
@@ -388,7 +396,7 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_tile_kernel(Int8Args a, int
     __syncthreads();
     write_results<TI, TJ, OUT>(a, acc, reinterpret_cast<char*>(lds0) + wave * (16 * TI * 16 * (int)sizeof(OUT)),
                                sq + wm * TJ * 16, sw + wn * TI * 16, sb + wn * TI * 16, t.m0 + wm * TJ * 16, t.n0 + wn * TI * 16,
-                               out_of<OUT>(a, t.split), a.ldy, vec);
+                               out_of<OUT>(a, t.split), a.ldy);
 }
 
 // ------------------------------------------------------------------ streaming
@@ -429,41 +437,41 @@ constexpr int vmcnt_of(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0f70; }  
 // Block j of 16 rows of a wave's results to memory, straight from registers:
 // fp32 lanes hold 16 bytes already; bf16 ones hold 8, and the exchange of
 // neighbouring groups of 16 lanes between two blocks of channels makes them 16.
-// Every store writes 64 contiguous bytes of 16 rows; rows and channels past
-// the end get an offset that drops them.
+// Every store writes 64 contiguous bytes of 16 rows.
 template <int TI, typename OUT, int TJ>
 __device__ __forceinline__ void store_rows(const Int8Args& a, const i32x4 (&acc)[TI][TJ], int j, float qs,
-                                           const float* sw, const float* sb, __amdgpu_buffer_rsrc_t y, int row, int n0) {
-    const int lane = threadIdx.x & 63, group = lane >> 4;
-    const int at = (int)((row + (lane & 15)) * a.ldy);
+                                           const float* sw, const float* sb, int m, int n0, bool whole) {
+    const int group = (threadIdx.x & 63) >> 4;
+    OUT* row = static_cast<OUT*>(a.y) + m * a.ldy;
+    // whole: rows are multiples of 16 bytes and written past the cache
+    auto put = [&](int n, const uint4& v) {
+        if (m >= a.M) return;
+        if (!whole) store_piece<OUT>(row, n, a.N, v);
+        else if (n < a.N) __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4*>(row + n));
+    };
     if constexpr (sizeof(OUT) == 4) {
 #pragma unroll
         for (int i = 0; i < TI; ++i) {
             const int c = i * 16 + group * 4;
-            const float4 v = finish4(a, acc[i][j], qs, sw + c, sb + c);
-            store16<kStoreStream>(y, n0 + c < a.N ? (at + n0 + c) * 4 : kOOB, __builtin_bit_cast(uint4, v));
+            put(n0 + c, __builtin_bit_cast(uint4, finish4(a, acc[i][j], qs, sw + c, sb + c)));
         }
     } else {
 #pragma unroll
         for (int i = 0; i < TI; i += 2) {
-            uint32_t x[2], z[2];
-            const int c = group * 4;
-            const float4 u = finish4(a, acc[i][j], qs, sw + i * 16 + c, sb + i * 16 + c);
-            const float4 v = finish4(a, acc[i + 1][j], qs, sw + i * 16 + 16 + c, sb + i * 16 + 16 + c);
-            x[0] = pack_bf16x2(u.x, u.y), x[1] = pack_bf16x2(u.z, u.w);
-            z[0] = pack_bf16x2(v.x, v.y), z[1] = pack_bf16x2(v.z, v.w);
+            const int c = i * 16 + group * 4;
+            const float4 u = finish4(a, acc[i][j], qs, sw + c, sb + c);
+            const float4 v = finish4(a, acc[i + 1][j], qs, sw + 16 + c, sb + 16 + c);
             // groups 0 .. 3 then hold channels 0-7 of block i, 0-7 of i + 1,
             // 8-15 of i, 8-15 of i + 1
-            const u32x2_t p = __builtin_amdgcn_permlane16_swap(x[0], z[0], false, false);
-            const u32x2_t q = __builtin_amdgcn_permlane16_swap(x[1], z[1], false, false);
-            const int n = n0 + (i + (group & 1)) * 16 + (group >> 1) * 8;
-            store16<kStoreStream>(y, n < a.N ? (at + n) * 2 : kOOB, make_uint4(p.x, q.x, p.y, q.y));
+            const u32x2_t p = __builtin_amdgcn_permlane16_swap(pack_bf16x2(u.x, u.y), pack_bf16x2(v.x, v.y), false, false);
+            const u32x2_t q = __builtin_amdgcn_permlane16_swap(pack_bf16x2(u.z, u.w), pack_bf16x2(v.z, v.w), false, false);
+            put(n0 + (i + (group & 1)) * 16 + (group >> 1) * 8, make_uint4(p.x, q.x, p.y, q.y));
         }
     }
 }
 
 template <int KS, int WN, int TJ, typename OUT>
-__global__ __launch_bounds__(512) void int8_stream_kernel(Int8Args a, int tiles, int cols) {
+__global__ __launch_bounds__(512) void int8_stream_kernel(Int8Args a, int tiles, int cols, bool whole) {
     using S = StreamShape<KS, WN, TJ, OUT>;
     constexpr int TI = 4, D = S::COPIES + 1;
     __shared__ uint4 lds0[S::BUF / 16], lds1[S::BUF / 16], lds2[S::BUF / 16];
@@ -538,15 +546,13 @@ __global__ __launch_bounds__(512) void int8_stream_kernel(Int8Args a, int tiles,
             products<TI, TJ>(acc, w[ks], q);                                                               \
         }                                                                                                  \
         const int m_ = (first + (T) * stride) * S::BM;                                                     \
-        const auto yr_ = make_rsrc(static_cast<OUT*>(a.y) + m_ * a.ldy,                                    \
-                                   (uint32_t)(((long long)(min(a.M - m_, S::BM) - 1) * a.ldy + a.N) * sizeof(OUT))); \
         __atomic_signal_fence(__ATOMIC_SEQ_CST);                                                           \
         __builtin_amdgcn_s_waitcnt(vmcnt_of(D));                                                           \
         __atomic_signal_fence(__ATOMIC_SEQ_CST);                                                           \
         _Pragma("unroll") for (int j = 0; j < TJ; ++j) {                                                   \
             const int row_ = (wm * TJ + j) * 16;                                                           \
             const float qs_ = reinterpret_cast<const float*>((CUR) + S::ROWS)[row_ + (lane & 15)];         \
-            store_rows<TI, OUT>(a, acc, j, qs_, sc, sc + S::BN, yr_, row_, n0 + wn * 64);                  \
+            store_rows<TI, OUT>(a, acc, j, qs_, sc, sc + S::BN, m_ + row_ + (lane & 15), n0 + wn * 64, whole); \
         }                                                                                                  \
     } while (0)
 
@@ -601,7 +607,7 @@ __device__ __forceinline__ uint4 shift_words(const Unaligned& u, int off, int le
 // Operands of any alignment: the loads of stage s + 1 are in flight during
 // the products of stage s.
 template <int BM, int BN, int WM, int WN, typename OUT>
-__global__ __launch_bounds__(WM * WN * 64) void int8_ragged_kernel(Int8Args a, int tm, int tn, int stages, bool vec) {
+__global__ __launch_bounds__(WM * WN * 64) void int8_ragged_kernel(Int8Args a, int tm, int tn, int stages) {
     constexpr int NT = WM * WN * 64, TI = BN / WN / 16, TJ = BM / WM / 16;
     constexpr int STAGE = (BM + BN) * kStageK, PER = (BM + BN) * 8 / NT;
     constexpr bool kScaled = !std::is_same_v<OUT, int>;
@@ -672,7 +678,7 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_ragged_kernel(Int8Args a, i
     __syncthreads();
     write_results<TI, TJ, OUT>(a, acc, reinterpret_cast<char*>(lds) + wave * (16 * TI * 16 * (int)sizeof(OUT)),
                                sq + wm * TJ * 16, sw + wn * TI * 16, sb + wn * TI * 16, t.m0 + wm * TJ * 16, t.n0 + wn * TI * 16,
-                               out_of<OUT>(a, t.split), a.ldy, vec);
+                               out_of<OUT>(a, t.split), a.ldy);
 }
 
 // Adds the pieces of a product that was split along k and finishes it.
@@ -788,11 +794,9 @@ struct Int8Plan {
 constexpr int kSkinnyRows = 64;
 constexpr int kUnits = 256;
 
-// `stream`: y takes 16-byte stores, which the streaming kernel needs.
 // The streaming kernel's instance for a K and N: ks of 64 bytes of k, wn of 64
 // channels, tj blocks of 16 rows a wave.
 constexpr int kStreamK = 512;
-constexpr long long kStreamStride = 1 << 20;  // a tile of y is addressed with 31 bits
 
 struct StreamTile {
     int ks, wn, tj, bm, bn;
@@ -809,17 +813,22 @@ StreamTile stream_tile(int K, int N) {
     return t;
 }
 
-Int8Plan make_int8_plan(int M, int K, int N, bool aligned, bool stream) {
+Int8Plan make_int8_plan(int M, int K, int N, bool aligned) {
     Int8Plan p;
     p.stages = p.splits = 1;
-    if (aligned && stream && M > kSkinnyRows && K <= kStreamK) {
+    if (aligned && M > kSkinnyRows && K <= kStreamK) {
         const StreamTile t = stream_tile(K, N);
         p.kernel = kStream;
         p.bm = t.bm;
         p.bn = t.bn;
         p.tm = (M + p.bm - 1) / p.bm;
         p.tn = (N + p.bn - 1) / p.bn;
-        if ((long long)p.tm * p.tn >= kUnits) return p;
+        // enough tiles for each workgroup to earn the load of its weights:
+        // 6 a compute unit up to k = 256 (16384 x 256 -> 1024, 4 each: 15.9 us
+        // against 14.3 tiled; 100352 x 256 -> 256, 6 each: 21.7 against 28.5),
+        // 16 above, where a tile is half as long (16384 x 512 -> 1024, 8 each:
+        // 22.4 against 17.0; 65536 x 512 -> 512, 16 each: 35.1 against 38.1)
+        if ((long long)p.tm * p.tn >= (K <= 256 ? 6 : 16) * kUnits && (K <= 256 || N > 64)) return p;
     }
     auto tiles = [&](int b) { return (long long)((M + b - 1) / b) * ((N + b - 1) / b); };
     if (aligned && M <= kSkinnyRows) {
@@ -827,14 +836,15 @@ Int8Plan make_int8_plan(int M, int K, int N, bool aligned, bool stream) {
         p.bm = kSkinnyRows;
         p.bn = 16;
     } else {
-        const int b = aligned && tiles(256) >= kUnits ? 256 : tiles(128) >= kUnits ? 128 : 64;
+        // no tile wider than the channels: 65536 x 512 -> 64 takes 9.9 us in
+        // tiles of 64 and 16.3 in tiles of 256
+        const int b = aligned && N > 128 && tiles(256) >= kUnits ? 256 : N > 64 && tiles(128) >= kUnits ? 128 : 64;
         p.kernel = aligned ? (b == 256 ? kTile256 : b == 128 ? kTile128 : kTile64) : b == 128 ? kRagged128 : kRagged64;
         p.bm = p.bn = b;
     }
     p.tm = (M + p.bm - 1) / p.bm;
     p.tn = (N + p.bn - 1) / p.bn;
     const int all = (K + kStageK - 1) / kStageK;
-    p.splits = 1;
     if (p.kernel != kSkinny) {
         const long long t = (long long)p.tm * p.tn;
         // a piece is at least 4 stages long
@@ -858,6 +868,11 @@ template <typename OUT> hipError_t skinny(const Int8Args& a, const Int8Plan& p, 
     return hipGetLastError();
 }
 
+// Rows of y are whole, aligned 16-byte pieces.
+bool vector_stores(const Int8Args& a, int es) {
+    return a.ldy * es % 16 == 0 && a.N * (long long)es % 16 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
+}
+
 template <int KS, int WN, int TJ, typename OUT>
 hipError_t stream_instance(const Int8Args& a, const Int8Plan& p, hipStream_t st) {
     int dev = 0;
@@ -867,7 +882,7 @@ hipError_t stream_instance(const Int8Args& a, const Int8Plan& p, hipStream_t st)
     const long long slots = (long long)cu_count(dev) * blocks_per_cu<kernel>(512, dev);
     long long rows = slots / p.tn;   // workgroups per block of channels
     rows = rows < 1 ? 1 : rows > p.tm ? p.tm : rows;
-    kernel<<<(unsigned)(rows * p.tn), 512, 0, st>>>(a, p.tm, p.tn);
+    kernel<<<(unsigned)(rows * p.tn), 512, 0, st>>>(a, p.tm, p.tn, vector_stores(a, (int)sizeof(OUT)));
     return hipGetLastError();
 }
 
@@ -883,20 +898,14 @@ template <typename OUT> hipError_t stream(const Int8Args& a, const Int8Plan& p, 
                                                                            : stream_instance<4, 1, 1, OUT>(a, p, st);
 }
 
-// y takes 16-byte stores
-bool vector_stores(const Int8Args& a, int es) {
-    return a.ldy * es % 16 == 0 && a.N * (long long)es % 16 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
-}
-
 template <typename OUT> hipError_t tiled(const Int8Args& a, const Int8Plan& p, hipStream_t st) {
-    const bool vec = vector_stores(a, (int)sizeof(OUT));
     const int blocks = p.tm * p.tn * p.splits;
     switch (p.kernel) {
-    case kTile256: int8_tile_kernel<256, 256, 2, 4, OUT><<<blocks, 512, 0, st>>>(a, p.tm, p.tn, p.stages, vec); break;
-    case kTile128: int8_tile_kernel<128, 128, 2, 2, OUT><<<blocks, 256, 0, st>>>(a, p.tm, p.tn, p.stages, vec); break;
-    case kTile64: int8_tile_kernel<64, 64, 2, 2, OUT><<<blocks, 256, 0, st>>>(a, p.tm, p.tn, p.stages, vec); break;
-    case kRagged128: int8_ragged_kernel<128, 128, 2, 2, OUT><<<blocks, 256, 0, st>>>(a, p.tm, p.tn, p.stages, vec); break;
-    default: int8_ragged_kernel<64, 64, 2, 2, OUT><<<blocks, 256, 0, st>>>(a, p.tm, p.tn, p.stages, vec); break;
+    case kTile256: int8_tile_kernel<256, 256, 2, 4, OUT><<<blocks, 512, 0, st>>>(a, p.tm, p.tn, p.stages); break;
+    case kTile128: int8_tile_kernel<128, 128, 2, 2, OUT><<<blocks, 256, 0, st>>>(a, p.tm, p.tn, p.stages); break;
+    case kTile64: int8_tile_kernel<64, 64, 2, 2, OUT><<<blocks, 256, 0, st>>>(a, p.tm, p.tn, p.stages); break;
+    case kRagged128: int8_ragged_kernel<128, 128, 2, 2, OUT><<<blocks, 256, 0, st>>>(a, p.tm, p.tn, p.stages); break;
+    default: int8_ragged_kernel<64, 64, 2, 2, OUT><<<blocks, 256, 0, st>>>(a, p.tm, p.tn, p.stages); break;
     }
     return hipGetLastError();
 }
@@ -909,8 +918,8 @@ size_t split_bytes(const Int8Plan& p, int M, int N) {
 
 // One figure for either alignment.
 size_t int8_matmul_workspace(int M, int K, int N) {
-    const size_t u = split_bytes(make_int8_plan(M, K, N, false, false), M, N);
-    const size_t v = K % 16 ? 0 : split_bytes(make_int8_plan(M, K, N, true, false), M, N);
+    const size_t u = split_bytes(make_int8_plan(M, K, N, false), M, N);
+    const size_t v = K % 16 ? 0 : split_bytes(make_int8_plan(M, K, N, true), M, N);
     return u > v ? u : v;
 }
 
@@ -918,15 +927,14 @@ bool int8_matmul_supports(int M, int K, int N, long long ldq, long long ldw) {
     // sums stay below 2^31; a tile's rows are addressed with 31 bits; the grid
     if (K > 131071 || ldq > (1 << 22) || ldw > (1 << 22)) return false;
     for (int al = 0; al < 2; ++al) {
-        const Int8Plan p = make_int8_plan(M, K, N, al, false);
+        const Int8Plan p = make_int8_plan(M, K, N, al);
         if ((long long)p.tm * p.tn * p.splits >= 0x7fffffffLL) return false;
     }
     return true;
 }
 
 hipError_t launch_int8_matmul(const Int8Args& a, int out_f32, void* ws, hipStream_t st) {
-    const bool wide = vector_stores(a, out_f32 ? 4 : 2) && a.ldy <= kStreamStride;
-    const Int8Plan p = make_int8_plan(a.M, a.K, a.N, aligned_operands(a), wide);
+    const Int8Plan p = make_int8_plan(a.M, a.K, a.N, aligned_operands(a));
     if (p.kernel == kStream) return out_f32 ? stream<float>(a, p, st) : stream<bf16_t>(a, p, st);
     if (p.kernel == kSkinny) return out_f32 ? skinny<float>(a, p, st) : skinny<bf16_t>(a, p, st);
     if (p.splits == 1) return out_f32 ? tiled<float>(a, p, st) : tiled<bf16_t>(a, p, st);
