@@ -58,20 +58,36 @@ __device__ __forceinline__ int lanes_per(int count) {
     return L;
 }
 
-// B vectors of a thread, `step` elements apart, from value i of cnt on.
+// B vectors of a thread, `step` elements apart, from value i of cnt on.  Loads
+// past the end repeat the last value (or the first, where there is none), so
+// that all B are issued together; p is the thread's first value, inside the
+// tensor even if cnt is 0.  `every`: the values that each thread of the
+// workgroup has, the same for all.
 template <typename T, int V, int B> struct Batch {
     typename Vec<T, V>::raw raw[B];
-    __device__ __forceinline__ void load(const T* p, long long step, int i, int cnt) {
-        if (i + B <= cnt) {
+    __device__ __forceinline__ void load(const T* p, long long step, int i, int cnt, int every) {
+        if (i + B <= every) {
 #pragma unroll
             for (int u = 0; u < B; ++u) raw[u] = Vec<T, V>::load(p + (i + u) * step);
         } else {
 #pragma unroll
-            for (int u = 0; u < B; ++u)
-                if (i + u < cnt) raw[u] = Vec<T, V>::load(p + (i + u) * step);
+            for (int u = 0; u < B; ++u) raw[u] = Vec<T, V>::load(p + max(min(i + u, cnt - 1), 0) * step);
         }
     }
 };
+
+// f(u) for the values i + u < cnt of a batch, without the comparisons where
+// every thread has them all.
+template <int B, typename F> __device__ __forceinline__ void each(int i, int cnt, int every, F&& f) {
+    if (i + B <= every) {
+#pragma unroll
+        for (int u = 0; u < B; ++u) f(u);
+    } else {
+#pragma unroll
+        for (int u = 0; u < B; ++u)
+            if (i + u < cnt) f(u);
+    }
+}
 
 // Combines an image's chunk partials (mean, M2) into mean and rstd in LDS, in
 // one pass: with d = mean_i - mean_0, M2 = sum(M2_i) + sum(n d^2) - sum(n d)^2 / N.
@@ -86,12 +102,17 @@ __device__ __forceinline__ void combine_stats(const float2* part, const NormArgs
         const float2* p = part + (long long)n * chunks * a.G + g;
         const float base = p[0].x;
         float s = 0.0f, ss = 0.0f;
-#pragma unroll 4
-        for (int j = lane; j < chunks; j += L) {
-            const float2 e = p[(long long)j * a.G];
-            const float w = j == chunks - 1 ? last : full, d = e.x - base;
-            s = fmaf(w, d, s);
-            ss += fmaf(w * d, d, e.y);
+        for (int j0 = lane; j0 < chunks; j0 += 8 * L) {
+            float2 e[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) e[u] = p[(long long)min(j0 + u * L, chunks - 1) * a.G];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int j = j0 + u * L;
+                const float w = j >= chunks ? 0.0f : j == chunks - 1 ? last : full, d = e[u].x - base;
+                s = fmaf(w, d, s);
+                ss += fmaf(w * d, d, j >= chunks ? 0.0f : e[u].y);
+            }
         }
         s = lanes_sum(s, L);
         ss = lanes_sum(ss, L);
@@ -111,21 +132,20 @@ __global__ __launch_bounds__(512) void gn_stats_kernel(NormArgs a, int TX, int R
     const int r = threadIdx.x / TX, tx = threadIdx.x - r * TX;
     const int p0 = chunk * pix, np = min(pix, a.P - p0);
     const long long step = (long long)R * a.ldx;
+    const int every = np / R;
     if (r < R) {
         const int cnt = row_count(np, R, r);
         for (int c = tx * V; c < a.C; c += TX * V) {
-            const T* p = static_cast<const T*>(a.x) + ((long long)n * a.P + p0 + r) * a.ldx + c;
-            float k[V], s[V], ss[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j) k[j] = s[j] = ss[j] = 0.0f;
+            const T* p = static_cast<const T*>(a.x) + ((long long)n * a.P + p0 + min(r, np - 1)) * a.ldx + c;
             Batch<T, V, kBatch> b;
-            b.load(p, step, 0, cnt);
-            if (cnt > 0) Vec<T, V>::unpack(b.raw[0], k);
-            for (int i = 0; i < cnt; i += kBatch) {
-                if (i > 0) b.load(p, step, i, cnt);
+            b.load(p, step, 0, cnt, every);
+            float k[V], s[V], ss[V];
+            Vec<T, V>::unpack(b.raw[0], k);
 #pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    if (i + u >= cnt) break;
+            for (int j = 0; j < V; ++j) s[j] = ss[j] = 0.0f;
+            for (int i = 0; i < cnt; i += kBatch) {
+                if (i > 0) b.load(p, step, i, cnt, every);
+                each<kBatch>(i, cnt, every, [&](int u) {
                     float v[V];
                     Vec<T, V>::unpack(b.raw[u], v);
 #pragma unroll
@@ -134,7 +154,7 @@ __global__ __launch_bounds__(512) void gn_stats_kernel(NormArgs a, int TX, int R
                         s[j] += d;
                         ss[j] = fmaf(d, d, ss[j]);
                     }
-                }
+                });
             }
             const float inv = cnt > 0 ? 1.0f / cnt : 0.0f;
 #pragma unroll
@@ -233,11 +253,11 @@ __global__ __launch_bounds__(512) void gn_apply_kernel(NormArgs a, int TX, int R
     const int n = blockIdx.x / chunks, piece = blockIdx.x - n * chunks;
     const int r = threadIdx.x / TX, tx = threadIdx.x - r * TX;
     const int p0 = piece * pix, np = min(pix, a.P - p0);
-    const long long first = (long long)n * a.P + p0 + r;
-    const int cnt = r < R ? row_count(np, R, r) : 0, c0 = tx * V;
+    const long long first = (long long)n * a.P + p0 + min(r, np - 1);
+    const int cnt = r < R ? row_count(np, R, r) : 0, every = np / R, c0 = tx * V;
     const long long xs = (long long)R * a.ldx, ys = (long long)R * a.ldy;
     Batch<T, V, kBatch> b;
-    b.load(static_cast<const T*>(a.x) + first * a.ldx + c0, xs, 0, cnt);
+    b.load(static_cast<const T*>(a.x) + first * a.ldx + c0, xs, 0, cnt, every);
     Affine<T, V> f;
     f.prepare(a, c0);
     combine_stats(part, a, n, chunks, pix, lds);
@@ -248,16 +268,14 @@ __global__ __launch_bounds__(512) void gn_apply_kernel(NormArgs a, int TX, int R
         if (c > c0) f.prepare(a, c);
         finish_affine<Affine<T, V>, V>(f, lds, c, a.C / a.G);
         for (int i = 0; i < cnt; i += kBatch) {
-            if (i > 0 || c > c0) b.load(p, xs, i, cnt);
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                if (i + u >= cnt) break;
+            if (i > 0 || c > c0) b.load(p, xs, i, cnt, every);
+            each<kBatch>(i, cnt, every, [&](int u) {
                 float v[V];
                 Vec<T, V>::unpack(b.raw[u], v);
 #pragma unroll
                 for (int j = 0; j < V; ++j) v[j] = activate<ACT>(f.z(v[j], j));
                 Vec<T, V>::store(q + (i + u) * ys, v);
-            }
+            });
         }
     }
 }
@@ -271,46 +289,41 @@ __global__ __launch_bounds__(256) void gn_quant_kernel(NormArgs a, int LPP, int 
     constexpr int B = 4;
     const int n = blockIdx.x / chunks, piece = blockIdx.x - n * chunks;
     const int sub = threadIdx.x / LPP, l = threadIdx.x - sub * LPP, subs = blockDim.x / LPP;
-    const int p0 = piece * pix, np = min(pix, a.P - p0), c = l * V;
-    const long long first = (long long)n * a.P + p0 + sub;
-    const bool in = c < a.C;
-    const int cnt = row_count(np, subs, sub);
+    const bool in = l * V < a.C;
+    const int p0 = piece * pix, np = min(pix, a.P - p0), c = in ? l * V : 0;
+    const long long first = (long long)n * a.P + p0 + min(sub, np - 1);
+    const int cnt = row_count(np, subs, sub), every = np / subs;
     const T* p = static_cast<const T*>(a.x) + first * a.ldx + c;
     int8_t* q = static_cast<int8_t*>(a.y) + first * a.ldy + c;
     const long long xs = (long long)subs * a.ldx, qs = (long long)subs * a.ldy;
     Batch<T, V, B> b;
-    b.load(p, xs, 0, in ? cnt : 0);
+    b.load(p, xs, 0, cnt, every);
     Affine<T, V> f;
-    if (in) f.prepare(a, c);
+    f.prepare(a, c);
     combine_stats(part, a, n, chunks, pix, lds);
     if (piece == 0) save_stats(a, lds, n);
-    if (in) finish_affine<Affine<T, V>, V>(f, lds, c, a.C / a.G);
+    finish_affine<Affine<T, V>, V>(f, lds, c, a.C / a.G);
     for (int i = 0; i < cnt; i += B) {
-        if (i > 0) b.load(p, xs, i, in ? cnt : 0);
+        if (i > 0) b.load(p, xs, i, cnt, every);
         float v[B][V];
         uint32_t top[B];
 #pragma unroll
-        for (int u = 0; u < B; ++u) {
+        for (int u = 0; u < B; ++u) {   // past the last pixel: not used
             top[u] = 0;
-            if (in && i + u < cnt) {
-                Vec<T, V>::unpack(b.raw[u], v[u]);
+            Vec<T, V>::unpack(b.raw[u], v[u]);
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    v[u][j] = activate<ACT>(f.z(v[u][j], j));
-                    top[u] = max(top[u], __float_as_uint(v[u][j]) & 0x7fffffffu);
-                }
+            for (int j = 0; j < V; ++j) {
+                v[u][j] = activate<ACT>(f.z(v[u][j], j));
+                top[u] = max(top[u], __float_as_uint(v[u][j]) & 0x7fffffffu);
             }
         }
 #pragma unroll
-        for (int u = 0; u < B; ++u) top[u] = lanes_max(top[u], LPP);
-#pragma unroll
-        for (int u = 0; u < B; ++u) {
-            if (i + u < cnt) {
-                const RowScale s = row_scale(top[u]);
-                if (in) store_quantised<V>(q + (i + u) * qs, v[u], s.inv);
-                if (l == 0) a.q_scale[first + (long long)(i + u) * subs] = s.scale;
-            }
-        }
+        for (int u = 0; u < B; ++u) top[u] = lanes_max(in ? top[u] : 0, LPP);
+        each<B>(i, cnt, every, [&](int u) {
+            const RowScale s = row_scale(top[u]);
+            if (in) store_quantised<V>(q + (i + u) * qs, v[u], s.inv);
+            if (l == 0) a.q_scale[first + (long long)(i + u) * subs] = s.scale;
+        });
     }
 }
 
@@ -421,15 +434,15 @@ __global__ __launch_bounds__(512) void gn_bwd_sums_kernel(NormArgs a, int TX, in
     const int r = threadIdx.x / TX, tx = threadIdx.x - r * TX;
     const int p0 = chunk * pix, np = min(pix, a.P - p0);
     if (r < R) {
-        const int cnt = row_count(np, R, r);
-        const long long first = (long long)n * a.P + p0 + r;
+        const int cnt = row_count(np, R, r), every = np / R;
+        const long long first = (long long)n * a.P + p0 + min(r, np - 1);
         const long long xs = (long long)R * a.ldx, ds = (long long)R * a.lddy;
         for (int c = tx * V; c < a.C; c += TX * V) {
             const T* px = static_cast<const T*>(a.x) + first * a.ldx + c;
             const T* pd = static_cast<const T*>(a.dy) + first * a.lddy + c;
             Batch<T, V, kBatchBwd> bx, bd;
-            bx.load(px, xs, 0, cnt);
-            bd.load(pd, ds, 0, cnt);
+            bx.load(px, xs, 0, cnt, every);
+            bd.load(pd, ds, 0, cnt, every);
             Slope<V> f;
             f.load(a, n, c);
             float A[V], B[V];
@@ -437,12 +450,10 @@ __global__ __launch_bounds__(512) void gn_bwd_sums_kernel(NormArgs a, int TX, in
             for (int j = 0; j < V; ++j) A[j] = B[j] = 0.0f;
             for (int i = 0; i < cnt; i += kBatchBwd) {
                 if (i > 0) {
-                    bx.load(px, xs, i, cnt);
-                    bd.load(pd, ds, i, cnt);
+                    bx.load(px, xs, i, cnt, every);
+                    bd.load(pd, ds, i, cnt, every);
                 }
-#pragma unroll
-                for (int u = 0; u < kBatchBwd; ++u) {
-                    if (i + u >= cnt) break;
+                each<kBatchBwd>(i, cnt, every, [&](int u) {
                     float x[V], d[V];
                     Vec<T, V>::unpack(bx.raw[u], x);
                     Vec<T, V>::unpack(bd.raw[u], d);
@@ -452,7 +463,7 @@ __global__ __launch_bounds__(512) void gn_bwd_sums_kernel(NormArgs a, int TX, in
                         A[j] += dz;
                         B[j] = fmaf(dz, xh, B[j]);
                     }
-                }
+                });
             }
 #pragma unroll
             for (int j = 0; j < V; ++j) lds[r * a.C + c + j] = make_float2(A[j], B[j]);
@@ -523,12 +534,12 @@ __global__ __launch_bounds__(512) void gn_bwd_apply_kernel(NormArgs a, int TX, i
     const int cg = a.C / a.G;
     const int r = threadIdx.x / TX, tx = threadIdx.x - r * TX;
     const int p0 = piece * pix, np = min(pix, a.P - p0);
-    const long long first = (long long)n * a.P + p0 + r;
-    const int cnt = r < R ? row_count(np, R, r) : 0, c0 = tx * V;
+    const long long first = (long long)n * a.P + p0 + min(r, np - 1);
+    const int cnt = r < R ? row_count(np, R, r) : 0, every = np / R, c0 = tx * V;
     const long long xs = (long long)R * a.ldx, ds = (long long)R * a.lddy, os = (long long)R * a.ldy;
     Batch<T, V, kBatchBwd> bx, bd;
-    bx.load(static_cast<const T*>(a.x) + first * a.ldx + c0, xs, 0, cnt);
-    bd.load(static_cast<const T*>(a.dy) + first * a.lddy + c0, ds, 0, cnt);
+    bx.load(static_cast<const T*>(a.x) + first * a.ldx + c0, xs, 0, cnt, every);
+    bd.load(static_cast<const T*>(a.dy) + first * a.lddy + c0, ds, 0, cnt, every);
     Slope<V> f;
     f.load(a, n, c0);
     {
@@ -537,11 +548,15 @@ __global__ __launch_bounds__(512) void gn_bwd_apply_kernel(NormArgs a, int TX, i
         for (int g = threadIdx.x / L; g < a.G; g += blockDim.x / L) {
             const float2* p = pg + (long long)n * chunks * a.G + g;
             float s = 0.0f, t = 0.0f;
-#pragma unroll 4
-            for (int j = lane; j < chunks; j += L) {
-                const float2 e = p[(long long)j * a.G];
-                s += e.x;
-                t += e.y;
+            for (int j0 = lane; j0 < chunks; j0 += 8 * L) {
+                float2 e[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) e[u] = p[(long long)min(j0 + u * L, chunks - 1) * a.G];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    s += j0 + u * L < chunks ? e[u].x : 0.0f;
+                    t += j0 + u * L < chunks ? e[u].y : 0.0f;
+                }
             }
             s = lanes_sum(s, L);
             t = lanes_sum(t, L);
@@ -566,12 +581,10 @@ __global__ __launch_bounds__(512) void gn_bwd_apply_kernel(NormArgs a, int TX, i
         T* po = static_cast<T*>(a.y) + first * a.ldy + c;
         for (int i = 0; i < cnt; i += kBatchBwd) {
             if (i > 0 || c > c0) {
-                bx.load(px, xs, i, cnt);
-                bd.load(pd, ds, i, cnt);
+                bx.load(px, xs, i, cnt, every);
+                bd.load(pd, ds, i, cnt, every);
             }
-#pragma unroll
-            for (int u = 0; u < kBatchBwd; ++u) {
-                if (i + u >= cnt) break;
+            each<kBatchBwd>(i, cnt, every, [&](int u) {
                 float x[V], d[V];
                 Vec<T, V>::unpack(bx.raw[u], x);
                 Vec<T, V>::unpack(bd.raw[u], d);
@@ -581,7 +594,7 @@ __global__ __launch_bounds__(512) void gn_bwd_apply_kernel(NormArgs a, int TX, i
                     d[j] = fmaf(dz, f.rstd[j] * f.gamma[j], -fmaf(xh, s2[j], s1[j]));
                 }
                 Vec<T, V>::store(po + (i + u) * os, d);
-            }
+            });
         }
     }
 }
@@ -613,31 +626,27 @@ __global__ __launch_bounds__(1024) void gn_resident_kernel(NormArgs a, int TX, i
     __shared__ float lds[3][32];
     const int b = xcd_tile_index(), n = b / a.G, g = b - n * a.G, cg = a.C / a.G;
     const int r = threadIdx.x / TX, tx = threadIdx.x - r * TX, c = g * cg + tx * V;
-    const long long first = (long long)n * a.P + r;
-    const int cnt = r < R ? row_count(a.P, R, r) : 0;
+    const long long first = (long long)n * a.P + min(r, a.P - 1);
+    const int cnt = r < R ? row_count(a.P, R, r) : 0, every = a.P / R;
     Batch<T, V, NV> x;
-    x.load(static_cast<const T*>(a.x) + first * a.ldx + c, (long long)R * a.ldx, 0, cnt);
+    x.load(static_cast<const T*>(a.x) + first * a.ldx + c, (long long)R * a.ldx, 0, cnt, every);
     Affine<T, V> f;
     f.prepare(a, c);
     float s = 0.0f;
-#pragma unroll
-    for (int u = 0; u < NV; ++u) {
-        if (u >= cnt) break;
+    each<NV>(0, cnt, every, [&](int u) {
         float v[V];
         Vec<T, V>::unpack(x.raw[u], v);
 #pragma unroll
         for (int j = 0; j < V; ++j) s += v[j];
-    }
+    });
     const float m = (float)a.P * cg, mean = block_sum(s, 0.0f, lds[0]).x / m;
     s = 0.0f;
-#pragma unroll
-    for (int u = 0; u < NV; ++u) {
-        if (u >= cnt) break;
+    each<NV>(0, cnt, every, [&](int u) {
         float v[V];
         Vec<T, V>::unpack(x.raw[u], v);
 #pragma unroll
         for (int j = 0; j < V; ++j) s = fmaf(v[j] - mean, v[j] - mean, s);
-    }
+    });
     const float rstd = 1.0f / sqrtf(block_sum(s, 0.0f, lds[1]).x / m + a.eps);
     if (threadIdx.x == 0) {
         if (a.mean) a.mean[b] = mean;
@@ -647,15 +656,13 @@ __global__ __launch_bounds__(1024) void gn_resident_kernel(NormArgs a, int TX, i
     for (int j = 0; j < V; ++j) f.finish(mean, rstd, j);
     T* q = static_cast<T*>(a.y) + first * a.ldy + c;
     const long long ys = (long long)R * a.ldy;
-#pragma unroll
-    for (int u = 0; u < NV; ++u) {
-        if (u >= cnt) break;
+    each<NV>(0, cnt, every, [&](int u) {
         float v[V];
         Vec<T, V>::unpack(x.raw[u], v);
 #pragma unroll
         for (int j = 0; j < V; ++j) v[j] = activate<ACT>(f.z(v[j], j));
         Vec<T, V>::store(q + u * ys, v);
-    }
+    });
 }
 
 // Backward: the same, with the channels' sums of this image to pc
@@ -667,19 +674,17 @@ __global__ __launch_bounds__(1024) void gn_bwd_resident_kernel(NormArgs a, int T
     __shared__ float lds[32];
     const int b = xcd_tile_index(), n = b / a.G, g = b - n * a.G, cg = a.C / a.G;
     const int r = threadIdx.x / TX, tx = threadIdx.x - r * TX, c = g * cg + tx * V;
-    const long long first = (long long)n * a.P + r;
-    const int cnt = r < R ? row_count(a.P, R, r) : 0;
+    const long long first = (long long)n * a.P + min(r, a.P - 1);
+    const int cnt = r < R ? row_count(a.P, R, r) : 0, every = a.P / R;
     Batch<T, V, NV> bx, bd;
-    bx.load(static_cast<const T*>(a.x) + first * a.ldx + c, (long long)R * a.ldx, 0, cnt);
-    bd.load(static_cast<const T*>(a.dy) + first * a.lddy + c, (long long)R * a.lddy, 0, cnt);
+    bx.load(static_cast<const T*>(a.x) + first * a.ldx + c, (long long)R * a.ldx, 0, cnt, every);
+    bd.load(static_cast<const T*>(a.dy) + first * a.lddy + c, (long long)R * a.lddy, 0, cnt, every);
     Slope<V, true> f;
     f.load(a, n, c);
     float A[V], B[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) A[j] = B[j] = 0.0f;
-#pragma unroll
-    for (int u = 0; u < NV; ++u) {
-        if (u >= cnt) break;
+    each<NV>(0, cnt, every, [&](int u) {
         float x[V], d[V];
         Vec<T, V>::unpack(bx.raw[u], x);
         Vec<T, V>::unpack(bd.raw[u], d);
@@ -689,7 +694,7 @@ __global__ __launch_bounds__(1024) void gn_bwd_resident_kernel(NormArgs a, int T
             A[j] += dz;
             B[j] = fmaf(dz, xh, B[j]);
         }
-    }
+    });
     float s = 0.0f, t = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -701,9 +706,7 @@ __global__ __launch_bounds__(1024) void gn_bwd_resident_kernel(NormArgs a, int T
     const float m = (float)a.P * cg, s1 = sum.x / m * f.rstd[0], s2 = sum.y / m * f.rstd[0];
     T* po = static_cast<T*>(a.y) + first * a.ldy + c;
     const long long os = (long long)R * a.ldy;
-#pragma unroll
-    for (int u = 0; u < NV; ++u) {
-        if (u >= cnt) break;
+    each<NV>(0, cnt, every, [&](int u) {
         float x[V], d[V];
         Vec<T, V>::unpack(bx.raw[u], x);
         Vec<T, V>::unpack(bd.raw[u], d);
@@ -713,7 +716,7 @@ __global__ __launch_bounds__(1024) void gn_bwd_resident_kernel(NormArgs a, int T
             d[j] = fmaf(dz, f.rstd[0] * f.gamma[j], -fmaf(xh, s2, s1));
         }
         Vec<T, V>::store(po + u * os, d);
-    }
+    });
     if (!a.dgamma && !a.dbeta) return;
     sum_rows(rows, R, cg);
     for (int k = threadIdx.x; k < cg; k += blockDim.x) {
@@ -777,7 +780,8 @@ Plan make_plan(int N, int P, int C, int V) {
 }
 
 // The resident form: threads and the vectors of each, or nv = 0 where the
-// group does not fit (most: the largest nv) or is not worth it.  Each
+// group does not fit (most: the largest nv that leaves 1024 threads their
+// registers) or is not worth it.  Each
 // workgroup reads C/G channels of every pixel: below 64 bytes that splits the
 // memory's lines over several workgroups, which costs more than the second
 // read once the tensor is large.
@@ -798,9 +802,8 @@ Resident make_resident(const NormArgs& a, int V, int elem, int most) {
     for (p.block = 256; p.block <= 1024; p.block *= 2) {
         p.R = p.block / p.TX;
         const long long nv = (a.P + (long long)p.R - 1) / p.R;
-        const int limit = p.block == 1024 ? most : 4;
-        if (nv <= limit) {
-            p.nv = nv <= 2 ? 2 : nv <= 4 ? 4 : most <= 6 || nv <= 8 ? (most <= 6 ? 6 : 8) : 16;
+        if (nv <= (p.block == 1024 ? most : 4)) {
+            p.nv = nv <= 2 ? 2 : nv <= 4 ? 4 : 8;
             return p;
         }
     }
@@ -809,7 +812,7 @@ Resident make_resident(const NormArgs& a, int V, int elem, int most) {
 
 template <typename T, int V, int ACT> hipError_t forward_resident(const NormArgs& a, const Resident& p, hipStream_t st) {
     auto k = p.nv == 2 ? gn_resident_kernel<T, V, ACT, 2> : p.nv == 4 ? gn_resident_kernel<T, V, ACT, 4>
-             : p.nv == 8 ? gn_resident_kernel<T, V, ACT, 8> : gn_resident_kernel<T, V, ACT, 16>;
+                         : gn_resident_kernel<T, V, ACT, 8>;
     k<<<a.N * a.G, p.block, 0, st>>>(a, p.TX, p.R);
     return hipGetLastError();
 }
@@ -866,8 +869,7 @@ template <typename T, int V, int ACT> hipError_t backward_resident(const NormArg
         return e;
     };
     const hipError_t e = p.nv == 2 ? run([] { return gn_bwd_resident_kernel<T, V, ACT, 2>; })
-                         : p.nv == 4 ? run([] { return gn_bwd_resident_kernel<T, V, ACT, 4>; })
-                                     : run([] { return gn_bwd_resident_kernel<T, V, ACT, 6>; });
+                                    : run([] { return gn_bwd_resident_kernel<T, V, ACT, 4>; });
     if (e != hipSuccess) return e;
     if (a.N > 1 && (a.dgamma || a.dbeta))
         gn_params_kernel<<<(a.C + kParamChannels - 1) / kParamChannels, 256, 0, st>>>(a, pc);
@@ -941,7 +943,7 @@ static hipError_t backward_group(const NormArgs& a, int act, const Resident& p, 
 
 hipError_t launch_group_norm(const NormArgs& a, int act, void* ws, hipStream_t st) {
     const int elem = a.dtype == 0 ? 4 : 2, cg = a.C / a.G;
-    const Resident p = make_resident(a, vector_width(a, cg, elem, elem), elem, 16);
+    const Resident p = make_resident(a, vector_width(a, cg, elem, elem), elem, 8);
     if (p.nv) {
         CONV2D_NORM_WIDTH(forward_group, cg, 0, a, act, p, st);
     }
@@ -954,7 +956,7 @@ hipError_t launch_group_norm_quant(const NormArgs& a, int act, void* ws, hipStre
 
 hipError_t launch_group_norm_bwd(const NormArgs& a, int act, void* ws, hipStream_t st) {
     const int elem = a.dtype == 0 ? 4 : 2, cg = a.C / a.G;
-    const Resident p = make_resident(a, vector_width(a, cg, elem, elem), elem, 6);
+    const Resident p = make_resident(a, vector_width(a, cg, elem, elem), elem, 4);
     if (p.nv) {
         CONV2D_NORM_WIDTH(backward_group, cg, 0, a, act, p, static_cast<float*>(ws), st);
     }
