@@ -42,52 +42,48 @@ namespace conv2d {
 
 namespace {
 
-constexpr int kBatch = 8;       // vector loads in flight per thread (forward)
+constexpr int kBatch = 4;       // vector loads in flight per thread (forward)
 constexpr int kBatchBwd = 4;    // of x and of dy each (backward)
-constexpr int kTargetBlocks = 1024;
+constexpr int kTargetBlocks = 512;
 constexpr int kMaxChunks = 128; // partials that the second launch combines per image
 
-// Values of row r of R in a chunk of np pixels.
-__device__ __forceinline__ int row_count(int np, int R, int r) { return r < np ? (np - r - 1) / R + 1 : 0; }
+// x / d for 0 <= x < 2^20, d > 0: (x + 1/2) / d is at least 1 / 2d away from the
+// next integer, more than the reciprocal's error can move it.  (The kernels are
+// a few KB of code that is fetched anew at every launch, so short code counts
+// for small tensors; an integer division is some 25 instructions.)
+__device__ __forceinline__ int small_div(int x, int d) {
+    return (int)(((float)x + 0.5f) * __builtin_amdgcn_rcpf((float)d));
+}
 
-// Lanes that work on one of `count` things together: a power of two, at most
-// 64, such that the block covers all of them in one go where it can.
+// A thread's part of np pixels that R rows of threads share, thread row r:
+// the pixels r, r + R, ...
+struct Part {
+    int first, cnt;   // first: a pixel inside even if cnt is 0
+    __device__ __forceinline__ Part(int np, int R, int r) {
+        const int every = np / R;
+        cnt = r < R ? every + (r < np - every * R) : 0;
+        first = min(r, np - 1);
+    }
+};
+
+// Threads that work on one of `count` things together: 2^lanes_per of them,
+// at most 64, such that the block covers all of them in one go where it can.
 __device__ __forceinline__ int lanes_per(int count) {
-    int L = 64;
-    while (L > 1 && (int)blockDim.x / L < count) L >>= 1;
-    return L;
+    int lg = 6;
+    while (lg > 0 && (int)(blockDim.x >> lg) < count) --lg;
+    return lg;
 }
 
 // B vectors of a thread, `step` elements apart, from value i of cnt on.  Loads
 // past the end repeat the last value (or the first, where there is none), so
-// that all B are issued together; p is the thread's first value, inside the
-// tensor even if cnt is 0.  `every`: the values that each thread of the
-// workgroup has, the same for all.
+// that all B are issued together.
 template <typename T, int V, int B> struct Batch {
     typename Vec<T, V>::raw raw[B];
-    __device__ __forceinline__ void load(const T* p, long long step, int i, int cnt, int every) {
-        if (i + B <= every) {
+    __device__ __forceinline__ void load(const T* p, long long step, int i, int cnt) {
 #pragma unroll
-            for (int u = 0; u < B; ++u) raw[u] = Vec<T, V>::load(p + (i + u) * step);
-        } else {
-#pragma unroll
-            for (int u = 0; u < B; ++u) raw[u] = Vec<T, V>::load(p + max(min(i + u, cnt - 1), 0) * step);
-        }
+        for (int u = 0; u < B; ++u) raw[u] = Vec<T, V>::load(p + max(min(i + u, cnt - 1), 0) * step);
     }
 };
-
-// f(u) for the values i + u < cnt of a batch, without the comparisons where
-// every thread has them all.
-template <int B, typename F> __device__ __forceinline__ void each(int i, int cnt, int every, F&& f) {
-    if (i + B <= every) {
-#pragma unroll
-        for (int u = 0; u < B; ++u) f(u);
-    } else {
-#pragma unroll
-        for (int u = 0; u < B; ++u)
-            if (i + u < cnt) f(u);
-    }
-}
 
 // Combines an image's chunk partials (mean, M2) into mean and rstd in LDS, in
 // one pass: with d = mean_i - mean_0, M2 = sum(M2_i) + sum(n d^2) - sum(n d)^2 / N.
@@ -95,19 +91,19 @@ template <int B, typename F> __device__ __forceinline__ void each(int i, int cnt
 // cancellation by the number of chunks.
 __device__ __forceinline__ void combine_stats(const float2* part, const NormArgs& a, int n, int chunks, int pix,
                                               float2* stat) {
-    const int cg = a.C / a.G, L = lanes_per(a.G), lane = threadIdx.x % L;
+    const int cg = a.C / a.G, lg = lanes_per(a.G), L = 1 << lg, lane = threadIdx.x & (L - 1);
     const float last = (float)(a.P - (chunks - 1) * pix) * cg, full = (float)pix * cg;
     const float total = (float)a.P * cg;
-    for (int g = threadIdx.x / L; g < a.G; g += blockDim.x / L) {
+    for (int g = threadIdx.x >> lg; g < a.G; g += blockDim.x >> lg) {
         const float2* p = part + (long long)n * chunks * a.G + g;
         const float base = p[0].x;
         float s = 0.0f, ss = 0.0f;
-        for (int j0 = lane; j0 < chunks; j0 += 8 * L) {
-            float2 e[8];
+        for (int j0 = lane; j0 < chunks; j0 += 4 * L) {
+            float2 e[4];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) e[u] = p[(long long)min(j0 + u * L, chunks - 1) * a.G];
+            for (int u = 0; u < 4; ++u) e[u] = p[(long long)min(j0 + u * L, chunks - 1) * a.G];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
+            for (int u = 0; u < 4; ++u) {
                 const int j = j0 + u * L;
                 const float w = j >= chunks ? 0.0f : j == chunks - 1 ? last : full, d = e[u].x - base;
                 s = fmaf(w, d, s);
@@ -129,32 +125,35 @@ template <typename T, int V>
 __global__ __launch_bounds__(512) void gn_stats_kernel(NormArgs a, int TX, int R, int chunks, int pix, float2* part) {
     extern __shared__ float2 lds[];
     const int n = blockIdx.x / chunks, chunk = blockIdx.x - n * chunks;
-    const int r = threadIdx.x / TX, tx = threadIdx.x - r * TX;
+    const int r = small_div(threadIdx.x, TX), tx = threadIdx.x - r * TX;
     const int p0 = chunk * pix, np = min(pix, a.P - p0);
     const long long step = (long long)R * a.ldx;
-    const int every = np / R;
+    const Part part_of(np, R, r);
+    const int cnt = part_of.cnt;
     if (r < R) {
-        const int cnt = row_count(np, R, r);
         for (int c = tx * V; c < a.C; c += TX * V) {
-            const T* p = static_cast<const T*>(a.x) + ((long long)n * a.P + p0 + min(r, np - 1)) * a.ldx + c;
+            const T* p = static_cast<const T*>(a.x) + ((long long)n * a.P + p0 + part_of.first) * a.ldx + c;
             Batch<T, V, kBatch> b;
-            b.load(p, step, 0, cnt, every);
+            b.load(p, step, 0, cnt);
+            const typename Vec<T, V>::raw k_raw = b.raw[0];
             float k[V], s[V], ss[V];
-            Vec<T, V>::unpack(b.raw[0], k);
+            Vec<T, V>::unpack(k_raw, k);
 #pragma unroll
             for (int j = 0; j < V; ++j) s[j] = ss[j] = 0.0f;
+#pragma clang loop unroll(disable)
             for (int i = 0; i < cnt; i += kBatch) {
-                if (i > 0) b.load(p, step, i, cnt, every);
-                each<kBatch>(i, cnt, every, [&](int u) {
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
                     float v[V];
-                    Vec<T, V>::unpack(b.raw[u], v);
+                    Vec<T, V>::unpack(i + u < cnt ? b.raw[u] : k_raw, v);   // past the end: adds nothing
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
                         const float d = v[j] - k[j];
                         s[j] += d;
                         ss[j] = fmaf(d, d, ss[j]);
                     }
-                });
+                }
+                b.load(p, step, i + kBatch, cnt);
             }
             const float inv = cnt > 0 ? 1.0f / cnt : 0.0f;
 #pragma unroll
@@ -165,26 +164,30 @@ __global__ __launch_bounds__(512) void gn_stats_kernel(NormArgs a, int TX, int R
         }
     }
     __syncthreads();
-    // a group's R x C/G entries, by `row` and channel; a row's entries all
-    // count row_count values
-    const int cg = a.C / a.G, L = lanes_per(a.G), lane = threadIdx.x % L;
-    const int few = np / R, more = np - few * R;   // rows below `more` have one value more
-    for (int g = threadIdx.x / L; g < a.G; g += blockDim.x / L) {
+    // a group's R x C/G entries, merged in one pass as in combine_stats: row
+    // `row` of the threads has one value more below `more`
+    const int cg = a.C / a.G, lg = lanes_per(a.G), L = 1 << lg, lane = threadIdx.x & (L - 1);
+    const int few = np / R, more = np - few * R, count = R * cg;
+    for (int g = threadIdx.x >> lg; g < a.G; g += blockDim.x >> lg) {
         const float2* e = lds + g * cg;
-        float s = 0.0f;
-        for (int k = lane, row = lane / cg, c = lane - row * cg; k < R * cg; k += L) {
-            s += (few + (row < more)) * e[row * a.C + c].x;
-            for (c += L; c >= cg; c -= cg) ++row;
+        const float base = e[0].x;
+        float s = 0.0f, ss = 0.0f;
+        for (int k0 = lane; k0 < count; k0 += 4 * L) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int k = min(k0 + u * L, count - 1), row = small_div(k, cg);
+                const float2 v = e[row * a.C + k - row * cg];
+                const int w = k0 + u * L < count ? few + (row < more) : 0;   // rows without values hold (0, 0)
+                const float d = v.x - base;
+                s = fmaf((float)w, d, s);
+                ss += w ? fmaf(w * d, d, v.y) : 0.0f;
+            }
         }
-        const float mean = lanes_sum(s, L) / ((float)np * cg);
-        float m2 = 0.0f;
-        for (int k = lane, row = lane / cg, c = lane - row * cg; k < R * cg; k += L) {
-            const float2 v = e[row * a.C + c];
-            const float d = v.x - mean;
-            m2 += v.y + (few + (row < more)) * d * d;
-            for (c += L; c >= cg; c -= cg) ++row;
-        }
-        m2 = lanes_sum(m2, L);
+        s = lanes_sum(s, L);
+        ss = lanes_sum(ss, L);
+        const float shift = s / ((float)np * cg), mean = base + shift;
+        float m2 = ss - s * shift;
+        m2 = m2 < 0.0f ? 0.0f : m2;   // a NaN stays
         if (lane == 0) part[(long long)blockIdx.x * a.G + g] = make_float2(mean, m2);
     }
 }
@@ -226,7 +229,7 @@ template <int V> struct Affine<bf16_t, V> {
 };
 // the same from the groups' (mean, rstd)
 template <typename A, int V> __device__ __forceinline__ void finish_affine(A& f, const float2* stat, int c, int cg) {
-    int g = c / cg, left = (g + 1) * cg - c;   // channels of group g from c on
+    int g = small_div(c, cg), left = (g + 1) * cg - c;   // channels of group g from c on
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         if (left == 0) ++g, left = cg;
@@ -251,60 +254,71 @@ __global__ __launch_bounds__(512) void gn_apply_kernel(NormArgs a, int TX, int R
                                                        const float2* part) {
     extern __shared__ float2 lds[];
     const int n = blockIdx.x / chunks, piece = blockIdx.x - n * chunks;
-    const int r = threadIdx.x / TX, tx = threadIdx.x - r * TX;
+    const int r = small_div(threadIdx.x, TX), tx = threadIdx.x - r * TX;
     const int p0 = piece * pix, np = min(pix, a.P - p0);
-    const long long first = (long long)n * a.P + p0 + min(r, np - 1);
-    const int cnt = r < R ? row_count(np, R, r) : 0, every = np / R, c0 = tx * V;
+    const Part part_of(np, R, r);
+    const long long first = (long long)n * a.P + p0 + part_of.first;
+    const int cnt = part_of.cnt, c0 = tx * V;
     const long long xs = (long long)R * a.ldx, ys = (long long)R * a.ldy;
     Batch<T, V, kBatch> b;
-    b.load(static_cast<const T*>(a.x) + first * a.ldx + c0, xs, 0, cnt, every);
+    b.load(static_cast<const T*>(a.x) + first * a.ldx + c0, xs, 0, cnt);
     Affine<T, V> f;
     f.prepare(a, c0);
     combine_stats(part, a, n, chunks, pix, lds);
     if (piece == 0) save_stats(a, lds, n);
-    for (int c = c0; c < a.C; c += TX * V) {
-        const T* p = static_cast<const T*>(a.x) + first * a.ldx + c;
-        T* q = static_cast<T*>(a.y) + first * a.ldy + c;
-        if (c > c0) f.prepare(a, c);
-        finish_affine<Affine<T, V>, V>(f, lds, c, a.C / a.G);
-        for (int i = 0; i < cnt; i += kBatch) {
-            if (i > 0 || c > c0) b.load(p, xs, i, cnt, every);
-            each<kBatch>(i, cnt, every, [&](int u) {
-                float v[V];
-                Vec<T, V>::unpack(b.raw[u], v);
+    const T* p = static_cast<const T*>(a.x) + first * a.ldx + c0;
+    T* q = static_cast<T*>(a.y) + first * a.ldy + c0;
+    finish_affine<Affine<T, V>, V>(f, lds, c0, a.C / a.G);
+#pragma clang loop unroll(disable)
+    for (int c = c0, i = 0; c < a.C && cnt > 0;) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) v[j] = activate<ACT>(f.z(v[j], j));
-                Vec<T, V>::store(q + (i + u) * ys, v);
-            });
+        for (int u = 0; u < kBatch; ++u) {
+            float v[V];
+            Vec<T, V>::unpack(b.raw[u], v);
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[j] = activate<ACT>(f.z(v[j], j));
+            if (i + u < cnt) Vec<T, V>::store(q + (i + u) * ys, v);
         }
+        i += kBatch;
+        if (i >= cnt) {   // more than blockDim.x vectors across: the next channels
+            c += TX * V;
+            if (c >= a.C) break;
+            i = 0;
+            p += TX * V;
+            q += TX * V;
+            f.prepare(a, c);
+            finish_affine<Affine<T, V>, V>(f, lds, c, a.C / a.G);
+        }
+        b.load(p, xs, i, cnt);
     }
 }
 
 // Second launch of the quantised forward pass.  LPP lanes (a power of two)
 // share a pixel, lane l holds the vectors l, l + LPP, ... of it.  LDS: G pairs.
-// One vector a lane: four pixels at a time, constants in registers.
+// One vector a lane: two pixels at a time, constants in registers.
 template <typename T, int V, int ACT>
 __global__ __launch_bounds__(256) void gn_quant_kernel(NormArgs a, int LPP, int chunks, int pix, const float2* part) {
     extern __shared__ float2 lds[];
-    constexpr int B = 4;
+    constexpr int B = 2;
     const int n = blockIdx.x / chunks, piece = blockIdx.x - n * chunks;
-    const int sub = threadIdx.x / LPP, l = threadIdx.x - sub * LPP, subs = blockDim.x / LPP;
+    const int sub = small_div(threadIdx.x, LPP), l = threadIdx.x - sub * LPP, subs = small_div(blockDim.x, LPP);
     const bool in = l * V < a.C;
     const int p0 = piece * pix, np = min(pix, a.P - p0), c = in ? l * V : 0;
-    const long long first = (long long)n * a.P + p0 + min(sub, np - 1);
-    const int cnt = row_count(np, subs, sub), every = np / subs;
+    const Part part_of(np, subs, sub);
+    const long long first = (long long)n * a.P + p0 + part_of.first;
+    const int cnt = part_of.cnt;
     const T* p = static_cast<const T*>(a.x) + first * a.ldx + c;
     int8_t* q = static_cast<int8_t*>(a.y) + first * a.ldy + c;
     const long long xs = (long long)subs * a.ldx, qs = (long long)subs * a.ldy;
     Batch<T, V, B> b;
-    b.load(p, xs, 0, cnt, every);
+    b.load(p, xs, 0, cnt);
     Affine<T, V> f;
     f.prepare(a, c);
     combine_stats(part, a, n, chunks, pix, lds);
     if (piece == 0) save_stats(a, lds, n);
     finish_affine<Affine<T, V>, V>(f, lds, c, a.C / a.G);
+#pragma clang loop unroll(disable)
     for (int i = 0; i < cnt; i += B) {
-        if (i > 0) b.load(p, xs, i, cnt, every);
         float v[B][V];
         uint32_t top[B];
 #pragma unroll
@@ -317,13 +331,17 @@ __global__ __launch_bounds__(256) void gn_quant_kernel(NormArgs a, int LPP, int 
                 top[u] = max(top[u], __float_as_uint(v[u][j]) & 0x7fffffffu);
             }
         }
+        b.load(p, xs, i + B, cnt);
 #pragma unroll
         for (int u = 0; u < B; ++u) top[u] = lanes_max(in ? top[u] : 0, LPP);
-        each<B>(i, cnt, every, [&](int u) {
+#pragma unroll
+        for (int u = 0; u < B; ++u) {
             const RowScale s = row_scale(top[u]);
-            if (in) store_quantised<V>(q + (i + u) * qs, v[u], s.inv);
-            if (l == 0) a.q_scale[first + (long long)(i + u) * subs] = s.scale;
-        });
+            if (i + u < cnt) {
+                if (in) store_quantised<V>(q + (i + u) * qs, v[u], s.inv);
+                if (l == 0) a.q_scale[first + (long long)(i + u) * subs] = s.scale;
+            }
+        }
     }
 }
 
@@ -383,7 +401,7 @@ template <int V, bool ONE = false> struct Slope {
     static constexpr __device__ __forceinline__ int at(int j) { return ONE ? 0 : j; }
     __device__ __forceinline__ void load(const NormArgs& a, int n, int c) {
         const int cg = a.C / a.G;
-        int g = c / cg, left = (g + 1) * cg - c;
+        int g = small_div(c, cg), left = (g + 1) * cg - c;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             if (left == 0) ++g, left = cg;
@@ -409,8 +427,8 @@ template <int V, bool ONE = false> struct Slope {
 // Sums of a workgroup's channels over its R rows of threads (pairs in LDS:
 // R * cols) into row 0, L lanes to a channel.
 __device__ __forceinline__ void sum_rows(float2* lds, int R, int cols) {
-    const int L = lanes_per(cols), lane = threadIdx.x % L;
-    for (int c = threadIdx.x / L; c < cols; c += blockDim.x / L) {
+    const int lg = lanes_per(cols), L = 1 << lg, lane = threadIdx.x & (L - 1);
+    for (int c = threadIdx.x >> lg; c < cols; c += blockDim.x >> lg) {
         float s = 0.0f, t = 0.0f;
         for (int k = lane; k < R; k += L) {
             s += lds[k * cols + c].x;
@@ -431,39 +449,40 @@ __global__ __launch_bounds__(512) void gn_bwd_sums_kernel(NormArgs a, int TX, in
                                                           float2* pg) {
     extern __shared__ float2 lds[];
     const int n = blockIdx.x / chunks, chunk = blockIdx.x - n * chunks;
-    const int r = threadIdx.x / TX, tx = threadIdx.x - r * TX;
+    const int r = small_div(threadIdx.x, TX), tx = threadIdx.x - r * TX;
     const int p0 = chunk * pix, np = min(pix, a.P - p0);
     if (r < R) {
-        const int cnt = row_count(np, R, r), every = np / R;
-        const long long first = (long long)n * a.P + p0 + min(r, np - 1);
+        const Part part_of(np, R, r);
+        const long long first = (long long)n * a.P + p0 + part_of.first;
+        const int cnt = part_of.cnt;
         const long long xs = (long long)R * a.ldx, ds = (long long)R * a.lddy;
         for (int c = tx * V; c < a.C; c += TX * V) {
             const T* px = static_cast<const T*>(a.x) + first * a.ldx + c;
             const T* pd = static_cast<const T*>(a.dy) + first * a.lddy + c;
             Batch<T, V, kBatchBwd> bx, bd;
-            bx.load(px, xs, 0, cnt, every);
-            bd.load(pd, ds, 0, cnt, every);
+            bx.load(px, xs, 0, cnt);
+            bd.load(pd, ds, 0, cnt);
             Slope<V> f;
             f.load(a, n, c);
             float A[V], B[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) A[j] = B[j] = 0.0f;
+#pragma clang loop unroll(disable)
             for (int i = 0; i < cnt; i += kBatchBwd) {
-                if (i > 0) {
-                    bx.load(px, xs, i, cnt, every);
-                    bd.load(pd, ds, i, cnt, every);
-                }
-                each<kBatchBwd>(i, cnt, every, [&](int u) {
+#pragma unroll
+                for (int u = 0; u < kBatchBwd; ++u) {
                     float x[V], d[V];
                     Vec<T, V>::unpack(bx.raw[u], x);
                     Vec<T, V>::unpack(bd.raw[u], d);
 #pragma unroll
                     for (int j = 0; j < V; ++j) {
                         const float xh = f.xh(x[j], j), dz = f.template dz<ACT>(d[j], xh, j);
-                        A[j] += dz;
-                        B[j] = fmaf(dz, xh, B[j]);
+                        A[j] += i + u < cnt ? dz : 0.0f;
+                        B[j] = i + u < cnt ? fmaf(dz, xh, B[j]) : B[j];
                     }
-                });
+                }
+                bx.load(px, xs, i + kBatchBwd, cnt);
+                bd.load(pd, ds, i + kBatchBwd, cnt);
             }
 #pragma unroll
             for (int j = 0; j < V; ++j) lds[r * a.C + c + j] = make_float2(A[j], B[j]);
@@ -476,8 +495,8 @@ __global__ __launch_bounds__(512) void gn_bwd_sums_kernel(NormArgs a, int TX, in
         out[c] = lds[c].x;
         out[a.C + c] = lds[c].y;
     }
-    const int cg = a.C / a.G, L = lanes_per(a.G), lane = threadIdx.x % L;
-    for (int g = threadIdx.x / L; g < a.G; g += blockDim.x / L) {
+    const int cg = a.C / a.G, lg = lanes_per(a.G), L = 1 << lg, lane = threadIdx.x & (L - 1);
+    for (int g = threadIdx.x >> lg; g < a.G; g += blockDim.x >> lg) {
         float s = 0.0f, t = 0.0f;
         for (int c = g * cg + lane; c < (g + 1) * cg; c += L) {
             const float w = a.gamma ? a.gamma[c] : 1.0f;
@@ -532,28 +551,29 @@ __global__ __launch_bounds__(512) void gn_bwd_apply_kernel(NormArgs a, int TX, i
     const int b = blockIdx.x - sums;
     const int n = b / chunks, piece = b - n * chunks;
     const int cg = a.C / a.G;
-    const int r = threadIdx.x / TX, tx = threadIdx.x - r * TX;
+    const int r = small_div(threadIdx.x, TX), tx = threadIdx.x - r * TX;
     const int p0 = piece * pix, np = min(pix, a.P - p0);
-    const long long first = (long long)n * a.P + p0 + min(r, np - 1);
-    const int cnt = r < R ? row_count(np, R, r) : 0, every = np / R, c0 = tx * V;
+    const Part part_of(np, R, r);
+    const long long first = (long long)n * a.P + p0 + part_of.first;
+    const int cnt = part_of.cnt, c0 = tx * V;
     const long long xs = (long long)R * a.ldx, ds = (long long)R * a.lddy, os = (long long)R * a.ldy;
     Batch<T, V, kBatchBwd> bx, bd;
-    bx.load(static_cast<const T*>(a.x) + first * a.ldx + c0, xs, 0, cnt, every);
-    bd.load(static_cast<const T*>(a.dy) + first * a.lddy + c0, ds, 0, cnt, every);
+    bx.load(static_cast<const T*>(a.x) + first * a.ldx + c0, xs, 0, cnt);
+    bd.load(static_cast<const T*>(a.dy) + first * a.lddy + c0, ds, 0, cnt);
     Slope<V> f;
     f.load(a, n, c0);
     {
-        const int L = lanes_per(a.G), lane = threadIdx.x % L;
+        const int lg = lanes_per(a.G), L = 1 << lg, lane = threadIdx.x & (L - 1);
         const float inv = 1.0f / ((float)a.P * cg);
-        for (int g = threadIdx.x / L; g < a.G; g += blockDim.x / L) {
+        for (int g = threadIdx.x >> lg; g < a.G; g += blockDim.x >> lg) {
             const float2* p = pg + (long long)n * chunks * a.G + g;
             float s = 0.0f, t = 0.0f;
-            for (int j0 = lane; j0 < chunks; j0 += 8 * L) {
-                float2 e[8];
+            for (int j0 = lane; j0 < chunks; j0 += 4 * L) {
+                float2 e[4];
 #pragma unroll
-                for (int u = 0; u < 8; ++u) e[u] = p[(long long)min(j0 + u * L, chunks - 1) * a.G];
+                for (int u = 0; u < 4; ++u) e[u] = p[(long long)min(j0 + u * L, chunks - 1) * a.G];
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
+                for (int u = 0; u < 4; ++u) {
                     s += j0 + u * L < chunks ? e[u].x : 0.0f;
                     t += j0 + u * L < chunks ? e[u].y : 0.0f;
                 }
@@ -564,10 +584,12 @@ __global__ __launch_bounds__(512) void gn_bwd_apply_kernel(NormArgs a, int TX, i
         }
         __syncthreads();
     }
-    for (int c = c0; c < a.C; c += TX * V) {
-        if (c > c0) f.load(a, n, c);
-        float s1[V], s2[V];   // rstd * s1, rstd * s2
-        int g = c / cg, left = (g + 1) * cg - c;
+    const T* px = static_cast<const T*>(a.x) + first * a.ldx + c0;
+    const T* pd = static_cast<const T*>(a.dy) + first * a.lddy + c0;
+    T* po = static_cast<T*>(a.y) + first * a.ldy + c0;
+    float s1[V], s2[V];   // rstd * s1, rstd * s2
+    auto group_sums = [&](int c) {
+        int g = small_div(c, cg), left = (g + 1) * cg - c;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             if (left == 0) ++g, left = cg;
@@ -576,26 +598,35 @@ __global__ __launch_bounds__(512) void gn_bwd_apply_kernel(NormArgs a, int TX, i
             s1[j] = s.x * f.rstd[j];
             s2[j] = s.y * f.rstd[j];
         }
-        const T* px = static_cast<const T*>(a.x) + first * a.ldx + c;
-        const T* pd = static_cast<const T*>(a.dy) + first * a.lddy + c;
-        T* po = static_cast<T*>(a.y) + first * a.ldy + c;
-        for (int i = 0; i < cnt; i += kBatchBwd) {
-            if (i > 0 || c > c0) {
-                bx.load(px, xs, i, cnt, every);
-                bd.load(pd, ds, i, cnt, every);
-            }
-            each<kBatchBwd>(i, cnt, every, [&](int u) {
-                float x[V], d[V];
-                Vec<T, V>::unpack(bx.raw[u], x);
-                Vec<T, V>::unpack(bd.raw[u], d);
+    };
+    group_sums(c0);
+#pragma clang loop unroll(disable)
+    for (int c = c0, i = 0; c < a.C && cnt > 0;) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float xh = f.xh(x[j], j), dz = f.template dz<ACT>(d[j], xh, j);
-                    d[j] = fmaf(dz, f.rstd[j] * f.gamma[j], -fmaf(xh, s2[j], s1[j]));
-                }
-                Vec<T, V>::store(po + (i + u) * os, d);
-            });
+        for (int u = 0; u < kBatchBwd; ++u) {
+            float x[V], d[V];
+            Vec<T, V>::unpack(bx.raw[u], x);
+            Vec<T, V>::unpack(bd.raw[u], d);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float xh = f.xh(x[j], j), dz = f.template dz<ACT>(d[j], xh, j);
+                d[j] = fmaf(dz, f.rstd[j] * f.gamma[j], -fmaf(xh, s2[j], s1[j]));
+            }
+            if (i + u < cnt) Vec<T, V>::store(po + (i + u) * os, d);
         }
+        i += kBatchBwd;
+        if (i >= cnt) {
+            c += TX * V;
+            if (c >= a.C) break;
+            i = 0;
+            px += TX * V;
+            pd += TX * V;
+            po += TX * V;
+            f.load(a, n, c);
+            group_sums(c);
+        }
+        bx.load(px, xs, i, cnt);
+        bd.load(pd, ds, i, cnt);
     }
 }
 
@@ -625,28 +656,33 @@ template <typename T, int V, int ACT, int NV>
 __global__ __launch_bounds__(1024) void gn_resident_kernel(NormArgs a, int TX, int R) {
     __shared__ float lds[3][32];
     const int b = xcd_tile_index(), n = b / a.G, g = b - n * a.G, cg = a.C / a.G;
-    const int r = threadIdx.x / TX, tx = threadIdx.x - r * TX, c = g * cg + tx * V;
-    const long long first = (long long)n * a.P + min(r, a.P - 1);
-    const int cnt = r < R ? row_count(a.P, R, r) : 0, every = a.P / R;
+    const int r = small_div(threadIdx.x, TX), tx = threadIdx.x - r * TX, c = g * cg + tx * V;
+    const Part part_of(a.P, R, r);
+    const long long first = (long long)n * a.P + part_of.first;
+    const int cnt = part_of.cnt;
     Batch<T, V, NV> x;
-    x.load(static_cast<const T*>(a.x) + first * a.ldx + c, (long long)R * a.ldx, 0, cnt, every);
+    x.load(static_cast<const T*>(a.x) + first * a.ldx + c, (long long)R * a.ldx, 0, cnt);
     Affine<T, V> f;
     f.prepare(a, c);
     float s = 0.0f;
-    each<NV>(0, cnt, every, [&](int u) {
-        float v[V];
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        float v[V], t = 0.0f;
         Vec<T, V>::unpack(x.raw[u], v);
 #pragma unroll
-        for (int j = 0; j < V; ++j) s += v[j];
-    });
+        for (int j = 0; j < V; ++j) t += v[j];
+        s += u < cnt ? t : 0.0f;
+    }
     const float m = (float)a.P * cg, mean = block_sum(s, 0.0f, lds[0]).x / m;
     s = 0.0f;
-    each<NV>(0, cnt, every, [&](int u) {
-        float v[V];
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        float v[V], t = 0.0f;
         Vec<T, V>::unpack(x.raw[u], v);
 #pragma unroll
-        for (int j = 0; j < V; ++j) s = fmaf(v[j] - mean, v[j] - mean, s);
-    });
+        for (int j = 0; j < V; ++j) t = fmaf(v[j] - mean, v[j] - mean, t);
+        s += u < cnt ? t : 0.0f;
+    }
     const float rstd = 1.0f / sqrtf(block_sum(s, 0.0f, lds[1]).x / m + a.eps);
     if (threadIdx.x == 0) {
         if (a.mean) a.mean[b] = mean;
@@ -656,13 +692,14 @@ __global__ __launch_bounds__(1024) void gn_resident_kernel(NormArgs a, int TX, i
     for (int j = 0; j < V; ++j) f.finish(mean, rstd, j);
     T* q = static_cast<T*>(a.y) + first * a.ldy + c;
     const long long ys = (long long)R * a.ldy;
-    each<NV>(0, cnt, every, [&](int u) {
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
         float v[V];
         Vec<T, V>::unpack(x.raw[u], v);
 #pragma unroll
         for (int j = 0; j < V; ++j) v[j] = activate<ACT>(f.z(v[j], j));
-        Vec<T, V>::store(q + u * ys, v);
-    });
+        if (u < cnt) Vec<T, V>::store(q + u * ys, v);
+    }
 }
 
 // Backward: the same, with the channels' sums of this image to pc
@@ -673,28 +710,30 @@ __global__ __launch_bounds__(1024) void gn_bwd_resident_kernel(NormArgs a, int T
     extern __shared__ float2 rows[];
     __shared__ float lds[32];
     const int b = xcd_tile_index(), n = b / a.G, g = b - n * a.G, cg = a.C / a.G;
-    const int r = threadIdx.x / TX, tx = threadIdx.x - r * TX, c = g * cg + tx * V;
-    const long long first = (long long)n * a.P + min(r, a.P - 1);
-    const int cnt = r < R ? row_count(a.P, R, r) : 0, every = a.P / R;
+    const int r = small_div(threadIdx.x, TX), tx = threadIdx.x - r * TX, c = g * cg + tx * V;
+    const Part part_of(a.P, R, r);
+    const long long first = (long long)n * a.P + part_of.first;
+    const int cnt = part_of.cnt;
     Batch<T, V, NV> bx, bd;
-    bx.load(static_cast<const T*>(a.x) + first * a.ldx + c, (long long)R * a.ldx, 0, cnt, every);
-    bd.load(static_cast<const T*>(a.dy) + first * a.lddy + c, (long long)R * a.lddy, 0, cnt, every);
+    bx.load(static_cast<const T*>(a.x) + first * a.ldx + c, (long long)R * a.ldx, 0, cnt);
+    bd.load(static_cast<const T*>(a.dy) + first * a.lddy + c, (long long)R * a.lddy, 0, cnt);
     Slope<V, true> f;
     f.load(a, n, c);
     float A[V], B[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) A[j] = B[j] = 0.0f;
-    each<NV>(0, cnt, every, [&](int u) {
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
         float x[V], d[V];
         Vec<T, V>::unpack(bx.raw[u], x);
         Vec<T, V>::unpack(bd.raw[u], d);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             const float xh = f.xh(x[j], j), dz = f.template dz<ACT>(d[j], xh, j);
-            A[j] += dz;
-            B[j] = fmaf(dz, xh, B[j]);
+            A[j] += u < cnt ? dz : 0.0f;
+            B[j] = u < cnt ? fmaf(dz, xh, B[j]) : B[j];
         }
-    });
+    }
     float s = 0.0f, t = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -706,7 +745,8 @@ __global__ __launch_bounds__(1024) void gn_bwd_resident_kernel(NormArgs a, int T
     const float m = (float)a.P * cg, s1 = sum.x / m * f.rstd[0], s2 = sum.y / m * f.rstd[0];
     T* po = static_cast<T*>(a.y) + first * a.ldy + c;
     const long long os = (long long)R * a.ldy;
-    each<NV>(0, cnt, every, [&](int u) {
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
         float x[V], d[V];
         Vec<T, V>::unpack(bx.raw[u], x);
         Vec<T, V>::unpack(bd.raw[u], d);
@@ -715,8 +755,8 @@ __global__ __launch_bounds__(1024) void gn_bwd_resident_kernel(NormArgs a, int T
             const float xh = f.xh(x[j], j), dz = f.template dz<ACT>(d[j], xh, j);
             d[j] = fmaf(dz, f.rstd[0] * f.gamma[j], -fmaf(xh, s2, s1));
         }
-        Vec<T, V>::store(po + u * os, d);
-    });
+        if (u < cnt) Vec<T, V>::store(po + u * os, d);
+    }
     if (!a.dgamma && !a.dbeta) return;
     sum_rows(rows, R, cg);
     for (int k = threadIdx.x; k < cg; k += blockDim.x) {
