@@ -794,8 +794,9 @@ struct Plan {
 };
 
 // Threads: TX across the channel vectors, R rows of them, the block size of
-// 256 to 512 that leaves the fewest idle.  Chunks: about kTargetBlocks
-// workgroups in all, at most kMaxChunks per image, of whole batches of loads.
+// 256 to 512 that leaves the fewest idle.  Chunks: kTargetBlocks workgroups
+// in all or a few less (two for each compute unit, of equal size: they run at
+// once), at most kMaxChunks per image, of a whole number of pixels a thread.
 Plan make_plan(int N, int P, int C, int V) {
     Plan p;
     const int cv = C / V;
@@ -807,13 +808,10 @@ Plan make_plan(int N, int P, int C, int V) {
         if (used > best) best = used, p.block = b;
     }
     p.R = p.block / p.TX;
-    long long k = (kTargetBlocks + (long long)N - 1) / N;
-    k = k < kMaxChunks ? k : kMaxChunks;
-    // a chunk has at least one vector per thread; more than a batch, and it is
-    // rounded to whole batches
-    const long long batch = (long long)p.R * kBatch;
+    long long k = kTargetBlocks / N;
+    k = k < 1 ? 1 : k < kMaxChunks ? k : kMaxChunks;
     long long each = (P + k - 1) / k;
-    each = each > batch ? (each + batch - 1) / batch * batch : (each + p.R - 1) / p.R * p.R;
+    each = (each + p.R - 1) / p.R * p.R;
     p.pix = (int)(each < 0x7fffffff ? each : 0x7fffffff);
     p.chunks = (int)((P + (long long)p.pix - 1) / p.pix);
     return p;
