@@ -41,7 +41,7 @@ EXPORTS = ("conv2d_fwd", "conv2d_fwd_noalloc", "conv2d_fwd_nhwc_packed", "conv2d
            "conv2d_packed_weight_bytes",
            "conv2d_pack_weights", "conv2d_nchw_to_nhwc", "conv2d_nhwc_to_nchw",
            "conv2d_out_dim", "conv2d_check_args", "conv2d_select_path",
-           "conv2d_set_path_override", "conv2d_set_grid_limit", "conv2d_release_scratch", "conv2d_strerror",
+           "conv2d_set_path_override", "conv2d_set_grid_limit", "conv2d_set_wait_limit", "conv2d_release_scratch", "conv2d_strerror",
            "conv2d_last_error")
 
 
@@ -107,6 +107,7 @@ def _load() -> ctypes.CDLL:
     lib.conv2d_select_path.argtypes, lib.conv2d_select_path.restype = [I] * 12, I
     lib.conv2d_set_path_override.argtypes, lib.conv2d_set_path_override.restype = [I], I
     lib.conv2d_set_grid_limit.argtypes, lib.conv2d_set_grid_limit.restype = [I], I
+    lib.conv2d_set_wait_limit.argtypes, lib.conv2d_set_wait_limit.restype = [I], I
     lib.conv2d_release_scratch.argtypes, lib.conv2d_release_scratch.restype = [], None
     lib.conv2d_strerror.argtypes, lib.conv2d_strerror.restype = [I], ctypes.c_char_p
     lib.conv2d_last_error.argtypes, lib.conv2d_last_error.restype = [], ctypes.c_char_p
@@ -160,8 +161,15 @@ def _stream(stream) -> int | None:
 
 def _raw_stream() -> int:
     """torch's current stream on the current device, without building a Stream object."""
-    import torch
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    global _current_stream, _current_device
+    if _current_stream is None:
+        import torch
+        torch.cuda.current_device()   # initialises the GPU once
+        _current_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    return _current_stream(_current_device())
+
+
+_current_stream = _current_device = None
 
 
 def _check(rc: int, where: str) -> int:
@@ -385,6 +393,12 @@ def conv2d_set_path_override(path: int) -> int:
 
 def conv2d_set_grid_limit(max_workgroups: int) -> int:
     return _check(int(lib.conv2d_set_grid_limit(max_workgroups)), "conv2d_set_grid_limit")
+
+
+def conv2d_set_wait_limit(looks: int) -> int:
+    """Looks for another workgroup's partial sums before a workgroup of a large
+    group norm computes them itself; returns the previous limit."""
+    return _check(int(lib.conv2d_set_wait_limit(looks)), "conv2d_set_wait_limit")
 
 
 def conv2d_release_scratch() -> None:

@@ -159,6 +159,10 @@ inline bool buffer_addressable(const Shape& s) {
 // workgroups and walk their items in a grid-stride loop, so any cap >= 1 is
 // valid; a small one makes every workgroup walk several items.
 int grid_limit();
+
+// Looks at another workgroup's result before a workgroup computes it itself, set
+// by conv2d_set_wait_limit.
+int wait_limit();
 inline long long persistent_slots(long long resident) {
     const int lim = grid_limit();
     return (lim > 0 && lim < resident) ? lim : resident;

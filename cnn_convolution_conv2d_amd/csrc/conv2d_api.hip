@@ -34,6 +34,8 @@ int hip_fail(hipError_t e, const char* what) {
 
 int g_path_override = CONV2D_PATH_AUTO;
 int g_grid_limit = 0;
+constexpr int kWaitLimit = 64;   // looks, about a microsecond each
+int g_wait_limit = kWaitLimit;
 
 // CONV2D_LOG (environment, read once): when set and not "0", every forward
 // entry prints the kernel path it chose to stderr, one line per call, so a
@@ -482,12 +484,18 @@ int validate_norm(const NormArgs& a, int H, int W, int act, const void* ws, size
 }  // namespace
 
 int conv2d::grid_limit() { return __atomic_load_n(&g_grid_limit, __ATOMIC_RELAXED); }
+int conv2d::wait_limit() { return __atomic_load_n(&g_wait_limit, __ATOMIC_RELAXED); }
 
 extern "C" {
 
 int conv2d_set_grid_limit(int max_workgroups) {
     if (max_workgroups < 0) return set_error(CONV2D_ERR_ARG, "grid limit %d must be >= 0", max_workgroups);
     return __atomic_exchange_n(&g_grid_limit, max_workgroups, __ATOMIC_RELAXED);
+}
+
+int conv2d_set_wait_limit(int looks) {
+    if (looks < 0 || looks > 1000) return set_error(CONV2D_ERR_ARG, "the wait limit must be 0 to 1000");
+    return __atomic_exchange_n(&g_wait_limit, looks, __ATOMIC_RELAXED);
 }
 
 int conv2d_out_dim(int in, int k, int stride, int pad, int dilation) {

@@ -9,7 +9,7 @@
 //     s1 = sum(gamma * dz) / m,  s2 = sum(gamma * dz * xh) / m   (over the group)
 //     dx = rstd * (gamma * dz - s1 - xh * s2)
 //
-// Two forms.
+// Three forms.
 //
 // Streaming, two launches.  The first reads the activations once and leaves
 // partial statistics per image, chunk of pixels and group in the workspace;
@@ -21,7 +21,13 @@
 // read once.  Forward and backward take it where a group fits and is either
 // small (latency counts) or has whole 64-byte pieces of every pixel.
 //
-// No atomics: every sum has a fixed order.
+// Joined, for large tensors of which no workgroup can hold a group: a workgroup
+// keeps a chunk of an image in registers and takes the statistics of the
+// image's other chunks from the workspace, so memory is read once here too.
+// 112x112x128 over 32 images 55.7 us, where streaming takes 69.2 and the bytes
+// alone 42; backward of 56x56x256 over 64 images 103 us for 116 (bytes: 63).
+//
+// Every sum has a fixed order: equal calls give equal bits.
 //
 // Every thread keeps V consecutive channels (16 bytes where the channel count
 // and the alignment allow) and walks down the pixels of its chunk, R rows of
@@ -119,53 +125,58 @@ __device__ __forceinline__ void combine_stats(const float2* part, const NormArgs
     __syncthreads();
 }
 
-// First launch of the streaming forward pass: (mean, M2) of every group of
-// one chunk.  One workgroup per image and chunk; LDS: R * C pairs.
-template <typename T, int V>
-__global__ __launch_bounds__(512) void gn_stats_kernel(NormArgs a, int TX, int R, int chunks, int pix, float2* part) {
-    extern __shared__ float2 lds[];
-    const int n = blockIdx.x / chunks, chunk = blockIdx.x - n * chunks;
-    const int r = small_div(threadIdx.x, TX), tx = threadIdx.x - r * TX;
-    const int p0 = chunk * pix, np = min(pix, a.P - p0);
-    const long long step = (long long)R * a.ldx;
-    const Part part_of(np, R, r);
-    const int cnt = part_of.cnt;
-    if (r < R) {
-        for (int c = tx * V; c < a.C; c += TX * V) {
-            const T* p = static_cast<const T*>(a.x) + ((long long)n * a.P + p0 + part_of.first) * a.ldx + c;
-            Batch<T, V, kBatch> b;
-            b.load(p, step, 0, cnt);
-            const typename Vec<T, V>::raw k_raw = b.raw[0];
-            float k[V], s[V], ss[V];
-            Vec<T, V>::unpack(k_raw, k);
+// A thread's running sums of x - k and (x - k)^2 for its V channels, k the first
+// value of each; finish: (mean, M2) of `cnt` values to LDS.
+template <typename T, int V> struct Moments {
+    typename Vec<T, V>::raw first;
+    float k[V], s[V], ss[V];
+    __device__ __forceinline__ void start(const typename Vec<T, V>::raw& f) {
+        first = f;
+        Vec<T, V>::unpack(f, k);
 #pragma unroll
-            for (int j = 0; j < V; ++j) s[j] = ss[j] = 0.0f;
-#pragma clang loop unroll(disable)
-            for (int i = 0; i < cnt; i += kBatch) {
+        for (int j = 0; j < V; ++j) s[j] = ss[j] = 0.0f;
+    }
+    __device__ __forceinline__ void add(const typename Vec<T, V>::raw& r, bool inside) {
+        float v[V];
+        Vec<T, V>::unpack(inside ? r : first, v);   // past the end: adds nothing
 #pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    float v[V];
-                    Vec<T, V>::unpack(i + u < cnt ? b.raw[u] : k_raw, v);   // past the end: adds nothing
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        const float d = v[j] - k[j];
-                        s[j] += d;
-                        ss[j] = fmaf(d, d, ss[j]);
-                    }
-                }
-                b.load(p, step, i + kBatch, cnt);
-            }
-            const float inv = cnt > 0 ? 1.0f / cnt : 0.0f;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float d = s[j] * inv, m2 = ss[j] - s[j] * d;
-                lds[r * a.C + c + j] = make_float2(k[j] + d, m2 < 0.0f ? 0.0f : m2);  // a NaN stays
-            }
+        for (int j = 0; j < V; ++j) {
+            const float d = v[j] - k[j];
+            s[j] += d;
+            ss[j] = fmaf(d, d, ss[j]);
         }
     }
-    __syncthreads();
-    // a group's R x C/G entries, merged in one pass as in combine_stats: row
-    // `row` of the threads has one value more below `more`
+    __device__ __forceinline__ void finish(int cnt, float2* out) const {
+        const float inv = cnt > 0 ? 1.0f / cnt : 0.0f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float d = s[j] * inv, m2 = ss[j] - s[j] * d;
+            out[j] = make_float2(k[j] + d, m2 < 0.0f ? 0.0f : m2);  // a NaN stays
+        }
+    }
+};
+
+// The same for `cnt` vectors that stream past.
+template <typename T, int V, int B = kBatch>
+__device__ __forceinline__ void stream_moments(const T* p, long long step, int cnt, float2* out) {
+    Batch<T, V, B> b;
+    b.load(p, step, 0, cnt);
+    Moments<T, V> m;
+    m.start(b.raw[0]);
+#pragma clang loop unroll(disable)
+    for (int i = 0; i < cnt; i += B) {
+#pragma unroll
+        for (int u = 0; u < B; ++u) m.add(b.raw[u], i + u < cnt);
+        b.load(p, step, i + B, cnt);
+    }
+    m.finish(cnt, out);
+}
+
+// A chunk's (mean, M2) of every group from its R x C entries in LDS, merged in
+// one pass as in combine_stats: row `row` of the threads has one value more
+// below `more`.  put(g, mean, M2) on one lane of every group.
+template <typename PUT>
+__device__ __forceinline__ void merge_rows(const float2* lds, const NormArgs& a, int np, int R, PUT put) {
     const int cg = a.C / a.G, lg = lanes_per(a.G), L = 1 << lg, lane = threadIdx.x & (L - 1);
     const int few = np / R, more = np - few * R, count = R * cg;
     for (int g = threadIdx.x >> lg; g < a.G; g += blockDim.x >> lg) {
@@ -186,10 +197,28 @@ __global__ __launch_bounds__(512) void gn_stats_kernel(NormArgs a, int TX, int R
         s = lanes_sum(s, L);
         ss = lanes_sum(ss, L);
         const float shift = s / ((float)np * cg), mean = base + shift;
-        float m2 = ss - s * shift;
-        m2 = m2 < 0.0f ? 0.0f : m2;   // a NaN stays
-        if (lane == 0) part[(long long)blockIdx.x * a.G + g] = make_float2(mean, m2);
+        const float m2 = ss - s * shift;
+        if (lane == 0) put(g, mean, m2 < 0.0f ? 0.0f : m2);   // a NaN stays
     }
+}
+
+// First launch of the streaming forward pass: (mean, M2) of every group of
+// one chunk.  One workgroup per image and chunk; LDS: R * C pairs.
+template <typename T, int V>
+__global__ __launch_bounds__(512) void gn_stats_kernel(NormArgs a, int TX, int R, int chunks, int pix, float2* part) {
+    extern __shared__ float2 lds[];
+    const int n = blockIdx.x / chunks, chunk = blockIdx.x - n * chunks;
+    const int r = small_div(threadIdx.x, TX), tx = threadIdx.x - r * TX;
+    const int p0 = chunk * pix, np = min(pix, a.P - p0);
+    const Part part_of(np, R, r);
+    if (r < R)
+        for (int c = tx * V; c < a.C; c += TX * V)
+            stream_moments<T, V>(static_cast<const T*>(a.x) + ((long long)n * a.P + p0 + part_of.first) * a.ldx + c,
+                                 (long long)R * a.ldx, part_of.cnt, lds + r * a.C + c);
+    __syncthreads();
+    merge_rows(lds, a, np, R, [&](int g, float mean, float m2) {
+        part[(long long)blockIdx.x * a.G + g] = make_float2(mean, m2);
+    });
 }
 
 // A thread's constants for its V channels.  bf16 activations carry 8 bits, so
@@ -394,10 +423,12 @@ __global__ __launch_bounds__(256) void gn_quant_wide_kernel(NormArgs a, int chun
     }
 }
 
-// A thread's constants of the backward pass, and an element's dz and xh.  ONE:
-// its channels are of one group.  ReLU's derivative at 0 is 0; a NaN stays.
+// A thread's constants of the backward pass, and an element's dz from
+// xc = x - mean.  scale = gamma * rstd; sums of dz * xc are multiplied with rstd
+// at their end.  ONE: its channels are of one group.  ReLU's derivative at 0 is
+// 0; a NaN stays.
 template <int V, bool ONE = false> struct Slope {
-    float mean[ONE ? 1 : V], rstd[ONE ? 1 : V], gamma[V], beta[V];
+    float mean[ONE ? 1 : V], rstd[ONE ? 1 : V], scale[V], beta[V];
     static constexpr __device__ __forceinline__ int at(int j) { return ONE ? 0 : j; }
     __device__ __forceinline__ void load(const NormArgs& a, int n, int c) {
         const int cg = a.C / a.G;
@@ -410,14 +441,14 @@ template <int V, bool ONE = false> struct Slope {
                 mean[at(j)] = a.mean[(long long)n * a.G + g];
                 rstd[at(j)] = a.rstd[(long long)n * a.G + g];
             }
-            gamma[j] = a.gamma ? a.gamma[c + j] : 1.0f;
+            scale[j] = rstd[at(j)] * (a.gamma ? a.gamma[c + j] : 1.0f);
             beta[j] = a.beta ? a.beta[c + j] : 0.0f;
         }
     }
-    __device__ __forceinline__ float xh(float x, int j) const { return (x - mean[at(j)]) * rstd[at(j)]; }
-    template <int ACT> __device__ __forceinline__ float dz(float dy, float xh, int j) const {
+    __device__ __forceinline__ float xc(float x, int j) const { return x - mean[at(j)]; }
+    template <int ACT> __device__ __forceinline__ float dz(float dy, float xc, int j) const {
         if (ACT == kActNone) return dy;
-        const float z = fmaf(xh, gamma[j], beta[j]);
+        const float z = fmaf(xc, scale[j], beta[j]);
         if (ACT == kActRelu) return z > 0.0f ? dy : z <= 0.0f ? 0.0f : z;
         const float e = sigmoid(z);
         return dy * fmaf(z * e, 1.0f - e, e);
@@ -441,6 +472,96 @@ __device__ __forceinline__ void sum_rows(float2* lds, int R, int cols) {
     __syncthreads();
 }
 
+// A chunk's two sums of every group, weighted with gamma, from those of its
+// channels in LDS.  put(g, sum, sum) on one lane of every group.
+template <typename PUT> __device__ __forceinline__ void weigh_groups(const float2* lds, const NormArgs& a, PUT put) {
+    const int cg = a.C / a.G, lg = lanes_per(a.G), L = 1 << lg, lane = threadIdx.x & (L - 1);
+    for (int g = threadIdx.x >> lg; g < a.G; g += blockDim.x >> lg) {
+        float s = 0.0f, t = 0.0f;
+        for (int c = g * cg + lane; c < (g + 1) * cg; c += L) {
+            const float w = a.gamma ? a.gamma[c] : 1.0f;
+            s = fmaf(w, lds[c].x, s);
+            t = fmaf(w, lds[c].y, t);
+        }
+        s = lanes_sum(s, L);
+        t = lanes_sum(t, L);
+        if (lane == 0) put(g, s, t);
+    }
+}
+
+// Adds an image's chunks: out[g] = the group's two sums over m.
+__device__ __forceinline__ void add_chunks(const float2* part, const NormArgs& a, int chunks, float2* out) {
+    const int lg = lanes_per(a.G), L = 1 << lg, lane = threadIdx.x & (L - 1);
+    const float inv = 1.0f / ((float)a.P * (a.C / a.G));
+    for (int g = threadIdx.x >> lg; g < a.G; g += blockDim.x >> lg) {
+        const float2* p = part + g;
+        float s = 0.0f, t = 0.0f;
+        for (int j0 = lane; j0 < chunks; j0 += 4 * L) {
+            float2 e[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) e[u] = p[(long long)min(j0 + u * L, chunks - 1) * a.G];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                s += j0 + u * L < chunks ? e[u].x : 0.0f;
+                t += j0 + u * L < chunks ? e[u].y : 0.0f;
+            }
+        }
+        s = lanes_sum(s, L);
+        t = lanes_sum(t, L);
+        if (lane == 0) out[g] = make_float2(s * inv, t * inv);
+    }
+    __syncthreads();
+}
+
+// A thread's sums of dz and dz * xc for its V channels; finish: those of dz and
+// dz * xh to LDS.
+template <typename T, int V, int ACT, typename F> struct SlopeSums {
+    float A[V], B[V];
+    __device__ __forceinline__ SlopeSums() {
+#pragma unroll
+        for (int j = 0; j < V; ++j) A[j] = B[j] = 0.0f;
+    }
+    __device__ __forceinline__ void add(const F& f, const typename Vec<T, V>::raw& rx, const typename Vec<T, V>::raw& rd,
+                                        bool inside) {
+        float x[V], d[V];
+        Vec<T, V>::unpack(rx, x);
+        Vec<T, V>::unpack(rd, d);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float xc = f.xc(x[j], j), dz = f.template dz<ACT>(d[j], xc, j);
+            A[j] += inside ? dz : 0.0f;
+            B[j] = inside ? fmaf(dz, xc, B[j]) : B[j];
+        }
+    }
+    __device__ __forceinline__ void finish(const F& f, float2* out) const {
+#pragma unroll
+        for (int j = 0; j < V; ++j) out[j] = make_float2(A[j], B[j] * f.rstd[F::at(j)]);
+    }
+};
+
+// The same for `cnt` pixels from `first` on, R apart, that stream past.
+template <typename T, int V, int ACT, typename F, int NB = kBatchBwd>
+__device__ __forceinline__ void stream_slopes(const NormArgs& a, int n, int c, long long first, int cnt, int R,
+                                              float2* out) {
+    const T* px = static_cast<const T*>(a.x) + first * a.ldx + c;
+    const T* pd = static_cast<const T*>(a.dy) + first * a.lddy + c;
+    const long long xs = (long long)R * a.ldx, ds = (long long)R * a.lddy;
+    Batch<T, V, NB> bx, bd;
+    bx.load(px, xs, 0, cnt);
+    bd.load(pd, ds, 0, cnt);
+    F f;
+    f.load(a, n, c);
+    SlopeSums<T, V, ACT, F> sums;
+#pragma clang loop unroll(disable)
+    for (int i = 0; i < cnt; i += NB) {
+#pragma unroll
+        for (int u = 0; u < NB; ++u) sums.add(f, bx.raw[u], bd.raw[u], i + u < cnt);
+        bx.load(px, xs, i + NB, cnt);
+        bd.load(pd, ds, i + NB, cnt);
+    }
+    sums.finish(f, out);
+}
+
 // First launch of the streaming backward pass: for every image and chunk the
 // sums of dz and dz * xh per channel (pc: [block][2][C]) and, weighted with
 // gamma, per group (pg).  LDS: R * C pairs.
@@ -454,39 +575,8 @@ __global__ __launch_bounds__(512) void gn_bwd_sums_kernel(NormArgs a, int TX, in
     if (r < R) {
         const Part part_of(np, R, r);
         const long long first = (long long)n * a.P + p0 + part_of.first;
-        const int cnt = part_of.cnt;
-        const long long xs = (long long)R * a.ldx, ds = (long long)R * a.lddy;
-        for (int c = tx * V; c < a.C; c += TX * V) {
-            const T* px = static_cast<const T*>(a.x) + first * a.ldx + c;
-            const T* pd = static_cast<const T*>(a.dy) + first * a.lddy + c;
-            Batch<T, V, kBatchBwd> bx, bd;
-            bx.load(px, xs, 0, cnt);
-            bd.load(pd, ds, 0, cnt);
-            Slope<V> f;
-            f.load(a, n, c);
-            float A[V], B[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j) A[j] = B[j] = 0.0f;
-#pragma clang loop unroll(disable)
-            for (int i = 0; i < cnt; i += kBatchBwd) {
-#pragma unroll
-                for (int u = 0; u < kBatchBwd; ++u) {
-                    float x[V], d[V];
-                    Vec<T, V>::unpack(bx.raw[u], x);
-                    Vec<T, V>::unpack(bd.raw[u], d);
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        const float xh = f.xh(x[j], j), dz = f.template dz<ACT>(d[j], xh, j);
-                        A[j] += i + u < cnt ? dz : 0.0f;
-                        B[j] = i + u < cnt ? fmaf(dz, xh, B[j]) : B[j];
-                    }
-                }
-                bx.load(px, xs, i + kBatchBwd, cnt);
-                bd.load(pd, ds, i + kBatchBwd, cnt);
-            }
-#pragma unroll
-            for (int j = 0; j < V; ++j) lds[r * a.C + c + j] = make_float2(A[j], B[j]);
-        }
+        for (int c = tx * V; c < a.C; c += TX * V)
+            stream_slopes<T, V, ACT, Slope<V>>(a, n, c, first, part_of.cnt, R, lds + r * a.C + c);
     }
     __syncthreads();
     sum_rows(lds, R, a.C);
@@ -495,18 +585,7 @@ __global__ __launch_bounds__(512) void gn_bwd_sums_kernel(NormArgs a, int TX, in
         out[c] = lds[c].x;
         out[a.C + c] = lds[c].y;
     }
-    const int cg = a.C / a.G, lg = lanes_per(a.G), L = 1 << lg, lane = threadIdx.x & (L - 1);
-    for (int g = threadIdx.x >> lg; g < a.G; g += blockDim.x >> lg) {
-        float s = 0.0f, t = 0.0f;
-        for (int c = g * cg + lane; c < (g + 1) * cg; c += L) {
-            const float w = a.gamma ? a.gamma[c] : 1.0f;
-            s = fmaf(w, lds[c].x, s);
-            t = fmaf(w, lds[c].y, t);
-        }
-        s = lanes_sum(s, L);
-        t = lanes_sum(t, L);
-        if (lane == 0) pg[(long long)blockIdx.x * a.G + g] = make_float2(s, t);
-    }
+    weigh_groups(lds, a, [&](int g, float s, float t) { pg[(long long)blockIdx.x * a.G + g] = make_float2(s, t); });
 }
 
 constexpr int kParamChannels = 32;  // channels of one workgroup that sums dgamma and dbeta
@@ -562,32 +641,11 @@ __global__ __launch_bounds__(512) void gn_bwd_apply_kernel(NormArgs a, int TX, i
     bd.load(static_cast<const T*>(a.dy) + first * a.lddy + c0, ds, 0, cnt);
     Slope<V> f;
     f.load(a, n, c0);
-    {
-        const int lg = lanes_per(a.G), L = 1 << lg, lane = threadIdx.x & (L - 1);
-        const float inv = 1.0f / ((float)a.P * cg);
-        for (int g = threadIdx.x >> lg; g < a.G; g += blockDim.x >> lg) {
-            const float2* p = pg + (long long)n * chunks * a.G + g;
-            float s = 0.0f, t = 0.0f;
-            for (int j0 = lane; j0 < chunks; j0 += 4 * L) {
-                float2 e[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) e[u] = p[(long long)min(j0 + u * L, chunks - 1) * a.G];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    s += j0 + u * L < chunks ? e[u].x : 0.0f;
-                    t += j0 + u * L < chunks ? e[u].y : 0.0f;
-                }
-            }
-            s = lanes_sum(s, L);
-            t = lanes_sum(t, L);
-            if (lane == 0) lds[g] = make_float2(s * inv, t * inv);
-        }
-        __syncthreads();
-    }
+    add_chunks(pg + (long long)n * chunks * a.G, a, chunks, lds);
     const T* px = static_cast<const T*>(a.x) + first * a.ldx + c0;
     const T* pd = static_cast<const T*>(a.dy) + first * a.lddy + c0;
     T* po = static_cast<T*>(a.y) + first * a.ldy + c0;
-    float s1[V], s2[V];   // rstd * s1, rstd * s2
+    float s1[V], s2[V];   // rstd * s1, rstd^2 * s2
     auto group_sums = [&](int c) {
         int g = small_div(c, cg), left = (g + 1) * cg - c;
 #pragma unroll
@@ -596,7 +654,7 @@ __global__ __launch_bounds__(512) void gn_bwd_apply_kernel(NormArgs a, int TX, i
             --left;
             const float2 s = lds[g];
             s1[j] = s.x * f.rstd[j];
-            s2[j] = s.y * f.rstd[j];
+            s2[j] = s.y * f.rstd[j] * f.rstd[j];
         }
     };
     group_sums(c0);
@@ -609,8 +667,8 @@ __global__ __launch_bounds__(512) void gn_bwd_apply_kernel(NormArgs a, int TX, i
             Vec<T, V>::unpack(bd.raw[u], d);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float xh = f.xh(x[j], j), dz = f.template dz<ACT>(d[j], xh, j);
-                d[j] = fmaf(dz, f.rstd[j] * f.gamma[j], -fmaf(xh, s2[j], s1[j]));
+                const float xc = f.xc(x[j], j), dz = f.template dz<ACT>(d[j], xc, j);
+                d[j] = fmaf(dz, f.scale[j], -fmaf(xc, s2[j], s1[j]));
             }
             if (i + u < cnt) Vec<T, V>::store(po + (i + u) * os, d);
         }
@@ -719,30 +777,18 @@ __global__ __launch_bounds__(1024) void gn_bwd_resident_kernel(NormArgs a, int T
     bd.load(static_cast<const T*>(a.dy) + first * a.lddy + c, (long long)R * a.lddy, 0, cnt);
     Slope<V, true> f;
     f.load(a, n, c);
-    float A[V], B[V];
+    SlopeSums<T, V, ACT, Slope<V, true>> sums;
 #pragma unroll
-    for (int j = 0; j < V; ++j) A[j] = B[j] = 0.0f;
-#pragma unroll
-    for (int u = 0; u < NV; ++u) {
-        float x[V], d[V];
-        Vec<T, V>::unpack(bx.raw[u], x);
-        Vec<T, V>::unpack(bd.raw[u], d);
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float xh = f.xh(x[j], j), dz = f.template dz<ACT>(d[j], xh, j);
-            A[j] += u < cnt ? dz : 0.0f;
-            B[j] = u < cnt ? fmaf(dz, xh, B[j]) : B[j];
-        }
-    }
+    for (int u = 0; u < NV; ++u) sums.add(f, bx.raw[u], bd.raw[u], u < cnt);
     float s = 0.0f, t = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        if (r < R) rows[r * cg + tx * V + j] = make_float2(A[j], B[j]);
-        s = fmaf(f.gamma[j], A[j], s);
-        t = fmaf(f.gamma[j], B[j], t);
+        s = fmaf(f.scale[j], sums.A[j], s);
+        t = fmaf(f.scale[j], sums.B[j], t);
     }
+    if (r < R) sums.finish(f, rows + r * cg + tx * V);
     const float2 sum = block_sum(s, t, lds);   // and the rows are in LDS
-    const float m = (float)a.P * cg, s1 = sum.x / m * f.rstd[0], s2 = sum.y / m * f.rstd[0];
+    const float m = (float)a.P * cg, s1 = sum.x / m, s2 = sum.y / m * f.rstd[0] * f.rstd[0];
     T* po = static_cast<T*>(a.y) + first * a.ldy + c;
     const long long os = (long long)R * a.ldy;
 #pragma unroll
@@ -752,8 +798,8 @@ __global__ __launch_bounds__(1024) void gn_bwd_resident_kernel(NormArgs a, int T
         Vec<T, V>::unpack(bd.raw[u], d);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const float xh = f.xh(x[j], j), dz = f.template dz<ACT>(d[j], xh, j);
-            d[j] = fmaf(dz, f.rstd[0] * f.gamma[j], -fmaf(xh, s2, s1));
+            const float xc = f.xc(x[j], j), dz = f.template dz<ACT>(d[j], xc, j);
+            d[j] = fmaf(dz, f.scale[j], -fmaf(xc, s2, s1));
         }
         if (u < cnt) Vec<T, V>::store(po + u * os, d);
     }
@@ -770,9 +816,271 @@ __global__ __launch_bounds__(1024) void gn_bwd_resident_kernel(NormArgs a, int T
     }
 }
 
+// ------------------------------------------------------------------ joined
+
+// Tensors that no workgroup can hold a group of, read from memory once all the
+// same: every workgroup keeps a chunk of an image in registers, puts the chunk's
+// partial statistics of every group into the workspace, takes those of its
+// image's other chunks from there and finishes its own.
+//
+// A pair of partials is one 64-bit word, so that it is its own flag: a launch
+// before fills the words with kMissing, which no pair is (its NaNs are made
+// one pattern), and whoever has a pair puts it in the place of kMissing, once.
+//
+// No workgroup depends on another being resident: after `polls` looks at words
+// that stay missing it computes the chunk's partials itself, by the same
+// arithmetic, and puts them there.  The input may be the output too: a
+// workgroup writes only after it has seen all words of its own chunk, so one
+// that reads that chunk in its place and then still finds a word missing has
+// read what was there before, and the word it offers otherwise is dropped.
+typedef unsigned long long word_t;
+constexpr word_t kMissing = ~0ull;
+
+__device__ __forceinline__ word_t pair_word(float x, float y) {
+    const uint32_t nan = 0x7fc00000u, lo = x == x ? __float_as_uint(x) : nan, hi = y == y ? __float_as_uint(y) : nan;
+    return (word_t)hi << 32 | lo;
+}
+
+__device__ __forceinline__ void put_word(word_t* at, word_t w) {
+    word_t expected = kMissing;
+    __hip_atomic_compare_exchange_strong(at, &expected, w, __ATOMIC_RELAXED, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__device__ __forceinline__ word_t look(const word_t* at) {
+    return __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__global__ __launch_bounds__(256) void gn_clear_kernel(word_t* words, long long count) {
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < count; i += gridDim.x * 256ll) words[i] = kMissing;
+}
+
+// An image's `count` words, [chunk][G], into LDS; help(chunk) for a chunk of
+// which words stay missing (the whole workgroup, with a barrier at its end).
+// Ends with a barrier.
+template <typename HELP>
+__device__ __forceinline__ void gather(const word_t* words, int count, int G, int polls, word_t* lds, HELP help) {
+    __shared__ int missing;
+    constexpr int B = 4;
+    for (;;) {
+        int miss = 0x7fffffff, left = polls;
+        if (threadIdx.x == 0) missing = miss;
+        for (int e0 = threadIdx.x; e0 < count; e0 += B * blockDim.x) {
+            word_t w[B];
+#pragma unroll
+            for (int u = 0; u < B; ++u) w[u] = look(words + min(e0 + u * (int)blockDim.x, count - 1));
+#pragma unroll
+            for (int u = 0; u < B; ++u) {
+                const int e = min(e0 + u * (int)blockDim.x, count - 1);
+                for (; w[u] == kMissing && left > 0; --left) {
+                    __builtin_amdgcn_s_sleep(2);
+                    w[u] = look(words + e);
+                }
+                if (w[u] == kMissing) miss = min(miss, e / G);
+                lds[e] = w[u];
+            }
+        }
+        __syncthreads();
+        if (miss != 0x7fffffff) atomicMin(&missing, miss);
+        __syncthreads();
+        const int m = missing;
+        __syncthreads();
+        if (m == 0x7fffffff) return;
+        help(m);
+    }
+}
+
+// Vectors are worked on one after the other: all at once, as the compiler would
+// order them, unpacked values push the resident ones out to memory.
+__device__ __forceinline__ void one_by_one() { __builtin_amdgcn_sched_barrier(0); }
+
+// A chunk's rows behind a buffer descriptor: 32-bit offsets, loads past the
+// chunk's last pixel give zeros and stores there are dropped.
+template <int NV> struct Chunk {
+    __amdgpu_buffer_rsrc_t rows;
+    uint32_t at, step;
+    // elem bytes an element, pixels `ld` apart; the thread starts at pixel r,
+    // channel c, or outside
+    __device__ __forceinline__ Chunk(const void* p, long long pixel, long long ld, int elem, int np, int C, int R, int r,
+                                     int c, bool in)
+        : rows(make_rsrc(static_cast<const char*>(p) + pixel * ld * elem, (uint32_t)(((np - 1) * ld + C) * elem))),
+          at(in ? (uint32_t)((r * ld + c) * elem) : (uint32_t)kOOB),
+          step((uint32_t)(R * ld * elem)) {}
+    __device__ __forceinline__ void load(uint4 (&v)[NV]) const {
+#pragma unroll
+        for (int u = 0; u < NV; ++u) v[u] = load16(rows, (int)(at + u * step));
+    }
+};
+
+// What the compiler knows of a vector ends here: it would keep the values that
+// it unpacked before, twice the registers, rather than unpack them again.
+__device__ __forceinline__ void forget(uint4& v) { asm("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w)); }
+
+// Forward (QUANT: with the quantisation of every pixel, whose vectors are then
+// TX lanes, a power of two, of one wave).  LDS: R * C pairs, or the image's
+// words and G pairs if those are more.
+template <typename T, int V, int ACT, int NV, bool QUANT>
+__global__ __launch_bounds__(256, 4) void gn_joined_kernel(NormArgs a, int TX, int R, int chunks, int pix, int polls,
+                                                           word_t* words) {
+    extern __shared__ float2 lds[];
+    const int n = blockIdx.x / chunks, chunk = blockIdx.x - n * chunks;
+    const int r = small_div(threadIdx.x, TX), tx = threadIdx.x - r * TX;
+    const bool in = r < R && tx * V < a.C;
+    const int c = in ? tx * V : 0;
+    const long long image = (long long)n * a.P;
+    const int p0 = chunk * pix, np = min(pix, a.P - p0);
+    const int cnt = in ? Part(np, R, r).cnt : 0;
+    words += (long long)n * chunks * a.G;
+    uint4 raw[NV];
+    Chunk<NV>(a.x, image + p0, a.ldx, sizeof(T), np, a.C, R, r, c, in).load(raw);
+    {
+        Moments<T, V> m;
+        m.start(raw[0]);
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            m.add(raw[u], u < cnt);
+            one_by_one();
+        }
+        if (in) m.finish(cnt, lds + r * a.C + c);
+    }
+    __syncthreads();
+    merge_rows(lds, a, np, R, [&](int g, float mean, float m2) { put_word(words + chunk * a.G + g, pair_word(mean, m2)); });
+    __syncthreads();
+    gather(words, chunks * a.G, a.G, polls, reinterpret_cast<word_t*>(lds), [&](int other) {
+        const int q0 = other * pix, nq = min(pix, a.P - q0);
+        const Part of(nq, R, r);
+#pragma clang loop unroll(disable)
+        for (int k = in ? c : a.C; k < min(c + V, a.C); ++k)   // channel by channel: few registers
+            stream_moments<T, 1, 1>(static_cast<const T*>(a.x) + (image + q0 + of.first) * a.ldx + k,
+                                    (long long)R * a.ldx, of.cnt, lds + r * a.C + k);
+        __syncthreads();
+        merge_rows(lds, a, nq, R, [&](int g, float mean, float m2) { put_word(words + other * a.G + g, pair_word(mean, m2)); });
+        __syncthreads();
+    });
+    Affine<T, V> f;
+    f.prepare(a, c);
+    float2* stat = lds + chunks * a.G;
+    combine_stats(lds, a, 0, chunks, pix, stat);
+    if (chunk == 0) save_stats(a, stat, n);
+    finish_affine<Affine<T, V>, V>(f, stat, c, a.C / a.G);
+    const Chunk<NV> out(a.y, image + p0, a.ldy, QUANT ? 1 : sizeof(T), np, a.C, R, r, c, in);
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        float v[V];
+        forget(raw[u]);
+        Vec<T, V>::unpack(raw[u], v);
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = activate<ACT>(f.z(v[j], j));
+        if constexpr (!QUANT) {
+            store16(out.rows, (int)(out.at + u * out.step), Vec<T, V>::pack(v));
+        } else {
+            uint32_t top = 0;
+#pragma unroll
+            for (int j = 0; j < V; ++j) top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
+            const RowScale s = row_scale(lanes_max(in ? top : 0, TX));
+            if (u < cnt) {
+                store_quantised<V>(static_cast<int8_t*>(a.y) + (image + p0 + r + u * R) * a.ldy + c, v, s.inv);
+                if (tx == 0) a.q_scale[image + p0 + r + u * R] = s.scale;
+            }
+        }
+        one_by_one();
+    }
+}
+
+// Backward, for vectors that lie in one group; the channels' sums of every
+// chunk go to pc ([block][2][C]).  LDS as in the forward pass.
+template <typename T, int V, int ACT, int NV>
+__global__ __launch_bounds__(256, 3) void gn_bwd_joined_kernel(NormArgs a, int TX, int R, int chunks, int pix, int polls,
+                                                               word_t* words, float* pc) {
+    extern __shared__ float2 lds[];
+    const int n = blockIdx.x / chunks, chunk = blockIdx.x - n * chunks;
+    const int r = small_div(threadIdx.x, TX), c = (threadIdx.x - r * TX) * V;
+    const int p0 = chunk * pix, np = min(pix, a.P - p0);
+    const int cnt = Part(np, R, r).cnt;
+    const bool in = r < R;
+    const long long image = (long long)n * a.P;
+    words += (long long)n * chunks * a.G;
+    typedef Slope<V, true> F;
+    uint4 rx[NV];
+    float dz[NV][V];   // kept: the sigmoid and its slope are most of the pass's arithmetic
+    float scale[V], mean, rstd;
+    {
+        uint4 rd[NV];
+        Chunk<NV>(a.x, image + p0, a.ldx, sizeof(T), np, a.C, R, r, c, in).load(rx);
+        Chunk<NV>(a.dy, image + p0, a.lddy, sizeof(T), np, a.C, R, r, c, in).load(rd);
+        F f;
+        f.load(a, n, c);
+        SlopeSums<T, V, ACT, F> sums;
+#pragma unroll
+        for (int u = 0; u < NV; ++u) {
+            float x[V], d[V];
+            Vec<T, V>::unpack(u < cnt ? rx[u] : rx[0], x);
+            Vec<T, V>::unpack(rd[u], d);   // outside: 0, and so is dz
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float xc = f.xc(x[j], j);
+                dz[u][j] = f.template dz<ACT>(d[j], xc, j);
+                sums.A[j] += dz[u][j];
+                sums.B[j] = fmaf(dz[u][j], xc, sums.B[j]);
+            }
+            one_by_one();
+        }
+        if (in) sums.finish(f, lds + r * a.C + c);
+#pragma unroll
+        for (int j = 0; j < V; ++j) scale[j] = f.scale[j];
+        mean = f.mean[0];
+        rstd = f.rstd[0];
+    }
+    __syncthreads();
+    sum_rows(lds, R, a.C);
+    if (a.dgamma || a.dbeta) {
+        float* out = pc + (long long)blockIdx.x * 2 * a.C;
+        for (int k = threadIdx.x; k < a.C; k += blockDim.x) {
+            out[k] = lds[k].x;
+            out[a.C + k] = lds[k].y;
+        }
+    }
+    weigh_groups(lds, a, [&](int g, float s, float t) { put_word(words + chunk * a.G + g, pair_word(s, t)); });
+    __syncthreads();
+    gather(words, chunks * a.G, a.G, polls, reinterpret_cast<word_t*>(lds), [&](int other) {
+        const int q0 = other * pix;
+        const Part of(min(pix, a.P - q0), R, r);
+#pragma clang loop unroll(disable)
+        for (int k = in ? c : a.C; k < min(c + V, a.C); ++k)
+            stream_slopes<T, 1, ACT, Slope<1, true>, 1>(a, n, k, image + q0 + of.first, of.cnt, R, lds + r * a.C + k);
+        __syncthreads();
+        sum_rows(lds, R, a.C);
+        weigh_groups(lds, a, [&](int g, float s, float t) { put_word(words + other * a.G + g, pair_word(s, t)); });
+        __syncthreads();
+    });
+    float2* sums = lds + chunks * a.G;
+    add_chunks(lds, a, chunks, sums);
+    const float2 sum = sums[small_div(c, a.C / a.G)];
+    const float s1 = sum.x * rstd, s2 = sum.y * rstd * rstd;
+    const Chunk<NV> out(a.y, image + p0, a.ldy, sizeof(T), np, a.C, R, r, c, in);
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+        float x[V], d[V];
+        forget(rx[u]);
+        Vec<T, V>::unpack(rx[u], x);
+#pragma unroll
+        for (int j = 0; j < V; ++j) d[j] = fmaf(dz[u][j], scale[j], -fmaf(x[j] - mean, s2, s1));
+        store16(out.rows, (int)(out.at + u * out.step), Vec<T, V>::pack(d));
+        one_by_one();
+    }
+}
+
 __global__ __launch_bounds__(256) void gn_params_kernel(NormArgs a, const float* pc) {
     __shared__ float2 lds[256];
     sum_params(a, pc, a.N, blockIdx.x, lds);
+}
+
+// An image's `count` partials of kParamChannels channels into one: out [N][2][C].
+__global__ __launch_bounds__(256) void gn_image_params_kernel(NormArgs a, const float* pc, int count, float* out) {
+    __shared__ float2 lds[256];
+    out += (long long)blockIdx.y * 2 * a.C;
+    a.dbeta = out;
+    a.dgamma = out + a.C;
+    sum_params(a, pc + (long long)blockIdx.y * count * 2 * a.C, count, blockIdx.x, lds);
 }
 
 // ------------------------------------------------------------------ host
@@ -932,6 +1240,114 @@ template <typename T, int V> hipError_t backward(const NormArgs& a, int act, voi
            : act == kActRelu ? backward_act<T, V, kActRelu>(a, ws, st) : backward_act<T, V, kActNone>(a, ws, st);
 }
 
+// The joined form: 256 threads, of which TX are the vectors of a pixel, R rows
+// of them, nv vectors a thread; nv = 0 where it is not taken.
+struct Joined {
+    int TX, R, chunks, pix, nv;
+    size_t lds;
+};
+
+// Vectors of a thread: with 16 four workgroups fit a compute unit's registers,
+// with 7 of x and 7 of dz (as fp32) three.  Shorter chunks, of which more fit,
+// wait more often (56x56x256 over 64 images backward: 7 vectors 103 us, 4
+// vectors at four workgroups 127; forward 112x112x128 over 32: 55.7, at 8
+// vectors and six workgroups 64).
+constexpr int kJoinedMost = 16, kJoinedMostBwd = 7;
+
+// Bytes of x from which one read saves more than the clearing launch and the
+// exchange cost (bf16, 256 channels of 56x56).  Forward: 8 MB 14.5 us against
+// 18.1 streaming, but 112x112x64 14.1 against 14.5, 4 MB 12.5 against 12.8.
+// Quantised: 16 MB even, 32 MB ahead by 2 us.  Backward: 32 MB 45.7 against
+// 41.7, 64 MB 70 against 74, 128 MB 123 against 148.
+constexpr long long kJoinedBytes = 12 << 20, kJoinedBytesQuant = 24 << 20, kJoinedBytesBwd = 48 << 20;
+
+// Every workgroup reads its image's words: at most a quarter of what it reads of x.
+constexpr int kJoinedWords = 2048;
+
+// Wider pixels leave a chunk few of them, and a chunk keeps 8 bytes a channel
+// for dgamma and dbeta.
+constexpr int kJoinedAcross = 64;
+
+// The plan for 16-byte vectors of V elements, whatever the tensor's size.
+// most: vectors of a thread (of x and of dy, where both are kept).
+Joined plan_joined(int P, int C, int G, int V, bool quant, int most) {
+    Joined p = {0, 0, 0, 0, 0, 0};
+    const int cv = C / V;
+    p.TX = cv;
+    if (quant)
+        for (p.TX = 1; p.TX < cv;) p.TX <<= 1;
+    if (p.TX > kJoinedAcross) return p;
+    p.R = 256 / p.TX;
+    const long long per = (long long)p.R * most, chunks = (P + per - 1) / per;
+    if (chunks * G > kJoinedWords) return p;
+    long long each = (P + chunks - 1) / chunks;
+    each = (each + p.R - 1) / p.R * p.R;
+    p.pix = (int)each;
+    p.chunks = (int)((P + each - 1) / each);
+    p.nv = each / p.R > most / 2 ? most : most / 2;
+    const int rows = p.R * C, words = (p.chunks + 1) * G;
+    p.lds = (size_t)(rows > words ? rows : words) * 8;
+    return p;
+}
+
+Joined make_joined(const NormArgs& a, int V, int elem, bool quant, int most) {
+    Joined p = {0, 0, 0, 0, 0, 0};
+    if (V * elem != 16) return p;
+    if ((long long)a.N * a.P * a.C * elem < (a.dy ? kJoinedBytesBwd : quant ? kJoinedBytesQuant : kJoinedBytes)) return p;
+    p = plan_joined(a.P, a.C, a.G, V, quant, most);
+    // 32-bit offsets in a chunk, one step past its end included
+    const long long ld = a.ldx > a.ldy ? (a.ldx > a.lddy ? a.ldx : a.lddy) : (a.ldy > a.lddy ? a.ldy : a.lddy);
+    if ((long long)a.N * p.chunks >= 0x7fffffffLL || (long long)p.R * (p.nv + 1) * ld * elem > 0x7fffff00LL) p.nv = 0;
+    return p;
+}
+
+hipError_t clear_words(void* ws, long long count, hipStream_t st) {
+    const long long blocks = (count + 1023) / 1024;
+    gn_clear_kernel<<<(int)(blocks < 1024 ? blocks : 1024), 256, 0, st>>>(static_cast<word_t*>(ws), count);
+    return hipGetLastError();
+}
+
+template <typename T, int V, int ACT, bool QUANT>
+hipError_t joined_act(const NormArgs& a, const Joined& p, void* ws, hipStream_t st) {
+    const hipError_t e = clear_words(ws, (long long)a.N * p.chunks * a.G, st);
+    if (e != hipSuccess) return e;
+    auto k = p.nv == kJoinedMost ? gn_joined_kernel<T, V, ACT, kJoinedMost, QUANT>
+                                 : gn_joined_kernel<T, V, ACT, kJoinedMost / 2, QUANT>;
+    k<<<a.N * p.chunks, 256, p.lds, st>>>(a, p.TX, p.R, p.chunks, p.pix, wait_limit(), static_cast<word_t*>(ws));
+    return hipGetLastError();
+}
+
+template <typename T, int V, bool QUANT>
+hipError_t joined(const NormArgs& a, int act, const Joined& p, void* ws, hipStream_t st) {
+    return act == kActSilu ? joined_act<T, V, kActSilu, QUANT>(a, p, ws, st)
+           : act == kActRelu ? joined_act<T, V, kActRelu, QUANT>(a, p, ws, st)
+                             : joined_act<T, V, kActNone, QUANT>(a, p, ws, st);
+}
+
+template <typename T, int V, int ACT> hipError_t joined_bwd_act(const NormArgs& a, const Joined& p, void* ws, hipStream_t st) {
+    const long long blocks = (long long)a.N * p.chunks;
+    const hipError_t e = clear_words(ws, blocks * a.G, st);
+    if (e != hipSuccess) return e;
+    word_t* words = static_cast<word_t*>(ws);
+    float* pc = reinterpret_cast<float*>(words + blocks * a.G);
+    auto k = p.nv == kJoinedMostBwd ? gn_bwd_joined_kernel<T, V, ACT, kJoinedMostBwd>
+                                    : gn_bwd_joined_kernel<T, V, ACT, kJoinedMostBwd / 2>;
+    k<<<(int)blocks, 256, p.lds, st>>>(a, p.TX, p.R, p.chunks, p.pix, wait_limit(), words, pc);
+    if (a.dgamma || a.dbeta) {
+        const int sums = (a.C + kParamChannels - 1) / kParamChannels;
+        float* images = pc + blocks * 2 * a.C;
+        gn_image_params_kernel<<<dim3(sums, a.N), 256, 0, st>>>(a, pc, p.chunks, images);
+        gn_params_kernel<<<sums, 256, 0, st>>>(a, images);
+    }
+    return hipGetLastError();
+}
+
+template <typename T, int V> hipError_t joined_bwd(const NormArgs& a, int act, const Joined& p, void* ws, hipStream_t st) {
+    return act == kActSilu ? joined_bwd_act<T, V, kActSilu>(a, p, ws, st)
+           : act == kActRelu ? joined_bwd_act<T, V, kActRelu>(a, p, ws, st)
+                             : joined_bwd_act<T, V, kActNone>(a, p, ws, st);
+}
+
 }  // namespace
 
 // The most partials that any vector width plans, so that one figure holds for
@@ -945,6 +1361,13 @@ size_t group_norm_workspace(int N, int P, int C, int G, int backward) {
         const size_t bytes = (size_t)N * p.chunks * (G + (backward ? (size_t)C : 0)) * 8;
         most = bytes > most ? bytes : most;
     }
+    for (int v = 4; v <= 8; v <<= 1)
+        for (int quant = 0; quant < (backward ? 1 : 2); ++quant) {
+            if (C % v) break;
+            const Joined p = plan_joined(P, C, G, v, quant, backward ? kJoinedMostBwd : kJoinedMost);
+            const size_t bytes = p.nv ? (size_t)N * (p.chunks * (G + (backward ? (size_t)C : 0)) + (backward ? C : 0)) * 8 : 0;
+            most = bytes > most ? bytes : most;
+        }
     return most;
 }
 
@@ -985,10 +1408,15 @@ hipError_t launch_group_norm(const NormArgs& a, int act, void* ws, hipStream_t s
     if (p.nv) {
         CONV2D_NORM_WIDTH(forward_group, cg, 0, a, act, p, st);
     }
+    const Joined j = make_joined(a, vector_width(a, a.C, elem, elem), elem, false, kJoinedMost);
+    if (j.nv) return elem == 4 ? joined<float, 4, false>(a, act, j, ws, st) : joined<bf16_t, 8, false>(a, act, j, ws, st);
     CONV2D_NORM_WIDTH(forward, a.C, 0, a, act, ws, st);
 }
 
 hipError_t launch_group_norm_quant(const NormArgs& a, int act, void* ws, hipStream_t st) {
+    const int elem = a.dtype == 0 ? 4 : 2;
+    const Joined j = make_joined(a, vector_width(a, a.C, elem, 1), elem, true, kJoinedMost);
+    if (j.nv) return elem == 4 ? joined<float, 4, true>(a, act, j, ws, st) : joined<bf16_t, 8, true>(a, act, j, ws, st);
     CONV2D_NORM_WIDTH(quantised, a.C, 1, a, act, ws, st);
 }
 
@@ -998,6 +1426,8 @@ hipError_t launch_group_norm_bwd(const NormArgs& a, int act, void* ws, hipStream
     if (p.nv) {
         CONV2D_NORM_WIDTH(backward_group, cg, 0, a, act, p, static_cast<float*>(ws), st);
     }
+    const Joined j = make_joined(a, vector_width(a, cg, elem, elem), elem, false, kJoinedMostBwd);
+    if (j.nv) return elem == 4 ? joined_bwd<float, 4>(a, act, j, ws, st) : joined_bwd<bf16_t, 8>(a, act, j, ws, st);
     CONV2D_NORM_WIDTH(backward, a.C, 0, a, act, ws, st);
 }
 

@@ -26,13 +26,14 @@ template <int V> struct Vec<float, V> {
 #pragma unroll
         for (int j = 0; j < V; ++j) v[j] = __uint_as_float(w[j]);
     }
-    static __device__ __forceinline__ void store(float* p, const float (&v)[V]) {
+    static __device__ __forceinline__ raw pack(const float (&v)[V]) {
         raw r;
         uint32_t* w = reinterpret_cast<uint32_t*>(&r);
 #pragma unroll
         for (int j = 0; j < V; ++j) w[j] = __float_as_uint(v[j]);
-        *reinterpret_cast<raw*>(p) = r;
+        return r;
     }
+    static __device__ __forceinline__ void store(float* p, const float (&v)[V]) { *reinterpret_cast<raw*>(p) = pack(v); }
 };
 
 template <int V> struct Vec<bf16_t, V> {
@@ -51,17 +52,18 @@ template <int V> struct Vec<bf16_t, V> {
         }
     }
     // one rounding, to nearest even
-    static __device__ __forceinline__ void store(bf16_t* p, const float (&v)[V]) {
+    static __device__ __forceinline__ raw pack(const float (&v)[V]) {
         if constexpr (V == 1) {
-            *p = f32_to_bf16(v[0]);
+            return f32_to_bf16(v[0]);
         } else {
             raw r;
             uint32_t* w = reinterpret_cast<uint32_t*>(&r);
 #pragma unroll
             for (int j = 0; j < V / 2; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-            *reinterpret_cast<raw*>(p) = r;
+            return r;
         }
     }
+    static __device__ __forceinline__ void store(bf16_t* p, const float (&v)[V]) { *reinterpret_cast<raw*>(p) = pack(v); }
 };
 
 // 1 / (1 + exp(-z)) from the hardware's exp2 and reciprocal (1 ulp each).

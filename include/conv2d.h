@@ -329,7 +329,7 @@ int conv2d_transpose_select_path(int N, int Cin, int H, int W, int Cout, int Kh,
  * gamma, beta: fp32 [C]; NULL means 1 and 0.  eps >= 0 and finite.  C must be
  * divisible by G, C <= 4096.  Any channel count, stride and alignment works;
  * C, the strides and the pointers as multiples of 16 bytes are fastest.
- * Sums have a fixed order (no atomics): equal calls give equal bits.  A NaN or
+ * Sums have a fixed order: equal calls give equal bits.  A NaN or
  * infinity spreads through its own (image, group) and no further.
  *
  * workspace: device memory of at least conv2d_group_norm_workspace_bytes
@@ -440,6 +440,14 @@ int conv2d_set_path_override(int path);
  * call.  Process-wide; returns the previous cap, or CONV2D_ERR_ARG if
  * max_workgroups < 0.  Host only. */
 int conv2d_set_grid_limit(int max_workgroups);
+
+/* How often (0 to 1000, 64 at first; about a microsecond each) a workgroup of a
+ * large group norm looks for another workgroup's partial sums before it
+ * computes them itself.  Neither the results nor their bits depend on it: it
+ * bounds the wait where other work keeps workgroups of the call off the device
+ * (0 makes every workgroup take that way, which tests use).  Process-wide;
+ * returns the previous limit, or CONV2D_ERR_ARG.  Host only. */
+int conv2d_set_wait_limit(int looks);
 
 /* Diagnostics: with the environment variable CONV2D_LOG set (and not "0")
  * when the library first checks it, every conv2d_fwd*, conv2d_transpose_fwd*

@@ -139,3 +139,10 @@ def test_definition_of_rows_and_products():
     y, size = ref.int8_matmul([[2, -3]], [0.5], [[4, 5], [1, 1]], [1.0, 2.0], bias=[1.0, 0.5], relu=True)
     np.testing.assert_array_equal(y, [[0.0, 0.0]])
     np.testing.assert_array_equal(size, [[4.5, 1.5]])
+
+
+def test_wait_limit_is_validated_and_returns_previous():
+    assert c2.lib.conv2d_set_wait_limit(-1) == c2.ERR_ARG
+    assert c2.lib.conv2d_set_wait_limit(1001) == c2.ERR_ARG
+    before = c2.conv2d_set_wait_limit(3)
+    assert c2.conv2d_set_wait_limit(before) == 3
