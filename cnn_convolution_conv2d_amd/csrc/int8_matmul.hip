@@ -8,13 +8,17 @@
 // Both operands are contiguous along k, which is how the matrix unit takes
 // them: 16 bytes of k per lane.
 //
-// Three kernels:
+// Four kernels:
 //   skinny  up to 64 rows: the weights stream from memory straight into the
-//           matrix unit's registers, 16 channels per workgroup, the waves
-//           split k and join in LDS.  Bound by reading the weights.
+//           matrix unit's registers, 16 or 32 channels per workgroup, the waves
+//           split k and join in LDS.  Bound by reading the weights (one row of
+//           4096, 16384 channels: 67 MB in 17.4 us, 3.9 TB/s) and, with more
+//           rows, by every workgroup reading all of them.
 //   tiled   BM rows x BN channels per workgroup, 128 bytes of k per stage,
 //           copied from memory into two LDS buffers without passing through
 //           registers.  Bound by the matrix unit.
+//   stream  many rows with k up to 512: the weights stay in registers, the rows
+//           stream past.  Bound by memory.
 //   ragged  the same tiles where k or a row stride is no multiple of 16 or a
 //           pointer is not aligned: rows are read as aligned words and
 //           shifted into place in registers.
@@ -50,35 +54,40 @@ __device__ __forceinline__ float finish(int acc, float scale, float bias, bool r
 
 // ------------------------------------------------------------------ skinny
 
-// One workgroup: 16 channels, MT * 16 rows, all of k.  Channels are the rows
-// of the 16x16 result, so a lane ends with 4 consecutive channels of one row.
-template <int MT, typename OUT>
+// One workgroup: NG * 16 channels, MT * 16 rows, all of k.  Channels are the
+// rows of the 16x16 result, so a lane ends with 4 consecutive channels of one
+// row.  128 bytes of k per wave and step, so that a step reads whole lines; U
+// steps are in flight.
+template <int MT, int NG, int U, typename OUT>
 __global__ void int8_skinny_kernel(Int8Args a) {
-    extern __shared__ i32x4 red[];   // [wave][MT][64]
+    extern __shared__ i32x4 red[];   // [wave][NG][MT][64]
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-    const int n0 = blockIdx.x * 16;
-    const auto wr = rows_rsrc(a.w, a.ldw, n0, a.N, 16, a.K);
+    const int n0 = blockIdx.x * (NG * 16);
+    const auto wr = rows_rsrc(a.w, a.ldw, n0, a.N, NG * 16, a.K);
     const auto qr = rows_rsrc(a.q, a.ldq, 0, a.M, 64, a.K);
     const int row = lane & 15, c = lane >> 4;
-    const int wo = n0 + row < a.N ? (int)(row * a.ldw) + c * 16 : kOOB;
-    int qo[MT];
+    int wo[NG], qo[MT];
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+        wo[g] = n0 + g * 16 + row < a.N ? (int)((g * 16 + row) * a.ldw) + c * 16 : kOOB;
 #pragma unroll
     for (int t = 0; t < MT; ++t) qo[t] = t * 16 + row < a.M ? (int)((t * 16 + row) * a.ldq) + c * 16 : kOOB;
-    i32x4 acc[MT];
+    i32x4 acc[NG][MT];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) acc[t] = i32x4{0, 0, 0, 0};
-    // 128 bytes of k per wave and step, so that a step reads whole lines
-    constexpr int U = MT <= 2 ? 4 : 2;
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[g][t] = i32x4{0, 0, 0, 0};
     const int stride = waves * 128;
     for (int k0 = wave * 128; k0 < a.K; k0 += stride * U) {
-        uint4 wv[U][2], qv[U][2][MT];
+        uint4 wv[U][2][NG], qv[U][2][MT];
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int k = k0 + u * stride + h * 64;
                 const bool in = k + c * 16 < a.K;   // K is a multiple of 16
-                wv[u][h] = load16(wr, in && wo != kOOB ? wo + k : kOOB);
+#pragma unroll
+                for (int g = 0; g < NG; ++g) wv[u][h][g] = load16(wr, in && wo[g] != kOOB ? wo[g] + k : kOOB);
 #pragma unroll
                 for (int t = 0; t < MT; ++t) qv[u][h][t] = load16(qr, in && qo[t] != kOOB ? qo[t] + k : kOOB);
             }
@@ -87,17 +96,22 @@ __global__ void int8_skinny_kernel(Int8Args a) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int t = 0; t < MT; ++t)
-                    acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, wv[u][h]),
-                                                                   __builtin_bit_cast(i32x4, qv[u][h][t]), acc[t], 0, 0, 0);
-    }
+                for (int g = 0; g < NG; ++g)
 #pragma unroll
-    for (int t = 0; t < MT; ++t) red[(wave * MT + t) * 64 + lane] = acc[t];
+                    for (int t = 0; t < MT; ++t)
+                        acc[g][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
+                            __builtin_bit_cast(i32x4, wv[u][h][g]), __builtin_bit_cast(i32x4, qv[u][h][t]), acc[g][t], 0, 0, 0);
+    }
+    constexpr int E = NG * MT * 64;
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) red[wave * E + (g * MT + t) * 64 + lane] = acc[g][t];
     __syncthreads();
-    for (int e = threadIdx.x; e < MT * 64; e += blockDim.x) {
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
         i32x4 s = red[e];
-        for (int k = 1; k < waves; ++k) s += red[k * MT * 64 + e];
-        const int m = (e >> 6) * 16 + (e & 15), n = n0 + ((e & 63) >> 4) * 4;
+        for (int k = 1; k < waves; ++k) s += red[k * E + e];
+        const int tile = e >> 6, m = tile % MT * 16 + (e & 15), n = n0 + tile / MT * 16 + ((e & 63) >> 4) * 4;
         if (m >= a.M) continue;
         const float qs = a.q_scale[m];
         OUT* y = static_cast<OUT*>(a.y) + (long long)m * a.ldy;
@@ -857,15 +871,32 @@ Int8Plan make_int8_plan(int M, int K, int N, bool aligned) {
     return p;
 }
 
-template <typename OUT> hipError_t skinny(const Int8Args& a, const Int8Plan& p, hipStream_t st) {
-    // waves that split k: 4 where the channels alone fill the chip, else up
-    // to 16, of at least 128 bytes of k each
-    int waves = 4;
-    while (waves < 16 && p.tn * waves < 8 * kUnits && waves * 2 * 128 <= a.K) waves *= 2;
-    if (a.M <= 16) int8_skinny_kernel<1, OUT><<<p.tn, waves * 64, waves * 1024, st>>>(a);
-    else if (a.M <= 32) int8_skinny_kernel<2, OUT><<<p.tn, waves * 64, waves * 2048, st>>>(a);
-    else int8_skinny_kernel<4, OUT><<<p.tn, waves * 64, waves * 4096, st>>>(a);
+template <int MT, int NG, int U, typename OUT> hipError_t skinny_instance(const Int8Args& a, int waves, hipStream_t st) {
+    int8_skinny_kernel<MT, NG, U, OUT><<<(a.N + NG * 16 - 1) / (NG * 16), waves * 64, waves * NG * MT * 1024, st>>>(a);
     return hipGetLastError();
+}
+
+// Two groups of 16 channels per workgroup use a row's values twice, where half
+// the workgroups still fill the chip and the rows are more than 16 (40 rows of
+// 4096, 16384 channels: 28.4 us against 38; 64 rows of 8192, 8192 channels: 34
+// against 45; but 4096 channels 18.2 against 16.3, and one row 20.6 against
+// 17.4).  Waves that split k: 4, or up to 16 where that leaves the chip few, of
+// at least 128 bytes of k each.  Up to 16 rows the steps in flight follow what
+// is left for a wave: 1 x 4096 -> 16384 takes 17.4 us with 8 and 21.2 with 4,
+// 1 x 2048 -> 2048 5.1 with 2 and 5.6 with 4.
+template <typename OUT> hipError_t skinny(const Int8Args& a, hipStream_t st) {
+    const int mt = a.M <= 16 ? 1 : a.M <= 32 ? 2 : 4;
+    const bool pairs = mt > 1 && a.N >= 32 * kUnits;
+    const int blocks = (a.N + (pairs ? 31 : 15)) / (pairs ? 32 : 16);
+    int waves = 4;   // 8 of 4 x 2 blocks: 64 KB of LDS
+    while (waves < (pairs && mt == 4 ? 8 : 16) && blocks * waves < 16 * kUnits && waves * 2 * 128 <= a.K) waves *= 2;
+    const int steps = (a.K + waves * 128 - 1) / (waves * 128);
+    if (mt == 1)
+        return steps > 4   ? skinny_instance<1, 1, 8, OUT>(a, waves, st)
+               : steps > 2 ? skinny_instance<1, 1, 4, OUT>(a, waves, st)
+                           : skinny_instance<1, 1, 2, OUT>(a, waves, st);
+    if (mt == 2) return pairs ? skinny_instance<2, 2, 2, OUT>(a, waves, st) : skinny_instance<2, 1, 2, OUT>(a, waves, st);
+    return pairs ? skinny_instance<4, 2, 2, OUT>(a, waves, st) : skinny_instance<4, 1, 2, OUT>(a, waves, st);
 }
 
 // Rows of y are whole, aligned 16-byte pieces.
@@ -936,7 +967,7 @@ bool int8_matmul_supports(int M, int K, int N, long long ldq, long long ldw) {
 hipError_t launch_int8_matmul(const Int8Args& a, int out_f32, void* ws, hipStream_t st) {
     const Int8Plan p = make_int8_plan(a.M, a.K, a.N, aligned_operands(a));
     if (p.kernel == kStream) return out_f32 ? stream<float>(a, p, st) : stream<bf16_t>(a, p, st);
-    if (p.kernel == kSkinny) return out_f32 ? skinny<float>(a, p, st) : skinny<bf16_t>(a, p, st);
+    if (p.kernel == kSkinny) return out_f32 ? skinny<float>(a, st) : skinny<bf16_t>(a, st);
     if (p.splits == 1) return out_f32 ? tiled<float>(a, p, st) : tiled<bf16_t>(a, p, st);
     Int8Args part = a;
     part.y = ws;
