@@ -212,9 +212,11 @@ __global__ __launch_bounds__(512) void gn_stats_kernel(NormArgs a, int TX, int R
     const int p0 = chunk * pix, np = min(pix, a.P - p0);
     const Part part_of(np, R, r);
     if (r < R)
-        for (int c = tx * V; c < a.C; c += TX * V)
+        for (int at = tx * V; at < a.C; at += TX * V) {
+            const int c = vector_start<V>(at, a.C);
             stream_moments<T, V>(static_cast<const T*>(a.x) + ((long long)n * a.P + p0 + part_of.first) * a.ldx + c,
                                  (long long)R * a.ldx, part_of.cnt, lds + r * a.C + c);
+        }
     __syncthreads();
     merge_rows(lds, a, np, R, [&](int g, float mean, float m2) {
         part[(long long)blockIdx.x * a.G + g] = make_float2(mean, m2);
@@ -287,7 +289,7 @@ __global__ __launch_bounds__(512) void gn_apply_kernel(NormArgs a, int TX, int R
     const int p0 = piece * pix, np = min(pix, a.P - p0);
     const Part part_of(np, R, r);
     const long long first = (long long)n * a.P + p0 + part_of.first;
-    const int cnt = part_of.cnt, c0 = tx * V;
+    const int cnt = part_of.cnt, c0 = vector_start<V>(tx * V, a.C);
     const long long xs = (long long)R * a.ldx, ys = (long long)R * a.ldy;
     Batch<T, V, kBatch> b;
     b.load(static_cast<const T*>(a.x) + first * a.ldx + c0, xs, 0, cnt);
@@ -299,7 +301,7 @@ __global__ __launch_bounds__(512) void gn_apply_kernel(NormArgs a, int TX, int R
     T* q = static_cast<T*>(a.y) + first * a.ldy + c0;
     finish_affine<Affine<T, V>, V>(f, lds, c0, a.C / a.G);
 #pragma clang loop unroll(disable)
-    for (int c = c0, i = 0; c < a.C && cnt > 0;) {
+    for (int at = tx * V, i = 0; cnt > 0;) {
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             float v[V];
@@ -310,11 +312,12 @@ __global__ __launch_bounds__(512) void gn_apply_kernel(NormArgs a, int TX, int R
         }
         i += kBatch;
         if (i >= cnt) {   // more than blockDim.x vectors across: the next channels
-            c += TX * V;
-            if (c >= a.C) break;
+            at += TX * V;
+            if (at >= a.C) break;
+            const int c = vector_start<V>(at, a.C);
             i = 0;
-            p += TX * V;
-            q += TX * V;
+            p = static_cast<const T*>(a.x) + first * a.ldx + c;
+            q = static_cast<T*>(a.y) + first * a.ldy + c;
             f.prepare(a, c);
             finish_affine<Affine<T, V>, V>(f, lds, c, a.C / a.G);
         }
@@ -332,7 +335,7 @@ __global__ __launch_bounds__(256) void gn_quant_kernel(NormArgs a, int LPP, int 
     const int n = blockIdx.x / chunks, piece = blockIdx.x - n * chunks;
     const int sub = small_div(threadIdx.x, LPP), l = threadIdx.x - sub * LPP, subs = small_div(blockDim.x, LPP);
     const bool in = l * V < a.C;
-    const int p0 = piece * pix, np = min(pix, a.P - p0), c = in ? l * V : 0;
+    const int p0 = piece * pix, np = min(pix, a.P - p0), c = in ? vector_start<V>(l * V, a.C) : 0;
     const Part part_of(np, subs, sub);
     const long long first = (long long)n * a.P + p0 + part_of.first;
     const int cnt = part_of.cnt;
@@ -406,16 +409,17 @@ __global__ __launch_bounds__(256) void gn_quant_wide_kernel(NormArgs a, int chun
         const T* p = static_cast<const T*>(a.x) + pixel * a.ldx;
         uint32_t top = 0;
 #pragma unroll 4
-        for (int c = l * V; c < a.C; c += 64 * V) {
+        for (int at = l * V; at < a.C; at += 64 * V) {
             float v[V];
-            values(p, c, v);
+            values(p, vector_start<V>(at, a.C), v);
 #pragma unroll
             for (int e = 0; e < V; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
         }
         const RowScale s = row_scale(lanes_max(top, 64));
 #pragma unroll 4
-        for (int c = l * V; c < a.C; c += 64 * V) {
+        for (int at = l * V; at < a.C; at += 64 * V) {
             float v[V];
+            const int c = vector_start<V>(at, a.C);
             values(p, c, v);
             store_quantised<V>(static_cast<int8_t*>(a.y) + pixel * a.ldy + c, v, s.inv);
         }
@@ -575,8 +579,10 @@ __global__ __launch_bounds__(512) void gn_bwd_sums_kernel(NormArgs a, int TX, in
     if (r < R) {
         const Part part_of(np, R, r);
         const long long first = (long long)n * a.P + p0 + part_of.first;
-        for (int c = tx * V; c < a.C; c += TX * V)
+        for (int at = tx * V; at < a.C; at += TX * V) {
+            const int c = vector_start<V>(at, a.C);
             stream_slopes<T, V, ACT, Slope<V>>(a, n, c, first, part_of.cnt, R, lds + r * a.C + c);
+        }
     }
     __syncthreads();
     sum_rows(lds, R, a.C);
@@ -634,7 +640,7 @@ __global__ __launch_bounds__(512) void gn_bwd_apply_kernel(NormArgs a, int TX, i
     const int p0 = piece * pix, np = min(pix, a.P - p0);
     const Part part_of(np, R, r);
     const long long first = (long long)n * a.P + p0 + part_of.first;
-    const int cnt = part_of.cnt, c0 = tx * V;
+    const int cnt = part_of.cnt, c0 = vector_start<V>(tx * V, a.C);
     const long long xs = (long long)R * a.ldx, ds = (long long)R * a.lddy, os = (long long)R * a.ldy;
     Batch<T, V, kBatchBwd> bx, bd;
     bx.load(static_cast<const T*>(a.x) + first * a.ldx + c0, xs, 0, cnt);
@@ -659,7 +665,7 @@ __global__ __launch_bounds__(512) void gn_bwd_apply_kernel(NormArgs a, int TX, i
     };
     group_sums(c0);
 #pragma clang loop unroll(disable)
-    for (int c = c0, i = 0; c < a.C && cnt > 0;) {
+    for (int at = tx * V, i = 0; cnt > 0;) {
 #pragma unroll
         for (int u = 0; u < kBatchBwd; ++u) {
             float x[V], d[V];
@@ -674,12 +680,13 @@ __global__ __launch_bounds__(512) void gn_bwd_apply_kernel(NormArgs a, int TX, i
         }
         i += kBatchBwd;
         if (i >= cnt) {
-            c += TX * V;
-            if (c >= a.C) break;
+            at += TX * V;
+            if (at >= a.C) break;
+            const int c = vector_start<V>(at, a.C);
             i = 0;
-            px += TX * V;
-            pd += TX * V;
-            po += TX * V;
+            px = static_cast<const T*>(a.x) + first * a.ldx + c;
+            pd = static_cast<const T*>(a.dy) + first * a.lddy + c;
+            po = static_cast<T*>(a.y) + first * a.ldy + c;
             f.load(a, n, c);
             group_sums(c);
         }
@@ -1097,6 +1104,22 @@ int vector_width(const NormArgs& a, int unit, int elem, int out_elem) {
     return v;
 }
 
+// The streaming form's, of large tensors: 16 bytes whatever the alignment, the
+// last vector of a row over part of the one before, unless the output is an
+// input too (a thread would read what another has written) or the row is
+// shorter.  bf16, 531 channels (one element an access otherwise): 98 MB 71 us
+// against 244, backward 117 against 283; 20 MB 28 against 51, 43 against 57; 10
+// MB 22 against 28, 34 against 33; 3 MB 18 against 14, 31 against 18.  252
+// channels (four elements): 100 MB 74 against 87, 10 MB 18 against 16.
+constexpr long long kRaggedBytes = 8 << 20;
+
+int row_width(const NormArgs& a, int elem, int out_elem) {
+    const int most = 16 / elem;
+    if (a.C < most || a.y == a.x || a.y == a.dy || (long long)a.N * a.P * a.C * elem < kRaggedBytes)
+        return vector_width(a, a.C, elem, out_elem);
+    return most;
+}
+
 struct Plan {
     int TX, R, block, chunks, pix;
 };
@@ -1107,7 +1130,7 @@ struct Plan {
 // once), at most kMaxChunks per image, of a whole number of pixels a thread.
 Plan make_plan(int N, int P, int C, int V) {
     Plan p;
-    const int cv = C / V;
+    const int cv = (C + V - 1) / V;
     p.TX = cv < 256 ? cv : 256;
     int best = 0;
     p.block = 256;
@@ -1175,7 +1198,7 @@ template <typename T, int V> hipError_t forward(const NormArgs& a, int act, void
 
 template <typename T, int V, int ACT> hipError_t quantised_apply(const NormArgs& a, const Plan& p, const float2* part,
                                                                  hipStream_t st) {
-    const int cv = a.C / V;
+    const int cv = (a.C + V - 1) / V;
     if (cv > 64) {
         const size_t lds = (size_t)a.G * 8 + (size_t)a.C * 12;
         int dev = 0;
@@ -1355,8 +1378,7 @@ template <typename T, int V> hipError_t joined_bwd(const NormArgs& a, int act, c
 // and channel, which is less).
 size_t group_norm_workspace(int N, int P, int C, int G, int backward) {
     size_t most = 0;
-    for (int v = 1; v <= 8; v <<= 1) {
-        if (C % v) break;
+    for (int v = 1; v <= 8 && v <= C; v <<= 1) {
         const Plan p = make_plan(N, P, C, v);
         const size_t bytes = (size_t)N * p.chunks * (G + (backward ? (size_t)C : 0)) * 8;
         most = bytes > most ? bytes : most;
@@ -1373,19 +1395,17 @@ size_t group_norm_workspace(int N, int P, int C, int G, int backward) {
 
 // Grids are one-dimensional: the largest must fit 2^31 - 1 workgroups.
 bool group_norm_supports(int N, int P, int C) {
-    for (int v = 1; v <= 8; v <<= 1) {
-        if (C % v) break;
+    for (int v = 1; v <= 8 && v <= C; v <<= 1) {
         if ((long long)N * make_plan(N, P, C, v).chunks + C >= 0x7fffffffLL) return false;
     }
     return true;
 }
 
-#define CONV2D_NORM_WIDTH(FN, UNIT, OUT_ELEM, ...)                                                  \
+#define CONV2D_NORM_WIDTH(FN, WIDTH, ...)                                                           \
+    const int v = WIDTH;                                                                            \
     if (a.dtype == 0 /* CONV2D_F32 */) {                                                            \
-        const int v = vector_width(a, UNIT, 4, OUT_ELEM ? OUT_ELEM : 4);                            \
         return v == 4 ? FN<float, 4>(__VA_ARGS__) : v == 2 ? FN<float, 2>(__VA_ARGS__) : FN<float, 1>(__VA_ARGS__); \
     }                                                                                               \
-    const int v = vector_width(a, UNIT, 2, OUT_ELEM ? OUT_ELEM : 2);                                \
     return v == 8 ? FN<bf16_t, 8>(__VA_ARGS__) : v == 4 ? FN<bf16_t, 4>(__VA_ARGS__)                \
            : v == 2 ? FN<bf16_t, 2>(__VA_ARGS__) : FN<bf16_t, 1>(__VA_ARGS__)
 
@@ -1406,29 +1426,29 @@ hipError_t launch_group_norm(const NormArgs& a, int act, void* ws, hipStream_t s
     const int elem = a.dtype == 0 ? 4 : 2, cg = a.C / a.G;
     const Resident p = make_resident(a, vector_width(a, cg, elem, elem), elem, 8);
     if (p.nv) {
-        CONV2D_NORM_WIDTH(forward_group, cg, 0, a, act, p, st);
+        CONV2D_NORM_WIDTH(forward_group, vector_width(a, cg, elem, elem), a, act, p, st);
     }
     const Joined j = make_joined(a, vector_width(a, a.C, elem, elem), elem, false, kJoinedMost);
     if (j.nv) return elem == 4 ? joined<float, 4, false>(a, act, j, ws, st) : joined<bf16_t, 8, false>(a, act, j, ws, st);
-    CONV2D_NORM_WIDTH(forward, a.C, 0, a, act, ws, st);
+    CONV2D_NORM_WIDTH(forward, row_width(a, elem, elem), a, act, ws, st);
 }
 
 hipError_t launch_group_norm_quant(const NormArgs& a, int act, void* ws, hipStream_t st) {
     const int elem = a.dtype == 0 ? 4 : 2;
     const Joined j = make_joined(a, vector_width(a, a.C, elem, 1), elem, true, kJoinedMost);
     if (j.nv) return elem == 4 ? joined<float, 4, true>(a, act, j, ws, st) : joined<bf16_t, 8, true>(a, act, j, ws, st);
-    CONV2D_NORM_WIDTH(quantised, a.C, 1, a, act, ws, st);
+    CONV2D_NORM_WIDTH(quantised, row_width(a, elem, 1), a, act, ws, st);
 }
 
 hipError_t launch_group_norm_bwd(const NormArgs& a, int act, void* ws, hipStream_t st) {
     const int elem = a.dtype == 0 ? 4 : 2, cg = a.C / a.G;
     const Resident p = make_resident(a, vector_width(a, cg, elem, elem), elem, 4);
     if (p.nv) {
-        CONV2D_NORM_WIDTH(backward_group, cg, 0, a, act, p, static_cast<float*>(ws), st);
+        CONV2D_NORM_WIDTH(backward_group, vector_width(a, cg, elem, elem), a, act, p, static_cast<float*>(ws), st);
     }
     const Joined j = make_joined(a, vector_width(a, cg, elem, elem), elem, false, kJoinedMostBwd);
     if (j.nv) return elem == 4 ? joined_bwd<float, 4>(a, act, j, ws, st) : joined_bwd<bf16_t, 8>(a, act, j, ws, st);
-    CONV2D_NORM_WIDTH(backward, a.C, 0, a, act, ws, st);
+    CONV2D_NORM_WIDTH(backward, row_width(a, elem, elem), a, act, ws, st);
 }
 
 }  // namespace conv2d

@@ -724,7 +724,7 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const T* x, int8_t* 
 #pragma unroll
     for (int j = 0; j < J; ++j) {
         const int c = (l + j * LPP) * V;
-        if (c < K) raw[j] = Vec<T, V>::load(p + c);
+        if (c < K) raw[j] = Vec<T, V>::load(p + vector_start<V>(c, K));
     }
 #pragma unroll
     for (int j = 0; j < J; ++j) {
@@ -737,7 +737,7 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(const T* x, int8_t* 
 #pragma unroll
     for (int j = 0; j < J; ++j) {
         const int c = (l + j * LPP) * V;
-        if (c < K) store_quantised<V>(q + row * ldq + c, v[j], s.inv);
+        if (c < K) store_quantised<V>(q + row * ldq + vector_start<V>(c, K), v[j], s.inv);
     }
     if (l == 0) scale[row] = s.scale;
 }
@@ -753,7 +753,7 @@ __global__ __launch_bounds__(256) void quantize_long_rows_kernel(const T* x, int
 #pragma unroll 4
     for (int c = threadIdx.x * V; c < K; c += 256 * V) {
         float v[V];
-        Vec<T, V>::unpack(Vec<T, V>::load(p + c), v);
+        Vec<T, V>::unpack(Vec<T, V>::load(p + vector_start<V>(c, K)), v);
 #pragma unroll
         for (int e = 0; e < V; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
     }
@@ -764,8 +764,9 @@ __global__ __launch_bounds__(256) void quantize_long_rows_kernel(const T* x, int
 #pragma unroll 4
     for (int c = threadIdx.x * V; c < K; c += 256 * V) {
         float v[V];
-        Vec<T, V>::unpack(Vec<T, V>::load(p + c), v);
-        store_quantised<V>(q + row * ldq + c, v, s.inv);
+        const int at = vector_start<V>(c, K);
+        Vec<T, V>::unpack(Vec<T, V>::load(p + at), v);
+        store_quantised<V>(q + row * ldq + at, v, s.inv);
     }
     if (threadIdx.x == 0) scale[row] = s.scale;
 }
@@ -982,12 +983,13 @@ hipError_t launch_int8_matmul(const Int8Args& a, int out_f32, void* ws, hipStrea
 
 hipError_t launch_quantize_rows(const void* x, void* q, float* scale, int M, int K, long long ldx, long long ldq,
                                 int dtype, hipStream_t st) {
+    // 16 bytes whatever the alignment, the last vector of a row over part of the
+    // one before, unless the row is shorter
     const int es = dtype == 0 /* CONV2D_F32 */ ? 4 : 2;
     int v = 16 / es;
-    while (v > 1 && !(K % v == 0 && ldx % v == 0 && ldq % v == 0 &&
-                      (reinterpret_cast<uintptr_t>(x) & (v * es - 1)) == 0 &&
-                      (reinterpret_cast<uintptr_t>(q) & (v - 1)) == 0))
-        v >>= 1;
+    while (v > K) v >>= 1;
+    if (v * es < 16)
+        while (K % v) v >>= 1;
     if (es == 4)
         return v == 4 ? quantize<float, 4>(x, q, scale, M, K, ldx, ldq, st)
                : v == 2 ? quantize<float, 2>(x, q, scale, M, K, ldx, ldq, st)

@@ -8,7 +8,7 @@
 namespace conv2d {
 
 // V consecutive elements of T in one load or store of V * sizeof(T) bytes
-// (2, 4, 8 or 16).
+// (2, 4, 8 or 16), aligned to one element at least.
 template <int BYTES> struct RawBytes;
 template <> struct RawBytes<16> { typedef uint4 type; };
 template <> struct RawBytes<8> { typedef uint2 type; };
@@ -18,9 +18,26 @@ template <> struct RawBytes<1> { typedef uint8_t type; };
 
 template <typename T, int V> struct Vec;
 
+// One access of any alignment.
+template <int BYTES> struct AnyAlign {
+    typedef typename RawBytes<BYTES>::type raw;
+    struct __attribute__((packed, may_alias)) type { raw v; };
+};
+template <int BYTES> __device__ __forceinline__ typename RawBytes<BYTES>::type load_bytes(const void* p) {
+    return static_cast<const typename AnyAlign<BYTES>::type*>(p)->v;
+}
+template <int BYTES> __device__ __forceinline__ void store_bytes(void* p, const typename RawBytes<BYTES>::type& v) {
+    static_cast<typename AnyAlign<BYTES>::type*>(p)->v = v;
+}
+
+// Where the vector of a row of C elements from element c on starts: the last one of a row
+// that is no multiple of V ends with the row and covers part of the one before
+// (whoever writes both writes the same values twice).
+template <int V> __device__ __forceinline__ int vector_start(int c, int C) { return min(c, C - V); }
+
 template <int V> struct Vec<float, V> {
     typedef typename RawBytes<4 * V>::type raw;
-    static __device__ __forceinline__ raw load(const float* p) { return *reinterpret_cast<const raw*>(p); }
+    static __device__ __forceinline__ raw load(const float* p) { return load_bytes<4 * V>(p); }
     static __device__ __forceinline__ void unpack(const raw& r, float (&v)[V]) {
         const uint32_t* w = reinterpret_cast<const uint32_t*>(&r);
 #pragma unroll
@@ -33,12 +50,12 @@ template <int V> struct Vec<float, V> {
         for (int j = 0; j < V; ++j) w[j] = __float_as_uint(v[j]);
         return r;
     }
-    static __device__ __forceinline__ void store(float* p, const float (&v)[V]) { *reinterpret_cast<raw*>(p) = pack(v); }
+    static __device__ __forceinline__ void store(float* p, const float (&v)[V]) { store_bytes<4 * V>(p, pack(v)); }
 };
 
 template <int V> struct Vec<bf16_t, V> {
     typedef typename RawBytes<2 * V>::type raw;
-    static __device__ __forceinline__ raw load(const bf16_t* p) { return *reinterpret_cast<const raw*>(p); }
+    static __device__ __forceinline__ raw load(const bf16_t* p) { return load_bytes<2 * V>(p); }
     static __device__ __forceinline__ void unpack(const raw& r, float (&v)[V]) {
         if constexpr (V == 1) {
             v[0] = bf16_to_f32(r);
@@ -63,7 +80,7 @@ template <int V> struct Vec<bf16_t, V> {
             return r;
         }
     }
-    static __device__ __forceinline__ void store(bf16_t* p, const float (&v)[V]) { *reinterpret_cast<raw*>(p) = pack(v); }
+    static __device__ __forceinline__ void store(bf16_t* p, const float (&v)[V]) { store_bytes<2 * V>(p, pack(v)); }
 };
 
 // 1 / (1 + exp(-z)) from the hardware's exp2 and reciprocal (1 ulp each).
@@ -171,7 +188,7 @@ __device__ __forceinline__ void store_quantised(int8_t* q, const float (&v)[V], 
         for (int j = 0; j < V; ++j) w |= (b[j] & 0xffu) << (8 * j);
         r = (raw)(inv == 0.0f ? 0u : w);
     }
-    *reinterpret_cast<raw*>(q) = r;
+    store_bytes<V>(q, r);
 }
 
 }  // namespace conv2d

@@ -171,3 +171,33 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for c, w in zip(cases, want):
         np.testing.assert_array_equal(c.host(c.y), w)
+
+
+# rows that 16-byte vectors do not divide or are not aligned to, read in such
+# vectors all the same where the tensor is large
+#          N   C   H    W   G  dtype  pad skip
+RAGGED = [(9, 531, 31, 29, 9, "bf16", 0, 0), (40, 9, 109, 107, 1, "bf16", 2, 1), (5, 258, 41, 40, 2, "f32", 1, 3),
+          (3, 2051, 27, 26, 7, "bf16", 0, 0)]
+
+
+@pytest.mark.parametrize("N,C,H,W,G,dtype,pad,skip", RAGGED)
+def test_ragged_rows(N, C, H, W, G, dtype, pad, skip):
+    say((N, C, H, W, G, dtype, pad, skip))
+    c = small.Case(N, C, H, W, G, 2, dtype, pad=pad, skip=skip)
+    c.forward()
+    small.check_forward(c, "forward")
+    dg, db = small.backward(c)
+    small.check_backward(c, dg, db, "backward")
+    assert c.y.untouched()
+    ws, n = c.workspace()
+    q = small.Padded(N * H * W, C, C + 1, 3, torch.int8, 77)
+    s = torch.full((N * H * W,), float("nan"), device="cuda")
+    c2.conv2d_group_norm_quant_nhwc(c.x.view, c.gd, c.bd, q.view, s, c.mean, c.rstd, ws, n, N, C, H, W, G, c.ld, C + 1,
+                                    small.EPS, small.lt(dtype), 2)
+    small.check_quantised(c, q, s, "quantised")
+    # x over itself, which takes other vectors: the same fp64 values
+    e = c.errors()
+    c2.conv2d_group_norm_nhwc(c.x.view, c.gd, c.bd, c.x.view, None, None, ws, n, N, C, H, W, G, c.ld, c.ld, small.EPS,
+                              small.lt(dtype), 2)
+    small.inside(c.host(c.x), e["y"], e["e_y"] + small.HALF[dtype] * (np.abs(e["y"]) + e["e_y"]), "in place")
+    assert c.x.untouched()
