@@ -1127,7 +1127,10 @@ struct Plan {
 // Threads: TX across the channel vectors, R rows of them, the block size of
 // 256 to 512 that leaves the fewest idle.  Chunks: kTargetBlocks workgroups
 // in all or a few less (two for each compute unit, of equal size: they run at
-// once), at most kMaxChunks per image, of a whole number of pixels a thread.
+// once), at most kMaxChunks per image, of a whole number of pixels a thread,
+// two at least where there are more than 64: the second launch waits for all of
+// an image's partials (4 images of 28x28x256, quantised and multiplied: 98
+// chunks 19.0 us, 49 14.6).
 Plan make_plan(int N, int P, int C, int V) {
     Plan p;
     const int cv = (C + V - 1) / V;
@@ -1142,6 +1145,7 @@ Plan make_plan(int N, int P, int C, int V) {
     long long k = kTargetBlocks / N;
     k = k < 1 ? 1 : k < kMaxChunks ? k : kMaxChunks;
     long long each = (P + k - 1) / k;
+    if (k > 64 && each < 2 * p.R) each = 2 * p.R;
     each = (each + p.R - 1) / p.R * p.R;
     p.pix = (int)(each < 0x7fffffff ? each : 0x7fffffff);
     p.chunks = (int)((P + (long long)p.pix - 1) / p.pix);
