@@ -14,7 +14,9 @@
 // Streaming, two launches.  The first reads the activations once and leaves
 // partial statistics per image, chunk of pixels and group in the workspace;
 // the second combines an image's partials (a few KB, from L2) in every
-// workgroup, then reads the activations again and writes the result.
+// workgroup, then reads the activations again and writes the result.  (The
+// quantised pass of small images: one launch, in which every workgroup takes
+// its image's statistics itself.)
 //
 // Resident, one launch: a workgroup loads one (image, group) whole into
 // registers, takes its statistics there and writes the result, so memory is
@@ -325,30 +327,15 @@ __global__ __launch_bounds__(512) void gn_apply_kernel(NormArgs a, int TX, int R
     }
 }
 
-// Second launch of the quantised forward pass.  LPP lanes (a power of two)
-// share a pixel, lane l holds the vectors l, l + LPP, ... of it.  LDS: G pairs.
-// One vector a lane: two pixels at a time, constants in registers.
-template <typename T, int V, int ACT>
-__global__ __launch_bounds__(256) void gn_quant_kernel(NormArgs a, int LPP, int chunks, int pix, const float2* part) {
-    extern __shared__ float2 lds[];
-    constexpr int B = 2;
-    const int n = blockIdx.x / chunks, piece = blockIdx.x - n * chunks;
-    const int sub = small_div(threadIdx.x, LPP), l = threadIdx.x - sub * LPP, subs = small_div(blockDim.x, LPP);
-    const bool in = l * V < a.C;
-    const int p0 = piece * pix, np = min(pix, a.P - p0), c = in ? vector_start<V>(l * V, a.C) : 0;
-    const Part part_of(np, subs, sub);
-    const long long first = (long long)n * a.P + p0 + part_of.first;
-    const int cnt = part_of.cnt;
+// Quantises a thread's `cnt` pixels, `subs` apart from pixel `first` on, B of
+// them at a time (the first B in b).  LPP lanes (a power of two) share a pixel;
+// a lane outside the row has nothing of it.
+template <typename T, int V, int ACT, int B, typename F>
+__device__ __forceinline__ void quantise_pixels(const NormArgs& a, const F& f, Batch<T, V, B>& b, long long first, int cnt,
+                                                int subs, int c, int l, bool in, int LPP) {
     const T* p = static_cast<const T*>(a.x) + first * a.ldx + c;
     int8_t* q = static_cast<int8_t*>(a.y) + first * a.ldy + c;
     const long long xs = (long long)subs * a.ldx, qs = (long long)subs * a.ldy;
-    Batch<T, V, B> b;
-    b.load(p, xs, 0, cnt);
-    Affine<T, V> f;
-    f.prepare(a, c);
-    combine_stats(part, a, n, chunks, pix, lds);
-    if (piece == 0) save_stats(a, lds, n);
-    finish_affine<Affine<T, V>, V>(f, lds, c, a.C / a.G);
 #pragma clang loop unroll(disable)
     for (int i = 0; i < cnt; i += B) {
         float v[B][V];
@@ -375,6 +362,75 @@ __global__ __launch_bounds__(256) void gn_quant_kernel(NormArgs a, int LPP, int 
             }
         }
     }
+}
+
+// Second launch of the quantised forward pass.  LPP lanes (a power of two)
+// share a pixel, lane l holds the vectors l, l + LPP, ... of it.  LDS: G pairs.
+// One vector a lane: two pixels at a time, constants in registers.
+template <typename T, int V, int ACT>
+__global__ __launch_bounds__(256) void gn_quant_kernel(NormArgs a, int LPP, int chunks, int pix, const float2* part) {
+    extern __shared__ float2 lds[];
+    constexpr int B = 2;
+    const int n = blockIdx.x / chunks, piece = blockIdx.x - n * chunks;
+    const int sub = small_div(threadIdx.x, LPP), l = threadIdx.x - sub * LPP, subs = small_div(blockDim.x, LPP);
+    const bool in = l * V < a.C;
+    const int p0 = piece * pix, np = min(pix, a.P - p0), c = in ? vector_start<V>(l * V, a.C) : 0;
+    const Part part_of(np, subs, sub);
+    const long long first = (long long)n * a.P + p0 + part_of.first;
+    const int cnt = part_of.cnt;
+    Batch<T, V, B> b;
+    b.load(static_cast<const T*>(a.x) + first * a.ldx + c, (long long)subs * a.ldx, 0, cnt);
+    Affine<T, V> f;
+    f.prepare(a, c);
+    combine_stats(part, a, n, chunks, pix, lds);
+    if (piece == 0) save_stats(a, lds, n);
+    finish_affine<Affine<T, V>, V>(f, lds, c, a.C / a.G);
+    quantise_pixels<T, V, ACT, B>(a, f, b, first, cnt, subs, c, l, in, LPP);
+}
+
+// The whole quantised pass in one launch, for small images: every workgroup
+// takes the statistics of its image itself, from the cache, rather than wait
+// for a launch that takes them.  LDS: R * C pairs, then G.
+template <typename T, int V, int ACT>
+__global__ __launch_bounds__(512) void gn_quant_whole_kernel(NormArgs a, int LPP, int chunks, int pix) {
+    extern __shared__ float2 lds[];
+    constexpr int B = 2, BS = 8;
+    const int n = blockIdx.x / chunks, piece = blockIdx.x - n * chunks;
+    const int sub = small_div(threadIdx.x, LPP), l = threadIdx.x - sub * LPP, subs = small_div(blockDim.x, LPP);
+    const bool in = l * V < a.C;
+    const int c = in ? vector_start<V>(l * V, a.C) : 0;
+    const long long image = (long long)n * a.P, step = (long long)subs * a.ldx;
+    Affine<T, V> f;
+    f.prepare(a, c);
+    {
+        const Part of(a.P, subs, sub);
+        const T* p = static_cast<const T*>(a.x) + (image + of.first) * a.ldx + c;
+        Moments<T, V> m;
+#pragma clang loop unroll(disable)
+        for (int i = 0; i == 0 || i < of.cnt; i += BS) {
+            Batch<T, V, BS> b;
+            b.load(p, step, i, of.cnt);
+            if (i == 0) m.start(b.raw[0]);
+#pragma unroll
+            for (int u = 0; u < BS; ++u) m.add(b.raw[u], i + u < of.cnt);
+        }
+        if (in) m.finish(of.cnt, lds + sub * a.C + c);
+    }
+    const int p0 = piece * pix, np = min(pix, a.P - p0);
+    const Part part_of(np, subs, sub);
+    const long long first = image + p0 + part_of.first;
+    Batch<T, V, B> b;
+    b.load(static_cast<const T*>(a.x) + first * a.ldx + c, step, 0, part_of.cnt);
+    __syncthreads();
+    float2* stat = lds + subs * a.C;
+    const float total = (float)a.P * (a.C / a.G);
+    merge_rows(lds, a, a.P, subs, [&](int g, float mean, float m2) {
+        stat[g] = make_float2(mean, 1.0f / sqrtf(m2 / total + a.eps));
+    });
+    __syncthreads();
+    if (piece == 0) save_stats(a, stat, n);
+    finish_affine<Affine<T, V>, V>(f, stat, c, a.C / a.G);
+    quantise_pixels<T, V, ACT, B>(a, f, b, first, part_of.cnt, subs, c, l, in, LPP);
 }
 
 // The same for pixels of more than 64 vectors: a wave per pixel, constants
@@ -1120,6 +1176,14 @@ int row_width(const NormArgs& a, int elem, int out_elem) {
     return most;
 }
 
+// The quantised pass in one launch: images of at most kWholeVectors vectors, no
+// more workgroups than compute units.  Through norm and product, against two
+// launches: 200 images of 8x8x64 (512 vectors) 11.9 us for 14.6, 32 of 14x14x256
+// (6272) 15.1 for 17.2; 3 of 16x7x512 (7168) 15.0 for 14.6, one of 28x28x128
+// (12544) 15.0 for 13.7.
+constexpr int kWholeThreads = 512, kWholeBlocks = 256;
+constexpr long long kWholeVectors = 6400;
+
 struct Plan {
     int TX, R, block, chunks, pix;
 };
@@ -1218,7 +1282,22 @@ template <typename T, int V, int ACT> hipError_t quantised_apply(const NormArgs&
     return hipGetLastError();
 }
 
+template <typename T, int V, int ACT> hipError_t quantised_whole(const NormArgs& a, hipStream_t st) {
+    int lpp = 1;
+    while (lpp * V < a.C) lpp <<= 1;
+    const int subs = kWholeThreads / lpp;
+    int chunks = kWholeBlocks / a.N;
+    int pix = (a.P + chunks - 1) / chunks;
+    pix = (pix + subs - 1) / subs * subs;
+    chunks = (a.P + pix - 1) / pix;
+    gn_quant_whole_kernel<T, V, ACT><<<a.N * chunks, kWholeThreads, ((size_t)subs * a.C + a.G) * 8, st>>>(a, lpp, chunks, pix);
+    return hipGetLastError();
+}
+
 template <typename T, int V> hipError_t quantised(const NormArgs& a, int act, void* ws, hipStream_t st) {
+    if (a.N <= kWholeBlocks && (a.C + V - 1) / V <= 64 && (long long)a.P * ((a.C + V - 1) / V) <= kWholeVectors)
+        return act == kActSilu ? quantised_whole<T, V, kActSilu>(a, st)
+               : act == kActRelu ? quantised_whole<T, V, kActRelu>(a, st) : quantised_whole<T, V, kActNone>(a, st);
     const Plan p = make_plan(a.N, a.P, a.C, V);
     float2* part = static_cast<float2*>(ws);
     gn_stats_kernel<T, V><<<a.N * p.chunks, p.block, (size_t)p.R * a.C * 8, st>>>(a, p.TX, p.R, p.chunks, p.pix, part);
