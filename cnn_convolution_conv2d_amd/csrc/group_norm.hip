@@ -625,7 +625,7 @@ __device__ __forceinline__ void stream_slopes(const NormArgs& a, int n, int c, l
 // First launch of the streaming backward pass: for every image and chunk the
 // sums of dz and dz * xh per channel (pc: [block][2][C]) and, weighted with
 // gamma, per group (pg).  LDS: R * C pairs.
-template <typename T, int V, int ACT>
+template <typename T, int V, int ACT, int NB>
 __global__ __launch_bounds__(512) void gn_bwd_sums_kernel(NormArgs a, int TX, int R, int chunks, int pix, float* pc,
                                                           float2* pg) {
     extern __shared__ float2 lds[];
@@ -637,7 +637,7 @@ __global__ __launch_bounds__(512) void gn_bwd_sums_kernel(NormArgs a, int TX, in
         const long long first = (long long)n * a.P + p0 + part_of.first;
         for (int at = tx * V; at < a.C; at += TX * V) {
             const int c = vector_start<V>(at, a.C);
-            stream_slopes<T, V, ACT, Slope<V>>(a, n, c, first, part_of.cnt, R, lds + r * a.C + c);
+            stream_slopes<T, V, ACT, Slope<V>, NB>(a, n, c, first, part_of.cnt, R, lds + r * a.C + c);
         }
     }
     __syncthreads();
@@ -681,7 +681,7 @@ __device__ __forceinline__ void sum_params(const NormArgs& a, const float* pc, l
 // Second launch of the streaming backward pass.  The first `sums` workgroups
 // add the channels' partials into dgamma and dbeta, the others write dx, one
 // per image and chunk.  LDS: max(G, blockDim.x) pairs.
-template <typename T, int V, int ACT>
+template <typename T, int V, int ACT, int NB>
 __global__ __launch_bounds__(512) void gn_bwd_apply_kernel(NormArgs a, int TX, int R, int chunks, int pix, int sums,
                                                            const float* pc, const float2* pg) {
     extern __shared__ float2 lds[];
@@ -698,7 +698,7 @@ __global__ __launch_bounds__(512) void gn_bwd_apply_kernel(NormArgs a, int TX, i
     const long long first = (long long)n * a.P + p0 + part_of.first;
     const int cnt = part_of.cnt, c0 = vector_start<V>(tx * V, a.C);
     const long long xs = (long long)R * a.ldx, ds = (long long)R * a.lddy, os = (long long)R * a.ldy;
-    Batch<T, V, kBatchBwd> bx, bd;
+    Batch<T, V, NB> bx, bd;
     bx.load(static_cast<const T*>(a.x) + first * a.ldx + c0, xs, 0, cnt);
     bd.load(static_cast<const T*>(a.dy) + first * a.lddy + c0, ds, 0, cnt);
     Slope<V> f;
@@ -723,7 +723,7 @@ __global__ __launch_bounds__(512) void gn_bwd_apply_kernel(NormArgs a, int TX, i
 #pragma clang loop unroll(disable)
     for (int at = tx * V, i = 0; cnt > 0;) {
 #pragma unroll
-        for (int u = 0; u < kBatchBwd; ++u) {
+        for (int u = 0; u < NB; ++u) {
             float x[V], d[V];
             Vec<T, V>::unpack(bx.raw[u], x);
             Vec<T, V>::unpack(bd.raw[u], d);
@@ -734,7 +734,7 @@ __global__ __launch_bounds__(512) void gn_bwd_apply_kernel(NormArgs a, int TX, i
             }
             if (i + u < cnt) Vec<T, V>::store(po + (i + u) * os, d);
         }
-        i += kBatchBwd;
+        i += NB;
         if (i >= cnt) {
             at += TX * V;
             if (at >= a.C) break;
@@ -752,6 +752,13 @@ __global__ __launch_bounds__(512) void gn_bwd_apply_kernel(NormArgs a, int TX, i
 }
 
 // ------------------------------------------------------------------ resident
+
+// What the compiler knows of a vector ends here: it would keep the values that
+// it unpacked before, twice the registers, rather than unpack them again.
+__device__ __forceinline__ void forget(uint4& v) { asm("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w)); }
+__device__ __forceinline__ void forget(uint2& v) { asm("" : "+v"(v.x), "+v"(v.y)); }
+__device__ __forceinline__ void forget(uint32_t& v) { asm("" : "+v"(v)); }
+__device__ __forceinline__ void forget(uint16_t&) {}
 
 // Sums over the workgroup; every thread gets them.  LDS: 2 * 16 floats, not
 // in use by an earlier call.
@@ -857,6 +864,10 @@ __global__ __launch_bounds__(1024) void gn_bwd_resident_kernel(NormArgs a, int T
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
         float x[V], d[V];
+        if constexpr (sizeof(T) == 2) {
+            forget(bx.raw[u]);
+            forget(bd.raw[u]);
+        }
         Vec<T, V>::unpack(bx.raw[u], x);
         Vec<T, V>::unpack(bd.raw[u], d);
 #pragma unroll
@@ -973,10 +984,6 @@ template <int NV> struct Chunk {
         for (int u = 0; u < NV; ++u) v[u] = load16(rows, (int)(at + u * step));
     }
 };
-
-// What the compiler knows of a vector ends here: it would keep the values that
-// it unpacked before, twice the registers, rather than unpack them again.
-__device__ __forceinline__ void forget(uint4& v) { asm("" : "+v"(v.x), "+v"(v.y), "+v"(v.z), "+v"(v.w)); }
 
 // Forward (QUANT: with the quantisation of every pixel, whose vectors are then
 // TX lanes, a power of two, of one wave).  LDS: R * C pairs, or the image's
@@ -1333,11 +1340,16 @@ template <typename T, int V, int ACT> hipError_t backward_act(const NormArgs& a,
     const long long blocks = (long long)a.N * p.chunks;
     float2* pg = static_cast<float2*>(ws);
     float* pc = reinterpret_cast<float*>(pg + blocks * a.G);
-    gn_bwd_sums_kernel<T, V, ACT><<<(int)blocks, p.block, (size_t)p.R * a.C * 8, st>>>(a, p.TX, p.R, p.chunks, p.pix,
-                                                                                      pc, pg);
+    // threads of one or two pixels take them one by one: a batch of four would do
+    // the arithmetic of four, with four times the code to fetch (15 images of
+    // 18x46x108 in fp32: 13.4 us for 14.6; forward, with little of either, even)
+    const bool few = p.pix <= 2 * p.R;
+    auto first = few ? gn_bwd_sums_kernel<T, V, ACT, 1> : gn_bwd_sums_kernel<T, V, ACT, kBatchBwd>;
+    first<<<(int)blocks, p.block, (size_t)p.R * a.C * 8, st>>>(a, p.TX, p.R, p.chunks, p.pix, pc, pg);
     const int sums = a.dgamma || a.dbeta ? (a.C + kParamChannels - 1) / kParamChannels : 0;
     const size_t lds = (size_t)(a.G > p.block ? a.G : p.block) * 8;
-    gn_bwd_apply_kernel<T, V, ACT><<<sums + (int)blocks, p.block, lds, st>>>(a, p.TX, p.R, p.chunks, p.pix, sums, pc, pg);
+    auto second = few ? gn_bwd_apply_kernel<T, V, ACT, 1> : gn_bwd_apply_kernel<T, V, ACT, kBatchBwd>;
+    second<<<sums + (int)blocks, p.block, lds, st>>>(a, p.TX, p.R, p.chunks, p.pix, sums, pc, pg);
     return hipGetLastError();
 }
 

@@ -19,15 +19,13 @@ template <> struct RawBytes<1> { typedef uint8_t type; };
 template <typename T, int V> struct Vec;
 
 // One access of any alignment.
-template <int BYTES> struct AnyAlign {
-    typedef typename RawBytes<BYTES>::type raw;
-    struct __attribute__((packed, may_alias)) type { raw v; };
-};
 template <int BYTES> __device__ __forceinline__ typename RawBytes<BYTES>::type load_bytes(const void* p) {
-    return static_cast<const typename AnyAlign<BYTES>::type*>(p)->v;
+    typename RawBytes<BYTES>::type v;
+    __builtin_memcpy(&v, p, BYTES);
+    return v;
 }
 template <int BYTES> __device__ __forceinline__ void store_bytes(void* p, const typename RawBytes<BYTES>::type& v) {
-    static_cast<typename AnyAlign<BYTES>::type*>(p)->v = v;
+    __builtin_memcpy(p, &v, BYTES);
 }
 
 // Where the vector of a row of C elements from element c on starts: the last one of a row
