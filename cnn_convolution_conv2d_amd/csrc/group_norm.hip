@@ -36,11 +36,15 @@
 // threads side by side, so its per-channel constants stay in registers and a
 // row of threads reads whole consecutive lines.
 //
-// Statistics in fp32.  Streaming: a thread sums x - k and (x - k)^2 with k its
-// first value of the channel, which bounds the cancellation in
-// M2 = ss - s^2/n by the (small) count of its values whatever the mean is;
-// partial means and M2 are then merged by the exact identity
-//   M2 = sum(M2_i) + sum(n_i * (mean_i - mean)^2).
+// Statistics.  Streaming and joined: a thread sums d = x - k and d^2, k its
+// first value of the channel, and M2 = sum(d^2) - sum(d)^2 / n; partial means and
+// M2 are merged the same way, with d = mean_i - mean_0 weighted by the counts,
+// and the M2_i added.  Where what lies first (a channel, a pixel, a chunk) is far
+// from the rest, sum(d^2) exceeds M2 by up to the count, and fp32 sums would lose
+// as much (196 pixels of 4096 channels, the first one at 300: rstd off by 3e-5):
+// the sums are fp64, and each partial result is rounded to fp32 once.  That costs
+// 1 to 3% of a large tensor's time (112x112x128 over 32 images 56.7 us for 55.2)
+// and up to 1.2 us of a small one's.
 // Resident: the deviations from the mean itself, in a second pass over the
 // registers.
 #include "mfma.hpp"
@@ -74,6 +78,13 @@ struct Part {
     }
 };
 
+// 1 / n to 2^-45 of itself: the hardware's reciprocal and one Newton step (the
+// division is three times the code).
+__device__ __forceinline__ double inverse(double n) {
+    const double r = __builtin_amdgcn_rcp(n);
+    return fma(fma(-n, r, 1.0), r, r);
+}
+
 // Threads that work on one of `count` things together: 2^lanes_per of them,
 // at most 64, such that the block covers all of them in one go where it can.
 __device__ __forceinline__ int lanes_per(int count) {
@@ -95,17 +106,15 @@ template <typename T, int V, int B> struct Batch {
 
 // Combines an image's chunk partials (mean, M2) into mean and rstd in LDS, in
 // one pass: with d = mean_i - mean_0, M2 = sum(M2_i) + sum(n d^2) - sum(n d)^2 / N.
-// Chunk 0's own distance from the mean is part of M2, which bounds the
-// cancellation by the number of chunks.
 __device__ __forceinline__ void combine_stats(const float2* part, const NormArgs& a, int n, int chunks, int pix,
                                               float2* stat) {
     const int cg = a.C / a.G, lg = lanes_per(a.G), L = 1 << lg, lane = threadIdx.x & (L - 1);
-    const float last = (float)(a.P - (chunks - 1) * pix) * cg, full = (float)pix * cg;
-    const float total = (float)a.P * cg;
+    const double last = (double)(a.P - (chunks - 1) * pix) * cg, full = (double)pix * cg;
+    const double inv = inverse((double)a.P * cg);
     for (int g = threadIdx.x >> lg; g < a.G; g += blockDim.x >> lg) {
         const float2* p = part + (long long)n * chunks * a.G + g;
         const float base = p[0].x;
-        float s = 0.0f, ss = 0.0f;
+        double s = 0.0, ss = 0.0;
         for (int j0 = lane; j0 < chunks; j0 += 4 * L) {
             float2 e[4];
 #pragma unroll
@@ -113,47 +122,50 @@ __device__ __forceinline__ void combine_stats(const float2* part, const NormArgs
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int j = j0 + u * L;
-                const float w = j >= chunks ? 0.0f : j == chunks - 1 ? last : full, d = e[u].x - base;
-                s = fmaf(w, d, s);
-                ss += fmaf(w * d, d, j >= chunks ? 0.0f : e[u].y);
+                const double w = j >= chunks ? 0.0 : j == chunks - 1 ? last : full, d = (double)e[u].x - base;
+                s = fma(w, d, s);
+                ss += fma(w * d, d, (double)(j >= chunks ? 0.0f : e[u].y));
             }
         }
         s = lanes_sum(s, L);
         ss = lanes_sum(ss, L);
-        const float shift = s / total, m2 = ss - s * shift;
+        const double shift = s * inv;
+        const float var = (float)((ss - s * shift) * inv);
         if (lane == 0)
-            stat[g] = make_float2(base + shift, 1.0f / sqrtf((m2 < 0.0f ? 0.0f : m2) / total + a.eps));  // a NaN stays
+            stat[g] = make_float2((float)(base + shift), 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + a.eps));  // a NaN stays
     }
     __syncthreads();
 }
 
 // A thread's running sums of x - k and (x - k)^2 for its V channels, k the first
-// value of each; finish: (mean, M2) of `cnt` values to LDS.
+// value of each; finish: (mean, M2) of `cnt` values to LDS, (0, 0) of none.
 template <typename T, int V> struct Moments {
     typename Vec<T, V>::raw first;
-    float k[V], s[V], ss[V];
+    float k[V];
+    double s[V], ss[V];
     __device__ __forceinline__ void start(const typename Vec<T, V>::raw& f) {
         first = f;
         Vec<T, V>::unpack(f, k);
 #pragma unroll
-        for (int j = 0; j < V; ++j) s[j] = ss[j] = 0.0f;
+        for (int j = 0; j < V; ++j) s[j] = ss[j] = 0.0;
     }
     __device__ __forceinline__ void add(const typename Vec<T, V>::raw& r, bool inside) {
         float v[V];
         Vec<T, V>::unpack(inside ? r : first, v);   // past the end: adds nothing
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const float d = v[j] - k[j];
+            const double d = (double)v[j] - k[j];
             s[j] += d;
-            ss[j] = fmaf(d, d, ss[j]);
+            ss[j] = fma(d, d, ss[j]);
         }
     }
     __device__ __forceinline__ void finish(int cnt, float2* out) const {
-        const float inv = cnt > 0 ? 1.0f / cnt : 0.0f;
+        const double inv = cnt > 0 ? inverse(cnt) : 0.0;
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const float d = s[j] * inv, m2 = ss[j] - s[j] * d;
-            out[j] = make_float2(k[j] + d, m2 < 0.0f ? 0.0f : m2);  // a NaN stays
+            const double d = s[j] * inv;
+            const float m2 = (float)(ss[j] - s[j] * d);
+            out[j] = make_float2(cnt > 0 ? (float)(k[j] + d) : 0.0f, m2 < 0.0f ? 0.0f : m2);  // a NaN stays
         }
     }
 };
@@ -181,25 +193,26 @@ template <typename PUT>
 __device__ __forceinline__ void merge_rows(const float2* lds, const NormArgs& a, int np, int R, PUT put) {
     const int cg = a.C / a.G, lg = lanes_per(a.G), L = 1 << lg, lane = threadIdx.x & (L - 1);
     const int few = np / R, more = np - few * R, count = R * cg;
+    const double inv = inverse((double)np * cg);
     for (int g = threadIdx.x >> lg; g < a.G; g += blockDim.x >> lg) {
         const float2* e = lds + g * cg;
         const float base = e[0].x;
-        float s = 0.0f, ss = 0.0f;
+        double s = 0.0, ss = 0.0;
         for (int k0 = lane; k0 < count; k0 += 4 * L) {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int k = min(k0 + u * L, count - 1), row = small_div(k, cg);
                 const float2 v = e[row * a.C + k - row * cg];
-                const int w = k0 + u * L < count ? few + (row < more) : 0;   // rows without values hold (0, 0)
-                const float d = v.x - base;
-                s = fmaf((float)w, d, s);
-                ss += w ? fmaf(w * d, d, v.y) : 0.0f;
+                const bool in = k0 + u * L < count;   // rows without values hold (0, 0)
+                const double w = in ? few + (row < more) : 0, d = (double)v.x - base;
+                s = fma(w, d, s);
+                ss += fma(w * d, d, (double)(in ? v.y : 0.0f));
             }
         }
         s = lanes_sum(s, L);
         ss = lanes_sum(ss, L);
-        const float shift = s / ((float)np * cg), mean = base + shift;
-        const float m2 = ss - s * shift;
+        const double shift = s * inv;
+        const float mean = (float)(base + shift), m2 = (float)(ss - s * shift);
         if (lane == 0) put(g, mean, m2 < 0.0f ? 0.0f : m2);   // a NaN stays
     }
 }
@@ -985,6 +998,12 @@ template <int NV> struct Chunk {
     }
 };
 
+// Channels h .. h + 3 of a 16-byte vector.
+template <typename T> __device__ __forceinline__ typename Vec<T, 4>::raw four_of(const uint4& v, int h) {
+    if constexpr (sizeof(T) == 4) return v;
+    else return h ? make_uint2(v.z, v.w) : make_uint2(v.x, v.y);
+}
+
 // Forward (QUANT: with the quantisation of every pixel, whose vectors are then
 // TX lanes, a power of two, of one wave).  LDS: R * C pairs, or the image's
 // words and G pairs if those are more.
@@ -1002,15 +1021,17 @@ __global__ __launch_bounds__(256, 4) void gn_joined_kernel(NormArgs a, int TX, i
     words += (long long)n * chunks * a.G;
     uint4 raw[NV];
     Chunk<NV>(a.x, image + p0, a.ldx, sizeof(T), np, a.C, R, r, c, in).load(raw);
-    {
-        Moments<T, V> m;
-        m.start(raw[0]);
+    constexpr int H = 4;   // channels at a time: all of bf16's, in fp64, would push out 61 registers
+#pragma unroll
+    for (int h = 0; h < V; h += H) {
+        Moments<T, H> m;
+        m.start(four_of<T>(raw[0], h));
 #pragma unroll
         for (int u = 0; u < NV; ++u) {
-            m.add(raw[u], u < cnt);
+            m.add(four_of<T>(raw[u], h), u < cnt);
             one_by_one();
         }
-        if (in) m.finish(cnt, lds + r * a.C + c);
+        if (in) m.finish(cnt, lds + r * a.C + c + h);
     }
     __syncthreads();
     merge_rows(lds, a, np, R, [&](int g, float mean, float m2) { put_word(words + chunk * a.G + g, pair_word(mean, m2)); });

@@ -133,6 +133,28 @@ __device__ __forceinline__ float lanes_sum(float v, int L) {
         return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
     }));
 }
+// The same in fp64, for L on every lane of the wave: the two halves of a value
+// move side by side.
+__device__ __forceinline__ double lanes_sum(double v, int L) {
+    const auto join = [](uint32_t lo, uint32_t hi) {
+        return __builtin_bit_cast(double, (unsigned long long)hi << 32 | lo);
+    };
+    const auto lo = [&] { return (uint32_t)__builtin_bit_cast(unsigned long long, v); };
+    const auto hi = [&] { return (uint32_t)(__builtin_bit_cast(unsigned long long, v) >> 32); };
+    if (L > 1) v += join(other_half<1>(lo()), other_half<1>(hi()));
+    if (L > 2) v += join(other_half<2>(lo()), other_half<2>(hi()));
+    if (L > 4) v += join(other_half<4>(lo()), other_half<4>(hi()));
+    if (L > 8) v += join(other_half<8>(lo()), other_half<8>(hi()));
+    if (L > 16) {
+        const u32x2_t p = rows_of_16(lo()), q = rows_of_16(hi());
+        v = join(p.x, q.x) + join(p.y, q.y);
+    }
+    if (L > 32) {
+        const u32x2_t p = halves_of_32(lo()), q = halves_of_32(hi());
+        v = join(p.x, q.x) + join(p.y, q.y);
+    }
+    return v;
+}
 __device__ __forceinline__ uint32_t lanes_max(uint32_t v, int L) {
     return lanes_reduce(v, L, [](uint32_t a, uint32_t b) { return max(a, b); });
 }

@@ -310,7 +310,8 @@ int conv2d_transpose_select_path(int N, int Cin, int H, int W, int Cout, int Kh,
  * with act none, ReLU or SiLU (z / (1 + exp(-z))), m = H*W*C/G.  x, y, dy and
  * dx are fp32 or bf16 (dtype), [N][H][W] pixels of C channels; ldx, ldy, lddy,
  * lddx: elements from one pixel to the next (>= C; images follow each other at
- * H*W of them).  Everything in between is fp32, each output is rounded once.
+ * H*W of them).  Everything in between is fp32, the sums of the statistics
+ * wider where values lie far apart, each output is rounded once.
  *
  * conv2d_group_norm_nhwc -- y, and mean and rstd (fp32 [N][G]; either may be
  *   NULL when it is not wanted).  y may be x itself (ldy == ldx).
