@@ -45,8 +45,8 @@
 // the sums are fp64, and each partial result is rounded to fp32 once.  That costs
 // 1 to 3% of a large tensor's time (112x112x128 over 32 images 56.7 us for 55.2)
 // and up to 1.2 us of a small one's.
-// Resident: the deviations from the mean itself, in a second pass over the
-// registers.
+// Resident: the mean from an fp64 sum, then the deviations from it in a second
+// pass over the registers.
 #include "mfma.hpp"
 #include "rowvec.hpp"
 
@@ -238,12 +238,10 @@ __global__ __launch_bounds__(512) void gn_stats_kernel(NormArgs a, int TX, int R
     });
 }
 
-// A thread's constants for its V channels.  bf16 activations carry 8 bits, so
-// z = x * (rstd gamma) + (beta - mean rstd gamma), whose error is 2^-24 of
-// |mean| rstd, cannot lose what their own rounding kept; fp32 ones subtract
-// the mean first.
-template <typename T, int V> struct Affine;
-template <int V> struct Affine<float, V> {
+// A thread's constants for its V channels.  The mean is subtracted first: x *
+// (rstd gamma) + (beta - mean rstd gamma) takes one instruction less, but is off
+// by 2^-24 of |mean| rstd gamma, 0.02 in a group that is constant at 1000.
+template <int V> struct Affine {
     float mean[V], rg[V], beta[V];
     __device__ __forceinline__ void prepare(const NormArgs& a, int c) {
 #pragma unroll
@@ -258,23 +256,8 @@ template <int V> struct Affine<float, V> {
     }
     __device__ __forceinline__ float z(float x, int j) const { return fmaf(x - mean[j], rg[j], beta[j]); }
 };
-template <int V> struct Affine<bf16_t, V> {
-    float rg[V], shift[V];
-    __device__ __forceinline__ void prepare(const NormArgs& a, int c) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            rg[j] = a.gamma ? a.gamma[c + j] : 1.0f;
-            shift[j] = a.beta ? a.beta[c + j] : 0.0f;
-        }
-    }
-    __device__ __forceinline__ void finish(float m, float r, int j) {
-        rg[j] *= r;
-        shift[j] = fmaf(-m, rg[j], shift[j]);
-    }
-    __device__ __forceinline__ float z(float x, int j) const { return fmaf(x, rg[j], shift[j]); }
-};
 // the same from the groups' (mean, rstd)
-template <typename A, int V> __device__ __forceinline__ void finish_affine(A& f, const float2* stat, int c, int cg) {
+template <int V> __device__ __forceinline__ void finish_affine(Affine<V>& f, const float2* stat, int c, int cg) {
     int g = small_div(c, cg), left = (g + 1) * cg - c;   // channels of group g from c on
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -308,13 +291,13 @@ __global__ __launch_bounds__(512) void gn_apply_kernel(NormArgs a, int TX, int R
     const long long xs = (long long)R * a.ldx, ys = (long long)R * a.ldy;
     Batch<T, V, kBatch> b;
     b.load(static_cast<const T*>(a.x) + first * a.ldx + c0, xs, 0, cnt);
-    Affine<T, V> f;
+    Affine<V> f;
     f.prepare(a, c0);
     combine_stats(part, a, n, chunks, pix, lds);
     if (piece == 0) save_stats(a, lds, n);
     const T* p = static_cast<const T*>(a.x) + first * a.ldx + c0;
     T* q = static_cast<T*>(a.y) + first * a.ldy + c0;
-    finish_affine<Affine<T, V>, V>(f, lds, c0, a.C / a.G);
+    finish_affine<V>(f, lds, c0, a.C / a.G);
 #pragma clang loop unroll(disable)
     for (int at = tx * V, i = 0; cnt > 0;) {
 #pragma unroll
@@ -334,7 +317,7 @@ __global__ __launch_bounds__(512) void gn_apply_kernel(NormArgs a, int TX, int R
             p = static_cast<const T*>(a.x) + first * a.ldx + c;
             q = static_cast<T*>(a.y) + first * a.ldy + c;
             f.prepare(a, c);
-            finish_affine<Affine<T, V>, V>(f, lds, c, a.C / a.G);
+            finish_affine<V>(f, lds, c, a.C / a.G);
         }
         b.load(p, xs, i, cnt);
     }
@@ -393,11 +376,11 @@ __global__ __launch_bounds__(256) void gn_quant_kernel(NormArgs a, int LPP, int 
     const int cnt = part_of.cnt;
     Batch<T, V, B> b;
     b.load(static_cast<const T*>(a.x) + first * a.ldx + c, (long long)subs * a.ldx, 0, cnt);
-    Affine<T, V> f;
+    Affine<V> f;
     f.prepare(a, c);
     combine_stats(part, a, n, chunks, pix, lds);
     if (piece == 0) save_stats(a, lds, n);
-    finish_affine<Affine<T, V>, V>(f, lds, c, a.C / a.G);
+    finish_affine<V>(f, lds, c, a.C / a.G);
     quantise_pixels<T, V, ACT, B>(a, f, b, first, cnt, subs, c, l, in, LPP);
 }
 
@@ -413,7 +396,7 @@ __global__ __launch_bounds__(512) void gn_quant_whole_kernel(NormArgs a, int LPP
     const bool in = l * V < a.C;
     const int c = in ? vector_start<V>(l * V, a.C) : 0;
     const long long image = (long long)n * a.P, step = (long long)subs * a.ldx;
-    Affine<T, V> f;
+    Affine<V> f;
     f.prepare(a, c);
     {
         const Part of(a.P, subs, sub);
@@ -442,7 +425,7 @@ __global__ __launch_bounds__(512) void gn_quant_whole_kernel(NormArgs a, int LPP
     });
     __syncthreads();
     if (piece == 0) save_stats(a, stat, n);
-    finish_affine<Affine<T, V>, V>(f, stat, c, a.C / a.G);
+    finish_affine<V>(f, stat, c, a.C / a.G);
     quantise_pixels<T, V, ACT, B>(a, f, b, first, part_of.cnt, subs, c, l, in, LPP);
 }
 
@@ -792,10 +775,23 @@ __device__ __forceinline__ float2 block_sum(float s, float t, float* lds) {
     return make_float2(s, t);
 }
 
+// One fp64 sum.  LDS: 16 doubles, not in use by an earlier call.
+__device__ __forceinline__ double block_sum(double s, double* lds) {
+    s = lanes_sum(s, 64);
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = s;
+    __syncthreads();
+    s = 0.0;
+    for (int w = 0; w < (int)(blockDim.x >> 6); ++w) s += lds[w];
+    return s;
+}
+
 // Forward: one workgroup per (image, group), NV vectors of it in each thread.
+// The mean from an fp64 sum, so that a constant group's is its value: the
+// deviations are multiplied with rstd, up to 1 / sqrt(eps).
 template <typename T, int V, int ACT, int NV>
 __global__ __launch_bounds__(1024) void gn_resident_kernel(NormArgs a, int TX, int R) {
-    __shared__ float lds[3][32];
+    __shared__ double lds64[16];
+    __shared__ float lds[32];
     const int b = xcd_tile_index(), n = b / a.G, g = b - n * a.G, cg = a.C / a.G;
     const int r = small_div(threadIdx.x, TX), tx = threadIdx.x - r * TX, c = g * cg + tx * V;
     const Part part_of(a.P, R, r);
@@ -803,19 +799,21 @@ __global__ __launch_bounds__(1024) void gn_resident_kernel(NormArgs a, int TX, i
     const int cnt = part_of.cnt;
     Batch<T, V, NV> x;
     x.load(static_cast<const T*>(a.x) + first * a.ldx + c, (long long)R * a.ldx, 0, cnt);
-    Affine<T, V> f;
+    Affine<V> f;
     f.prepare(a, c);
-    float s = 0.0f;
+    double total = 0.0;
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
-        float v[V], t = 0.0f;
+        float v[V];
         Vec<T, V>::unpack(x.raw[u], v);
+        double t = v[0];
 #pragma unroll
-        for (int j = 0; j < V; ++j) t += v[j];
-        s += u < cnt ? t : 0.0f;
+        for (int j = 1; j < V; ++j) t += v[j];
+        total += u < cnt ? t : 0.0;
     }
-    const float m = (float)a.P * cg, mean = block_sum(s, 0.0f, lds[0]).x / m;
-    s = 0.0f;
+    const double inv = inverse((double)a.P * cg);
+    const float mean = (float)(block_sum(total, lds64) * inv);
+    float s = 0.0f;
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
         float v[V], t = 0.0f;
@@ -824,7 +822,7 @@ __global__ __launch_bounds__(1024) void gn_resident_kernel(NormArgs a, int TX, i
         for (int j = 0; j < V; ++j) t = fmaf(v[j] - mean, v[j] - mean, t);
         s += u < cnt ? t : 0.0f;
     }
-    const float rstd = 1.0f / sqrtf(block_sum(s, 0.0f, lds[1]).x / m + a.eps);
+    const float rstd = 1.0f / sqrtf(block_sum(s, 0.0f, lds).x / ((float)a.P * cg) + a.eps);
     if (threadIdx.x == 0) {
         if (a.mean) a.mean[b] = mean;
         if (a.rstd) a.rstd[b] = rstd;
@@ -1047,12 +1045,12 @@ __global__ __launch_bounds__(256, 4) void gn_joined_kernel(NormArgs a, int TX, i
         merge_rows(lds, a, nq, R, [&](int g, float mean, float m2) { put_word(words + other * a.G + g, pair_word(mean, m2)); });
         __syncthreads();
     });
-    Affine<T, V> f;
+    Affine<V> f;
     f.prepare(a, c);
     float2* stat = lds + chunks * a.G;
     combine_stats(lds, a, 0, chunks, pix, stat);
     if (chunk == 0) save_stats(a, stat, n);
-    finish_affine<Affine<T, V>, V>(f, stat, c, a.C / a.G);
+    finish_affine<V>(f, stat, c, a.C / a.G);
     const Chunk<NV> out(a.y, image + p0, a.ldy, QUANT ? 1 : sizeof(T), np, a.C, R, r, c, in);
 #pragma unroll
     for (int u = 0; u < NV; ++u) {
