@@ -874,7 +874,7 @@ int conv2d_int8_matmul(const void* q, const float* q_scale, const void* w, const
     if (reinterpret_cast<uintptr_t>(y) % elem_bytes(dtype))
         return set_error(CONV2D_ERR_ALIGN, "y is not aligned to its elements");
     if (!int8_matmul_supports(M, K, N, ldq, ldw))
-        return set_error(CONV2D_ERR_UNSUPPORTED, "int8 products take K <= 131071 and row strides up to 2^22");
+        return set_error(CONV2D_ERR_UNSUPPORTED, "int8 products take K <= 131071, N <= 2^27 and row strides up to 2^22");
     const size_t need = conv2d_int8_matmul_workspace_bytes(M, K, N);
     if (need) {
         if (!workspace) return set_error(CONV2D_ERR_NULL, "the workspace is NULL (%zu bytes needed)", need);

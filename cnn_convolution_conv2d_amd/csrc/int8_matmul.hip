@@ -948,24 +948,51 @@ size_t split_bytes(const Int8Plan& p, int M, int N) {
 
 }  // namespace
 
+// The most rows of one launch (more are taken in equal parts) and the most
+// channels: indexes stay below 2^31 past the end of the last tile too.
+constexpr int kMostRows = 1 << 29, kMostChannels = 1 << 27;
+
+static int part_rows(int M) {
+    const long long parts = ((long long)M + kMostRows - 1) / kMostRows;
+    return (int)((M + parts - 1) / parts);
+}
+
 // One figure for either alignment.
 size_t int8_matmul_workspace(int M, int K, int N) {
+    if (N > kMostChannels) return 0;
+    M = part_rows(M);
     const size_t u = split_bytes(make_int8_plan(M, K, N, false), M, N);
     const size_t v = K % 16 ? 0 : split_bytes(make_int8_plan(M, K, N, true), M, N);
     return u > v ? u : v;
 }
 
 bool int8_matmul_supports(int M, int K, int N, long long ldq, long long ldw) {
-    // sums stay below 2^31; a tile's rows are addressed with 31 bits; the grid
-    if (K > 131071 || ldq > (1 << 22) || ldw > (1 << 22)) return false;
+    // sums stay below 2^31; a tile's rows are addressed with 31 bits; a launch
+    // counts its threads in 32 (the other two kernels have fewer)
+    if (K > 131071 || ldq > (1 << 22) || ldw > (1 << 22) || N > kMostChannels) return false;
     for (int al = 0; al < 2; ++al) {
-        const Int8Plan p = make_int8_plan(M, K, N, al);
-        if ((long long)p.tm * p.tn * p.splits >= 0x7fffffffLL) return false;
+        const Int8Plan p = make_int8_plan(part_rows(M), K, N, al);
+        if (p.kernel != kStream && p.kernel != kSkinny &&
+            (long long)p.tm * p.tn * p.splits * (p.kernel == kTile256 ? 512 : 256) > 0xffffffffLL)
+            return false;
     }
     return true;
 }
 
 hipError_t launch_int8_matmul(const Int8Args& a, int out_f32, void* ws, hipStream_t st) {
+    if (a.M > kMostRows) {   // parts of 2^28 rows and more are never split along k: they share no workspace
+        const int rows = part_rows(a.M);
+        for (long long m = 0; m < a.M; m += rows) {
+            Int8Args part = a;
+            part.M = (int)(a.M - m < rows ? a.M - m : rows);
+            part.q += m * a.ldq;
+            part.q_scale += m;
+            part.y = static_cast<char*>(a.y) + m * a.ldy * (out_f32 ? 4 : 2);
+            const hipError_t e = launch_int8_matmul(part, out_f32, ws, st);
+            if (e != hipSuccess) return e;
+        }
+        return hipSuccess;
+    }
     const Int8Plan p = make_int8_plan(a.M, a.K, a.N, aligned_operands(a));
     if (p.kernel == kStream) return out_f32 ? stream<float>(a, p, st) : stream<bf16_t>(a, p, st);
     if (p.kernel == kSkinny) return out_f32 ? skinny<float>(a, st) : skinny<bf16_t>(a, st);

@@ -376,7 +376,8 @@ int conv2d_group_norm_bwd_nhwc(const void* dy, const void* x, const float* gamma
  *   K <= 131071), the rest is fp32, rounded once.  ReLU keeps a NaN.
  *   Any K, stride and alignment works; K, ldq and ldw as multiples of 16 with
  *   16-byte aligned pointers run without repacking in registers.  ldq and ldw
- *   up to 2^22.
+ *   up to 2^22, N up to 2^27, any M; some of more than 2^37 results are
+ *   refused (CONV2D_ERR_UNSUPPORTED).
  * workspace as for the group norm, conv2d_int8_matmul_workspace_bytes(M, K, N)
  * bytes (0: none is needed and workspace may be NULL).  Neither call allocates
  * and both may be captured into a graph.

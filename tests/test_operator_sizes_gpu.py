@@ -1,0 +1,57 @@
+"""Operators at sizes that one launch or one 32-bit grid does not hold: every
+result compared on the device, part by part, with values made so that the
+answers are exact.
+"""
+import sys
+
+import pytest
+
+from helpers import ensure_built, gpu_available
+
+pytestmark = pytest.mark.gpu
+
+if gpu_available():
+    ensure_built()
+    import torch
+    import cnn_convolution_conv2d_amd as c2
+
+TOP = 2 ** 31 - 1
+
+
+@pytest.fixture(autouse=True)
+def _need_gpu():
+    if not gpu_available():
+        pytest.skip("no GPU")
+    yield
+    torch.cuda.empty_cache()
+
+
+def say(*what):
+    print("[large sizes]", *what, file=sys.stderr, flush=True)
+
+
+def parts(n, each):
+    return ((i, min(i + each, n)) for i in range(0, n, each))
+
+
+@pytest.mark.parametrize("M,K", [(TOP, 16), (TOP - 200, 17)])   # rows that stream past the weights; unaligned rows
+def test_product_of_as_many_rows_as_an_int_holds(M, K):
+    """Integer sums below 2^24 and scales that are powers of two: fp32 results are exact."""
+    say("product", M, K)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(K)
+    q = torch.empty(M, K, dtype=torch.int8, device="cuda")
+    qs = torch.empty(M, device="cuda")
+    for a, b in parts(M, 1 << 27):
+        q[a:b].random_(-128, 128, generator=gen)
+        qs[a:b] = torch.exp2(torch.randint(-3, 4, (b - a,), generator=gen, device="cuda").float())
+    w = torch.randint(-128, 128, (1, K), generator=gen, device="cuda", dtype=torch.int8)
+    y = torch.full((M + 64, 1), -77.5, device="cuda")
+    c2.conv2d_int8_matmul(q, qs, w, torch.full((1,), 0.25, device="cuda"), None, y, None, 0, M, K, 1, K, K, 1, c2.F32, 0)
+    torch.cuda.synchronize()
+    for a, b in parts(M, 1 << 26):
+        acc = torch.zeros(b - a, device="cuda")
+        for k in range(K):
+            acc += q[a:b, k].float() * float(w[0, k])
+        assert torch.equal(y[a:b, 0], acc * qs[a:b] * 0.25), (a, b)
+    assert bool((y[M:] == -77.5).all())
