@@ -777,15 +777,17 @@ hipError_t quantize(const void* x, void* q, float* scale, int M, int K, long lon
     int lpp = 1;
     while (lpp < cv && lpp < 64) lpp <<= 1;
     const int j = (cv + lpp - 1) / lpp;
-    const T* xt = static_cast<const T*>(x);
-    int8_t* qt = static_cast<int8_t*>(q);
-    if (j > 4) {
-        quantize_long_rows_kernel<T, V><<<M, 256, 0, st>>>(xt, qt, scale, K, ldx, ldq);
-        return hipGetLastError();
-    }
-    const int per = 256 / lpp, blocks = (int)(((long long)M + per - 1) / per);
+    const int per = j > 4 ? 1 : 256 / lpp;   // rows of a workgroup
     auto k = j == 1 ? quantize_rows_kernel<T, V, 1> : j == 2 ? quantize_rows_kernel<T, V, 2> : quantize_rows_kernel<T, V, 4>;
-    k<<<blocks, 256, 0, st>>>(xt, qt, scale, M, K, ldx, ldq, lpp);
+    // a launch counts its threads in 32 bits: 2^23 workgroups of 256 at a time
+    const long long most = (long long)per << 23;
+    for (long long m = 0; m < M; m += most) {
+        const int rows = (int)(M - m < most ? M - m : most);
+        const T* xt = static_cast<const T*>(x) + m * ldx;
+        int8_t* qt = static_cast<int8_t*>(q) + m * ldq;
+        if (j > 4) quantize_long_rows_kernel<T, V><<<rows, 256, 0, st>>>(xt, qt, scale + m, K, ldx, ldq);
+        else k<<<(int)(((long long)rows + per - 1) / per), 256, 0, st>>>(xt, qt, scale + m, rows, K, ldx, ldq, lpp);
+    }
     return hipGetLastError();
 }
 

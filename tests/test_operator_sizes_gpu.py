@@ -55,3 +55,23 @@ def test_product_of_as_many_rows_as_an_int_holds(M, K):
             acc += q[a:b, k].float() * float(w[0, k])
         assert torch.equal(y[a:b, 0], acc * qs[a:b] * 0.25), (a, b)
     assert bool((y[M:] == -77.5).all())
+
+
+#                          lanes that share a row: 64, 4 vectors each; a workgroup
+@pytest.mark.parametrize("M,K", [(2 ** 26 + 77, 520), (2 ** 24 + 33, 2050)])
+def test_more_rows_in_8_bits_than_a_grid_holds(M, K):
+    """Whole numbers up to 127, one of them in every row: the rows come back as they are, with scale 1."""
+    say("rows", M, K)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(K)
+    x = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+    for a, b in parts(M, 1 << 22):
+        x[a:b] = torch.randint(-126, 127, (b - a, K), generator=gen, device="cuda", dtype=torch.int8)
+    x[:, K - 1] = 127
+    q = torch.empty(M, K, dtype=torch.int8, device="cuda")
+    s = torch.empty(M, device="cuda")
+    c2.conv2d_quantize_rows(x, q, s, M, K, K, K, c2.BF16)
+    torch.cuda.synchronize()
+    for a, b in parts(M, 1 << 22):
+        assert torch.equal(q[a:b].bfloat16(), x[a:b]), (a, b)
+    assert bool((s == 1).all())
