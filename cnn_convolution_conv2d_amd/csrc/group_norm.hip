@@ -648,12 +648,12 @@ __global__ __launch_bounds__(512) void gn_bwd_sums_kernel(NormArgs a, int TX, in
 
 constexpr int kParamChannels = 32;  // channels of one workgroup that sums dgamma and dbeta
 
-// Adds `count` partials of kParamChannels channels into dgamma and dbeta.
-// LDS: blockDim.x pairs.
-__device__ __forceinline__ void sum_params(const NormArgs& a, const float* pc, long long count, int block, float2* lds) {
+// Adds `count` partials of kParamChannels channels into dgamma and dbeta, in
+// fp64: they may be many and of one sign.  LDS: blockDim.x pairs.
+__device__ __forceinline__ void sum_params(const NormArgs& a, const float* pc, long long count, int block, double2* lds) {
     const int c = block * kParamChannels + threadIdx.x % kParamChannels;
     const int row = threadIdx.x / kParamChannels, rows = blockDim.x / kParamChannels;
-    float s = 0.0f, t = 0.0f;
+    double s = 0.0, t = 0.0;
     if (c < a.C) {
         const float* p = pc + c;
 #pragma unroll 8
@@ -662,29 +662,30 @@ __device__ __forceinline__ void sum_params(const NormArgs& a, const float* pc, l
             t += p[i * 2 * a.C + a.C];
         }
     }
-    lds[threadIdx.x] = make_float2(s, t);
+    lds[threadIdx.x] = make_double2(s, t);
     __syncthreads();
     if (row == 0 && c < a.C) {
         for (int k = 1; k < rows; ++k) {
             s += lds[k * kParamChannels + threadIdx.x].x;
             t += lds[k * kParamChannels + threadIdx.x].y;
         }
-        if (a.dbeta) a.dbeta[c] = s;
-        if (a.dgamma) a.dgamma[c] = t;
+        if (a.dbeta) a.dbeta[c] = (float)s;
+        if (a.dgamma) a.dgamma[c] = (float)t;
     }
 }
 
 // Second launch of the streaming backward pass.  The first `sums` workgroups
 // add the channels' partials into dgamma and dbeta, the others write dx, one
-// per image and chunk.  LDS: max(G, blockDim.x) pairs.
+// per image and chunk.  LDS: G pairs, or blockDim.x fp64 ones.
 template <typename T, int V, int ACT, int NB>
 __global__ __launch_bounds__(512) void gn_bwd_apply_kernel(NormArgs a, int TX, int R, int chunks, int pix, int sums,
                                                            const float* pc, const float2* pg) {
-    extern __shared__ float2 lds[];
+    extern __shared__ double2 lds_pairs[];
     if ((int)blockIdx.x < sums) {
-        sum_params(a, pc, (long long)a.N * chunks, blockIdx.x, lds);
+        sum_params(a, pc, (long long)a.N * chunks, blockIdx.x, lds_pairs);
         return;
     }
+    float2* const lds = reinterpret_cast<float2*>(lds_pairs);
     const int b = blockIdx.x - sums;
     const int n = b / chunks, piece = b - n * chunks;
     const int cg = a.C / a.G;
@@ -1159,13 +1160,13 @@ __global__ __launch_bounds__(256, 3) void gn_bwd_joined_kernel(NormArgs a, int T
 }
 
 __global__ __launch_bounds__(256) void gn_params_kernel(NormArgs a, const float* pc) {
-    __shared__ float2 lds[256];
+    __shared__ double2 lds[256];
     sum_params(a, pc, a.N, blockIdx.x, lds);
 }
 
 // An image's `count` partials of kParamChannels channels into one: out [N][2][C].
 __global__ __launch_bounds__(256) void gn_image_params_kernel(NormArgs a, const float* pc, int count, float* out) {
-    __shared__ float2 lds[256];
+    __shared__ double2 lds[256];
     out += (long long)blockIdx.y * 2 * a.C;
     a.dbeta = out;
     a.dgamma = out + a.C;
@@ -1366,7 +1367,7 @@ template <typename T, int V, int ACT> hipError_t backward_act(const NormArgs& a,
     auto first = few ? gn_bwd_sums_kernel<T, V, ACT, 1> : gn_bwd_sums_kernel<T, V, ACT, kBatchBwd>;
     first<<<(int)blocks, p.block, (size_t)p.R * a.C * 8, st>>>(a, p.TX, p.R, p.chunks, p.pix, pc, pg);
     const int sums = a.dgamma || a.dbeta ? (a.C + kParamChannels - 1) / kParamChannels : 0;
-    const size_t lds = (size_t)(a.G > p.block ? a.G : p.block) * 8;
+    const size_t lds = (size_t)(a.G > 2 * p.block ? a.G : 2 * p.block) * 8;
     auto second = few ? gn_bwd_apply_kernel<T, V, ACT, 1> : gn_bwd_apply_kernel<T, V, ACT, kBatchBwd>;
     second<<<sums + (int)blocks, p.block, lds, st>>>(a, p.TX, p.R, p.chunks, p.pix, sums, pc, pg);
     return hipGetLastError();
