@@ -234,10 +234,9 @@ hipError_t launch_winograd(const Shape& s, const void* x, const void* w_wino, co
                            hipStream_t st);
 hipError_t launch_winograd_weights(const void* w, void* w_wino, int Cout, int Cin, hipStream_t st);
 
-// Group norm: the bytes of workspace, whether the sizes fit the grids, and the
-// three passes (two launches each; act: CONV2D_ACT_*).
+// Group norm: the bytes of workspace and the three passes (one to four launches
+// each; act: CONV2D_ACT_*).
 size_t group_norm_workspace(int N, int P, int C, int G, int backward);
-bool group_norm_supports(int N, int P, int C);
 hipError_t launch_group_norm(const NormArgs& a, int act, void* ws, hipStream_t st);
 hipError_t launch_group_norm_quant(const NormArgs& a, int act, void* ws, hipStream_t st);
 hipError_t launch_group_norm_bwd(const NormArgs& a, int act, void* ws, hipStream_t st);

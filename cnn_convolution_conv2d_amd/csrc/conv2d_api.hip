@@ -472,7 +472,7 @@ int validate_norm(const NormArgs& a, int H, int W, int act, const void* ws, size
     if ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.dy)) % eb ||
         (!a.q_scale && reinterpret_cast<uintptr_t>(a.y) % eb))
         return set_error(CONV2D_ERR_ALIGN, "a tensor is not aligned to its elements");
-    if (a.C > 4096 || sat_mul({a.N, H, W}) >= INT_MAX || !group_norm_supports(a.N, H * W, a.C))
+    if (a.C > 4096 || sat_mul({a.N, H, W}) >= INT_MAX)
         return set_error(CONV2D_ERR_UNSUPPORTED, "group norm takes C <= 4096 and N*H*W < 2^31");
     const size_t need = conv2d_group_norm_workspace_bytes(a.N, a.C, H, W, a.G, backward);
     if (!ws) return set_error(CONV2D_ERR_NULL, "the workspace is NULL (%zu bytes needed)", need);

@@ -843,7 +843,7 @@ __global__ __launch_bounds__(1024) void gn_resident_kernel(NormArgs a, int TX, i
 }
 
 // Backward: the same, with the channels' sums of this image to pc
-// ([image][2][C]), or, for a single image, to dgamma and dbeta themselves.
+// ([image][2][C]), or, for a single image (pc null), to dgamma and dbeta themselves.
 // LDS: R * C/G pairs.
 template <typename T, int V, int ACT, int NV>
 __global__ __launch_bounds__(1024) void gn_bwd_resident_kernel(NormArgs a, int TX, int R, float* pc) {
@@ -892,7 +892,7 @@ __global__ __launch_bounds__(1024) void gn_bwd_resident_kernel(NormArgs a, int T
     if (!a.dgamma && !a.dbeta) return;
     sum_rows(rows, R, cg);
     for (int k = threadIdx.x; k < cg; k += blockDim.x) {
-        if (a.N == 1) {
+        if (!pc) {
             if (a.dbeta) a.dbeta[g * cg + k] = rows[k].x;
             if (a.dgamma) a.dgamma[g * cg + k] = rows[k].y;
         } else {
@@ -1159,18 +1159,20 @@ __global__ __launch_bounds__(256, 3) void gn_bwd_joined_kernel(NormArgs a, int T
     }
 }
 
-__global__ __launch_bounds__(256) void gn_params_kernel(NormArgs a, const float* pc) {
+__global__ __launch_bounds__(256) void gn_params_kernel(NormArgs a, const float* pc, long long count) {
     __shared__ double2 lds[256];
-    sum_params(a, pc, a.N, blockIdx.x, lds);
+    sum_params(a, pc, count, blockIdx.x, lds);
 }
 
 // An image's `count` partials of kParamChannels channels into one: out [N][2][C].
-__global__ __launch_bounds__(256) void gn_image_params_kernel(NormArgs a, const float* pc, int count, float* out) {
+// `sums` workgroups an image.
+__global__ __launch_bounds__(256) void gn_image_params_kernel(NormArgs a, const float* pc, int count, int sums, float* out) {
     __shared__ double2 lds[256];
-    out += (long long)blockIdx.y * 2 * a.C;
+    const int image = blockIdx.x / sums;
+    out += (long long)image * 2 * a.C;
     a.dbeta = out;
     a.dgamma = out + a.C;
-    sum_params(a, pc + (long long)blockIdx.y * count * 2 * a.C, count, blockIdx.x, lds);
+    sum_params(a, pc + (long long)image * count * 2 * a.C, count, blockIdx.x - image * sums, lds);
 }
 
 // ------------------------------------------------------------------ host
@@ -1214,6 +1216,31 @@ constexpr long long kWholeVectors = 6400;
 struct Plan {
     int TX, R, block, chunks, pix;
 };
+
+// run(images, first) for all images, `per` workgroups of `threads` each: a launch
+// counts its threads in 32 bits, so that very many images (of one pixel, say)
+// take several.
+template <typename F> hipError_t in_launches(const NormArgs& a, long long per, int threads, F run) {
+    const long long most = 0xff000000LL / (per * threads);   // 2^24 left for workgroups beside them
+    const int elem = a.dtype == 0 /* CONV2D_F32 */ ? 4 : 2;
+    for (long long n = 0; n < a.N; n += most) {
+        NormArgs s = a;
+        auto pixels = [&](const void* p, long long ld, int bytes) { return p ? static_cast<const char*>(p) + n * a.P * ld * bytes : nullptr; };
+        s.N = (int)(a.N - n < most ? a.N - n : most);
+        s.x = pixels(a.x, a.ldx, elem);
+        s.dy = pixels(a.dy, a.lddy, elem);
+        s.y = const_cast<char*>(pixels(a.y, a.ldy, a.q_scale ? 1 : elem));
+        if (a.q_scale) s.q_scale += n * a.P;
+        if (a.mean) s.mean += n * a.G;
+        if (a.rstd) s.rstd += n * a.G;
+        run(s, n);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+int param_blocks(const NormArgs& a) { return a.dgamma || a.dbeta ? (a.C + kParamChannels - 1) / kParamChannels : 0; }
 
 // Threads: TX across the channel vectors, R rows of them, the block size of
 // 256 to 512 that leaves the fewest idle.  Chunks: kTargetBlocks workgroups
@@ -1262,7 +1289,7 @@ Resident make_resident(const NormArgs& a, int V, int elem, int most) {
     p.TX = cg / V;
     const long long bytes = (long long)a.N * a.P * a.C * elem;
     if ((long long)a.N * a.G < 256 && (long long)a.P * cg * elem > kResidentUnitBytes) return p;
-    if (p.TX > 256 || (bytes > kResidentBytes && cg * elem < 64) || (long long)a.N * a.G >= 0x7fffffffLL) return p;
+    if (p.TX > 256 || (bytes > kResidentBytes && cg * elem < 64)) return p;
     for (p.block = 256; p.block <= 1024; p.block *= 2) {
         p.R = p.block / p.TX;
         const long long nv = (a.P + (long long)p.R - 1) / p.R;
@@ -1277,36 +1304,40 @@ Resident make_resident(const NormArgs& a, int V, int elem, int most) {
 template <typename T, int V, int ACT> hipError_t forward_resident(const NormArgs& a, const Resident& p, hipStream_t st) {
     auto k = p.nv == 2 ? gn_resident_kernel<T, V, ACT, 2> : p.nv == 4 ? gn_resident_kernel<T, V, ACT, 4>
                          : gn_resident_kernel<T, V, ACT, 8>;
-    k<<<a.N * a.G, p.block, 0, st>>>(a, p.TX, p.R);
-    return hipGetLastError();
+    return in_launches(a, a.G, p.block, [&](const NormArgs& s, long long) { k<<<s.N * s.G, p.block, 0, st>>>(s, p.TX, p.R); });
 }
 
 template <typename T, int V> hipError_t forward(const NormArgs& a, int act, void* ws, hipStream_t st) {
     const Plan p = make_plan(a.N, a.P, a.C, V);
     float2* part = static_cast<float2*>(ws);
-    gn_stats_kernel<T, V><<<a.N * p.chunks, p.block, (size_t)p.R * a.C * 8, st>>>(a, p.TX, p.R, p.chunks, p.pix, part);
     auto k = act == kActSilu ? gn_apply_kernel<T, V, kActSilu>
              : act == kActRelu ? gn_apply_kernel<T, V, kActRelu> : gn_apply_kernel<T, V, kActNone>;
-    k<<<a.N * p.chunks, p.block, (size_t)a.G * 8, st>>>(a, p.TX, p.R, p.chunks, p.pix, part);
-    return hipGetLastError();
+    return in_launches(a, p.chunks, p.block, [&](const NormArgs& s, long long n) {
+        float2* at = part + n * p.chunks * a.G;
+        gn_stats_kernel<T, V><<<s.N * p.chunks, p.block, (size_t)p.R * a.C * 8, st>>>(s, p.TX, p.R, p.chunks, p.pix, at);
+        k<<<s.N * p.chunks, p.block, (size_t)a.G * 8, st>>>(s, p.TX, p.R, p.chunks, p.pix, at);
+    });
 }
 
-template <typename T, int V, int ACT> hipError_t quantised_apply(const NormArgs& a, const Plan& p, const float2* part,
-                                                                 hipStream_t st) {
+template <typename T, int V, int ACT> hipError_t quantised_act(const NormArgs& a, void* ws, hipStream_t st) {
+    const Plan p = make_plan(a.N, a.P, a.C, V);
     const int cv = (a.C + V - 1) / V;
-    if (cv > 64) {
-        const size_t lds = (size_t)a.G * 8 + (size_t)a.C * 12;
+    const bool wide = cv > 64;
+    const size_t lds = (size_t)a.G * 8 + (wide ? (size_t)a.C * 12 : 0);
+    if (lds > 65536) {
         int dev = 0;
         hipError_t e = hipGetDevice(&dev);
-        if (e == hipSuccess && lds > 65536) e = ensure_dynamic_lds<gn_quant_wide_kernel<T, V, ACT>>((int)lds, dev);
+        if (e == hipSuccess) e = ensure_dynamic_lds<gn_quant_wide_kernel<T, V, ACT>>((int)lds, dev);
         if (e != hipSuccess) return e;
-        gn_quant_wide_kernel<T, V, ACT><<<a.N * p.chunks, 256, lds, st>>>(a, p.chunks, p.pix, part);
-        return hipGetLastError();
     }
     int lpp = 1;
     while (lpp < cv) lpp <<= 1;
-    gn_quant_kernel<T, V, ACT><<<a.N * p.chunks, 256, (size_t)a.G * 8, st>>>(a, lpp, p.chunks, p.pix, part);
-    return hipGetLastError();
+    return in_launches(a, p.chunks, p.block, [&](const NormArgs& s, long long n) {
+        float2* part = static_cast<float2*>(ws) + n * p.chunks * a.G;
+        gn_stats_kernel<T, V><<<s.N * p.chunks, p.block, (size_t)p.R * a.C * 8, st>>>(s, p.TX, p.R, p.chunks, p.pix, part);
+        if (wide) gn_quant_wide_kernel<T, V, ACT><<<s.N * p.chunks, 256, lds, st>>>(s, p.chunks, p.pix, part);
+        else gn_quant_kernel<T, V, ACT><<<s.N * p.chunks, 256, lds, st>>>(s, lpp, p.chunks, p.pix, part);
+    });
 }
 
 template <typename T, int V, int ACT> hipError_t quantised_whole(const NormArgs& a, hipStream_t st) {
@@ -1325,12 +1356,8 @@ template <typename T, int V> hipError_t quantised(const NormArgs& a, int act, vo
     if (a.N <= kWholeBlocks && (a.C + V - 1) / V <= 64 && (long long)a.P * ((a.C + V - 1) / V) <= kWholeVectors)
         return act == kActSilu ? quantised_whole<T, V, kActSilu>(a, st)
                : act == kActRelu ? quantised_whole<T, V, kActRelu>(a, st) : quantised_whole<T, V, kActNone>(a, st);
-    const Plan p = make_plan(a.N, a.P, a.C, V);
-    float2* part = static_cast<float2*>(ws);
-    gn_stats_kernel<T, V><<<a.N * p.chunks, p.block, (size_t)p.R * a.C * 8, st>>>(a, p.TX, p.R, p.chunks, p.pix, part);
-    return act == kActSilu ? quantised_apply<T, V, kActSilu>(a, p, part, st)
-           : act == kActRelu ? quantised_apply<T, V, kActRelu>(a, p, part, st)
-                             : quantised_apply<T, V, kActNone>(a, p, part, st);
+    return act == kActSilu ? quantised_act<T, V, kActSilu>(a, ws, st)
+           : act == kActRelu ? quantised_act<T, V, kActRelu>(a, ws, st) : quantised_act<T, V, kActNone>(a, ws, st);
 }
 
 template <typename T, int V, int ACT> hipError_t backward_resident(const NormArgs& a, const Resident& p, float* pc,
@@ -1344,14 +1371,15 @@ template <typename T, int V, int ACT> hipError_t backward_resident(const NormArg
             e = hipGetDevice(&dev);
             if (e == hipSuccess) e = ensure_dynamic_lds<kernel>((int)lds, dev);
         }
-        if (e == hipSuccess) kernel<<<a.N * a.G, p.block, lds, st>>>(a, p.TX, p.R, pc);
-        return e;
+        if (e != hipSuccess) return e;
+        return in_launches(a, a.G, p.block, [&](const NormArgs& s, long long n) {
+            kernel<<<s.N * s.G, p.block, lds, st>>>(s, p.TX, p.R, a.N > 1 ? pc + n * 2 * a.C : nullptr);
+        });
     };
     const hipError_t e = p.nv == 2 ? run([] { return gn_bwd_resident_kernel<T, V, ACT, 2>; })
                                     : run([] { return gn_bwd_resident_kernel<T, V, ACT, 4>; });
     if (e != hipSuccess) return e;
-    if (a.N > 1 && (a.dgamma || a.dbeta))
-        gn_params_kernel<<<(a.C + kParamChannels - 1) / kParamChannels, 256, 0, st>>>(a, pc);
+    if (a.N > 1 && param_blocks(a)) gn_params_kernel<<<param_blocks(a), 256, 0, st>>>(a, pc, a.N);
     return hipGetLastError();
 }
 
@@ -1365,12 +1393,23 @@ template <typename T, int V, int ACT> hipError_t backward_act(const NormArgs& a,
     // 18x46x108 in fp32: 13.4 us for 14.6; forward, with little of either, even)
     const bool few = p.pix <= 2 * p.R;
     auto first = few ? gn_bwd_sums_kernel<T, V, ACT, 1> : gn_bwd_sums_kernel<T, V, ACT, kBatchBwd>;
-    first<<<(int)blocks, p.block, (size_t)p.R * a.C * 8, st>>>(a, p.TX, p.R, p.chunks, p.pix, pc, pg);
-    const int sums = a.dgamma || a.dbeta ? (a.C + kParamChannels - 1) / kParamChannels : 0;
-    const size_t lds = (size_t)(a.G > 2 * p.block ? a.G : 2 * p.block) * 8;
     auto second = few ? gn_bwd_apply_kernel<T, V, ACT, 1> : gn_bwd_apply_kernel<T, V, ACT, kBatchBwd>;
-    second<<<sums + (int)blocks, p.block, lds, st>>>(a, p.TX, p.R, p.chunks, p.pix, sums, pc, pg);
-    return hipGetLastError();
+    const size_t lds = (size_t)(a.G > 2 * p.block ? a.G : 2 * p.block) * 8;
+    // dgamma and dbeta along with dx, unless there are several launches of that
+    int sums = param_blocks(a), launches = 0;
+    const hipError_t e = in_launches(a, p.chunks, p.block, [&](const NormArgs& s, long long n) {
+        ++launches;
+        first<<<s.N * p.chunks, p.block, (size_t)p.R * a.C * 8, st>>>(s, p.TX, p.R, p.chunks, p.pix,
+                                                                      pc + n * p.chunks * 2 * a.C, pg + n * p.chunks * a.G);
+    });
+    if (e != hipSuccess) return e;
+    if (launches > 1 && sums) {
+        gn_params_kernel<<<sums, 256, 0, st>>>(a, pc, blocks);
+        sums = 0;
+    }
+    return in_launches(a, p.chunks, p.block, [&](const NormArgs& s, long long n) {
+        second<<<sums + s.N * p.chunks, p.block, lds, st>>>(s, p.TX, p.R, p.chunks, p.pix, sums, pc, pg + n * p.chunks * a.G);
+    });
 }
 
 template <typename T, int V> hipError_t backward(const NormArgs& a, int act, void* ws, hipStream_t st) {
@@ -1435,7 +1474,7 @@ Joined make_joined(const NormArgs& a, int V, int elem, bool quant, int most) {
     p = plan_joined(a.P, a.C, a.G, V, quant, most);
     // 32-bit offsets in a chunk, one step past its end included
     const long long ld = a.ldx > a.ldy ? (a.ldx > a.lddy ? a.ldx : a.lddy) : (a.ldy > a.lddy ? a.ldy : a.lddy);
-    if ((long long)a.N * p.chunks >= 0x7fffffffLL || (long long)p.R * (p.nv + 1) * ld * elem > 0x7fffff00LL) p.nv = 0;
+    if ((long long)p.R * (p.nv + 1) * ld * elem > 0x7fffff00LL) p.nv = 0;
     return p;
 }
 
@@ -1451,8 +1490,10 @@ hipError_t joined_act(const NormArgs& a, const Joined& p, void* ws, hipStream_t 
     if (e != hipSuccess) return e;
     auto k = p.nv == kJoinedMost ? gn_joined_kernel<T, V, ACT, kJoinedMost, QUANT>
                                  : gn_joined_kernel<T, V, ACT, kJoinedMost / 2, QUANT>;
-    k<<<a.N * p.chunks, 256, p.lds, st>>>(a, p.TX, p.R, p.chunks, p.pix, wait_limit(), static_cast<word_t*>(ws));
-    return hipGetLastError();
+    return in_launches(a, p.chunks, 256, [&](const NormArgs& s, long long n) {
+        k<<<s.N * p.chunks, 256, p.lds, st>>>(s, p.TX, p.R, p.chunks, p.pix, wait_limit(),
+                                              static_cast<word_t*>(ws) + n * p.chunks * a.G);
+    });
 }
 
 template <typename T, int V, bool QUANT>
@@ -1464,20 +1505,27 @@ hipError_t joined(const NormArgs& a, int act, const Joined& p, void* ws, hipStre
 
 template <typename T, int V, int ACT> hipError_t joined_bwd_act(const NormArgs& a, const Joined& p, void* ws, hipStream_t st) {
     const long long blocks = (long long)a.N * p.chunks;
-    const hipError_t e = clear_words(ws, blocks * a.G, st);
+    hipError_t e = clear_words(ws, blocks * a.G, st);
     if (e != hipSuccess) return e;
     word_t* words = static_cast<word_t*>(ws);
     float* pc = reinterpret_cast<float*>(words + blocks * a.G);
     auto k = p.nv == kJoinedMostBwd ? gn_bwd_joined_kernel<T, V, ACT, kJoinedMostBwd>
                                     : gn_bwd_joined_kernel<T, V, ACT, kJoinedMostBwd / 2>;
-    k<<<(int)blocks, 256, p.lds, st>>>(a, p.TX, p.R, p.chunks, p.pix, wait_limit(), words, pc);
-    if (a.dgamma || a.dbeta) {
-        const int sums = (a.C + kParamChannels - 1) / kParamChannels;
+    e = in_launches(a, p.chunks, 256, [&](const NormArgs& s, long long n) {
+        k<<<s.N * p.chunks, 256, p.lds, st>>>(s, p.TX, p.R, p.chunks, p.pix, wait_limit(), words + n * p.chunks * a.G,
+                                              pc + n * p.chunks * 2 * a.C);
+    });
+    const int sums = param_blocks(a);
+    if (e == hipSuccess && sums) {
         float* images = pc + blocks * 2 * a.C;
-        gn_image_params_kernel<<<dim3(sums, a.N), 256, 0, st>>>(a, pc, p.chunks, images);
-        gn_params_kernel<<<sums, 256, 0, st>>>(a, images);
+        e = in_launches(a, sums, 256, [&](const NormArgs& s, long long n) {
+            gn_image_params_kernel<<<s.N * sums, 256, 0, st>>>(s, pc + n * p.chunks * 2 * a.C, p.chunks, sums, images + n * 2 * a.C);
+        });
+        if (e != hipSuccess) return e;
+        gn_params_kernel<<<sums, 256, 0, st>>>(a, images, a.N);
+        e = hipGetLastError();
     }
-    return hipGetLastError();
+    return e;
 }
 
 template <typename T, int V> hipError_t joined_bwd(const NormArgs& a, int act, const Joined& p, void* ws, hipStream_t st) {
@@ -1506,14 +1554,6 @@ size_t group_norm_workspace(int N, int P, int C, int G, int backward) {
             most = bytes > most ? bytes : most;
         }
     return most;
-}
-
-// Grids are one-dimensional: the largest must fit 2^31 - 1 workgroups.
-bool group_norm_supports(int N, int P, int C) {
-    for (int v = 1; v <= 8 && v <= C; v <<= 1) {
-        if ((long long)N * make_plan(N, P, C, v).chunks + C >= 0x7fffffffLL) return false;
-    }
-    return true;
 }
 
 #define CONV2D_NORM_WIDTH(FN, WIDTH, ...)                                                           \

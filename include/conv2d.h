@@ -328,7 +328,7 @@ int conv2d_transpose_select_path(int N, int Cin, int H, int W, int Cout, int Kh,
  *   either may be NULL.  dx may be dy or x (same ld).
  *
  * gamma, beta: fp32 [C]; NULL means 1 and 0.  eps >= 0 and finite.  C must be
- * divisible by G, C <= 4096.  Any channel count, stride and alignment works;
+ * divisible by G, C <= 4096, N*H*W < 2^31.  Any channel count, stride and alignment works;
  * C, the strides and the pointers as multiples of 16 bytes are fastest.
  * Sums have a fixed order: equal calls give equal bits.  A NaN or
  * infinity spreads through its own (image, group) and no further.
