@@ -16,10 +16,12 @@
 
 static PyObject* data_ptr_name;
 
-/* Every converter leaves a Python error set when it fails; the callers check
- * once, after the last argument. */
+/* Every converter leaves a Python error set when it fails, and does nothing when
+ * an earlier one has (Python must not be called with an error set, and the first
+ * bad argument is the one to name); the callers check once, after the last
+ * argument. */
 static void* as_ptr(PyObject* o) {
-    if (o == Py_None) return NULL;
+    if (o == Py_None || PyErr_Occurred()) return NULL;
     if (PyLong_Check(o)) return PyLong_AsVoidPtr(o);
     PyObject* r = PyObject_CallMethodNoArgs(o, data_ptr_name);
     if (!r) return NULL;
@@ -29,6 +31,7 @@ static void* as_ptr(PyObject* o) {
 }
 
 static int as_int(PyObject* o) {
+    if (PyErr_Occurred()) return 0;
     const long v = PyLong_AsLong(o);
     if (v != (int)v) {
         if (!PyErr_Occurred()) PyErr_SetString(PyExc_OverflowError, "argument does not fit a C int");
@@ -37,8 +40,8 @@ static int as_int(PyObject* o) {
     return (int)v;
 }
 
-static size_t as_size(PyObject* o) { return PyLong_AsSize_t(o); }
-static float as_float(PyObject* o) { return (float)PyFloat_AsDouble(o); }
+static size_t as_size(PyObject* o) { return PyErr_Occurred() ? 0 : PyLong_AsSize_t(o); }
+static float as_float(PyObject* o) { return PyErr_Occurred() ? 0.0f : (float)PyFloat_AsDouble(o); }
 
 static int arity(const char* name, Py_ssize_t got, Py_ssize_t want) {
     if (got == want) return 1;
