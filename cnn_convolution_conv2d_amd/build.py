@@ -6,7 +6,9 @@ operator entries from Python (in-tree, no JIT cache).
 Every ``csrc/*.hip`` file is compiled to an object under ``_build/`` at the
 repository root, in parallel, then linked into
 ``cnn_convolution_conv2d_amd/libconv2d.so``; ``csrc/binding.c`` becomes
-``cnn_convolution_conv2d_amd/_binding.so``.
+``cnn_convolution_conv2d_amd/_binding.<this Python's ABI>.so``.  The extension
+only saves host time: without Python's headers it is left out, and the calls
+go through ctypes.
 """
 from __future__ import annotations
 
@@ -22,7 +24,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libconv2d.so")
-BINDING = os.path.join(PKG, "_binding.so")
+# named for the Python it is built for: another version's binary is not loaded
+BINDING = os.path.join(PKG, "_binding" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 BUILD_DIR = os.path.join(ROOT, "_build")
 ARCH = os.environ.get("CONV2D_OFFLOAD_ARCH", "gfx950")
 
@@ -57,7 +60,14 @@ def _compile(src: str) -> str:
     return obj
 
 
+def has_python_headers() -> bool:
+    return os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h"))
+
+
 def _build_binding() -> None:
+    if not has_python_headers():
+        print("no Python.h: the operators are called through ctypes", file=sys.stderr)
+        return
     tmp = BINDING + ".tmp"
     cc = shutil.which("gcc") or shutil.which("cc") or hipcc()
     cmd = [cc, "-O2", "-Wall", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"],
@@ -100,8 +110,8 @@ def sources() -> list[str]:
 
 def stale() -> bool:
     """True when libconv2d.so is missing or older than any file it is built from,
-    or the extension is missing."""
-    if not os.path.exists(OUT) or not os.path.exists(BINDING):
+    or the extension is missing where it can be built."""
+    if not os.path.exists(OUT) or (has_python_headers() and not os.path.exists(BINDING)):
         return True
     built = os.path.getmtime(OUT)
     return any(os.path.getmtime(p) > built for p in sources())
