@@ -818,6 +818,8 @@ int conv2d_group_norm_quant_nhwc(const void* x, const float* gamma, const float*
     if (!q_scale) return set_error(CONV2D_ERR_NULL, "q_scale must be non-NULL");
     const int rc = validate_norm(a, H, W, act, workspace, workspace_bytes, 0);
     if (rc) return rc;
+    // a pixel's bytes lie over other pixels' values, which other workgroups still read
+    if (x == q) return set_error(CONV2D_ERR_ARG, "q must not be x");
     a.P = H * W;
     const hipError_t e = launch_group_norm_quant(a, act, workspace, stream);
     return e == hipSuccess ? CONV2D_OK : hip_fail(e, "quantised group norm launch");
@@ -850,6 +852,7 @@ int conv2d_quantize_rows(const void* x, void* q, float* scale, int M, int K, int
     if (!x || !q || !scale) return set_error(CONV2D_ERR_NULL, "x, q and scale must be non-NULL");
     if (reinterpret_cast<uintptr_t>(x) % elem_bytes(dtype))
         return set_error(CONV2D_ERR_ALIGN, "x is not aligned to its elements");
+    if (x == q) return set_error(CONV2D_ERR_ARG, "q must not be x");
     const hipError_t e = launch_quantize_rows(x, q, scale, M, K, ldx, ldq, dtype, stream);
     return e == hipSuccess ? CONV2D_OK : hip_fail(e, "quantize_rows launch");
 }

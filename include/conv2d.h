@@ -318,7 +318,7 @@ int conv2d_transpose_select_path(int N, int Cin, int H, int W, int Cout, int Kh,
  * conv2d_group_norm_quant_nhwc -- y in 8 bits instead, ready to be the rows of
  *   conv2d_int8_matmul: q int8 [N][H][W] pixels of C (ldq apart) and q_scale
  *   fp32 [N*H*W], quantised for each pixel as conv2d_quantize_rows does (the
- *   unrounded fp32 activations).
+ *   unrounded fp32 activations).  q must not overlap x.
  * conv2d_group_norm_bwd_nhwc -- the gradients, from dy, x and the mean and
  *   rstd of the forward pass (the pass recomputes z; nothing else is kept):
  *     dz = dy * act'(z),  dbeta[c] = sum dz,  dgamma[c] = sum dz * xh
@@ -328,8 +328,9 @@ int conv2d_transpose_select_path(int N, int Cin, int H, int W, int Cout, int Kh,
  *   either may be NULL.  dx may be dy or x (same ld).
  *
  * gamma, beta: fp32 [C]; NULL means 1 and 0.  eps >= 0 and finite.  C must be
- * divisible by G, C <= 4096, N*H*W < 2^31.  Any channel count, stride and alignment works;
- * C, the strides and the pointers as multiples of 16 bytes are fastest.
+ * divisible by G, C <= 4096, N*H*W < 2^31.  Any channel count, stride and
+ * alignment works; C, the strides and the pointers as multiples of 16 bytes are
+ * fastest.
  * Sums have a fixed order: equal calls give equal bits.  A NaN or
  * infinity spreads through its own (image, group) and no further.
  *
@@ -366,8 +367,8 @@ int conv2d_group_norm_bwd_nhwc(const void* dy, const void* x, const float* gamma
  *     a = max(max_k |x|, 2^-100),  q = round(x * (127 / a)) (to nearest even),
  *     scale = a / 127
  *   A row that holds a NaN or an infinity gets scale NaN and q = 0, so every
- *   product with it is NaN.  Also the way to quantise weights, whose rows are
- *   output channels.
+ *   product with it is NaN.  q must not overlap x.  Also the way to quantise
+ *   weights, whose rows are output channels.
  * conv2d_int8_matmul --
  *     y[m][n] = epi( (sum_k q[m][k] * w[n][k]) * (q_scale[m] * w_scale[n]) )
  *   q int8 [M][K] (ldq apart), w int8 [N][K] (ldw apart), q_scale fp32 [M],

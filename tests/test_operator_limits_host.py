@@ -1,4 +1,4 @@
-"""Sizes at the ends of the operators' ranges, as far as the host decides them
+"""What the operators take and refuse at the ends of their ranges
 (no GPU: workspace sizes and refusals; a refused call enqueues nothing)."""
 import pytest
 
@@ -28,3 +28,11 @@ def test_products_whose_tiles_cannot_be_counted_are_refused(M, K, N):
 @pytest.mark.parametrize("K,N", [(16, 16), (17, 16), (8192, 64), (16, 300)])
 def test_many_rows_need_no_workspace(M, K, N):
     assert c2.conv2d_int8_matmul_workspace_bytes(M, K, N) == 0
+
+
+def test_eight_bits_over_their_input_are_refused():
+    """Written in another place than they are read from: other rows would be lost."""
+    for dtype in (c2.F32, c2.BF16):
+        assert c2.lib.conv2d_quantize_rows(P, P, P, 8, 64, 64, 64, dtype, None) == c2.ERR_ARG
+        assert c2.lib.conv2d_group_norm_quant_nhwc(P, None, None, P, P, None, None, P, 1 << 40, 2, 32, 5, 7, 4, 32, 32,
+                                                   1e-5, dtype, 0, None) == c2.ERR_ARG
