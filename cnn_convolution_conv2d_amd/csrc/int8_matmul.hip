@@ -951,8 +951,9 @@ size_t split_bytes(const Int8Plan& p, int M, int N) {
 }  // namespace
 
 // The most rows of one launch (more are taken in equal parts) and the most
-// channels: indexes stay below 2^31 past the end of the last tile too.
-constexpr int kMostRows = 1 << 29, kMostChannels = 1 << 27;
+// channels: indexes stay below 2^31 past the end of the last tile too.  The
+// longest row: sums stay below 2^31.
+constexpr int kMostRows = 1 << 29, kMostChannels = 1 << 27, kMostK = 131071;
 
 static int part_rows(int M) {
     const long long parts = ((long long)M + kMostRows - 1) / kMostRows;
@@ -961,7 +962,7 @@ static int part_rows(int M) {
 
 // One figure for either alignment.
 size_t int8_matmul_workspace(int M, int K, int N) {
-    if (N > kMostChannels) return 0;
+    if (K > kMostK || N > kMostChannels) return 0;   // refused
     M = part_rows(M);
     const size_t u = split_bytes(make_int8_plan(M, K, N, false), M, N);
     const size_t v = K % 16 ? 0 : split_bytes(make_int8_plan(M, K, N, true), M, N);
@@ -969,9 +970,9 @@ size_t int8_matmul_workspace(int M, int K, int N) {
 }
 
 bool int8_matmul_supports(int M, int K, int N, long long ldq, long long ldw) {
-    // sums stay below 2^31; a tile's rows are addressed with 31 bits; a launch
-    // counts its threads in 32 (the other two kernels have fewer)
-    if (K > 131071 || ldq > (1 << 22) || ldw > (1 << 22) || N > kMostChannels) return false;
+    // a tile's rows are addressed with 31 bits; a launch counts its threads in 32
+    // (the other two kernels have fewer)
+    if (K > kMostK || ldq > (1 << 22) || ldw > (1 << 22) || N > kMostChannels) return false;
     for (int al = 0; al < 2; ++al) {
         const Int8Plan p = make_int8_plan(part_rows(M), K, N, al);
         if (p.kernel != kStream && p.kernel != kSkinny &&
