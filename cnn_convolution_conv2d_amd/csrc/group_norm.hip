@@ -26,8 +26,8 @@
 // Joined, for large tensors of which no workgroup can hold a group: a workgroup
 // keeps a chunk of an image in registers and takes the statistics of the
 // image's other chunks from the workspace, so memory is read once here too.
-// 112x112x128 over 32 images 55.7 us, where streaming takes 69.2 and the bytes
-// alone 42; backward of 56x56x256 over 64 images 103 us for 116 (bytes: 63).
+// 112x112x128 over 32 images with SiLU 59 us, where streaming takes 71 and the
+// bytes alone 42; backward of 56x56x256 over 64 images 103 us for 116 (bytes: 63).
 //
 // Every sum has a fixed order: equal calls give equal bits.
 //
@@ -1192,10 +1192,10 @@ int vector_width(const NormArgs& a, int unit, int elem, int out_elem) {
 // The streaming form's, of large tensors: 16 bytes whatever the alignment, the
 // last vector of a row over part of the one before, unless the output is an
 // input too (a thread would read what another has written) or the row is
-// shorter.  bf16, 531 channels (one element an access otherwise): 98 MB 71 us
-// against 244, backward 117 against 283; 20 MB 28 against 51, 43 against 57; 10
-// MB 22 against 28, 34 against 33; 3 MB 18 against 14, 31 against 18.  252
-// channels (four elements): 100 MB 74 against 87, 10 MB 18 against 16.
+// shorter.  bf16, 531 channels (one element an access otherwise): 98 MB 73 us
+// against 213, backward 117 against 283; 20 MB 27 against 41, 40 against 51; 11
+// MB 22 against 23, 32 against 30; 4 MB 14.5 against 16.6, 17.8 against 19.9.
+// 252 channels (four elements): 100 MB 71 against 84, 10 MB 17.5 against 14.4.
 constexpr long long kRaggedBytes = 8 << 20;
 
 int row_width(const NormArgs& a, int elem, int out_elem) {
@@ -1207,9 +1207,9 @@ int row_width(const NormArgs& a, int elem, int out_elem) {
 
 // The quantised pass in one launch: images of at most kWholeVectors vectors, no
 // more workgroups than compute units.  Through norm and product, against two
-// launches: 200 images of 8x8x64 (512 vectors) 11.9 us for 14.6, 32 of 14x14x256
-// (6272) 15.1 for 17.2; 3 of 16x7x512 (7168) 15.0 for 14.6, one of 28x28x128
-// (12544) 15.0 for 13.7.
+// launches: 200 images of 8x8x64 (512 vectors) 12.7 us for 15.2, 32 of 14x14x256
+// (6272) 16.1 for 17.6; 3 of 16x7x512 (7168) 16.2 for 15.2, one of 28x28x128
+// (12544) 17.5 for 14.3.
 constexpr int kWholeThreads = 512, kWholeBlocks = 256;
 constexpr long long kWholeVectors = 6400;
 
@@ -1248,7 +1248,7 @@ int param_blocks(const NormArgs& a) { return a.dgamma || a.dbeta ? (a.C + kParam
 // once), at most kMaxChunks per image, of a whole number of pixels a thread,
 // two at least where there are more than 64: the second launch waits for all of
 // an image's partials (4 images of 28x28x256, quantised and multiplied: 98
-// chunks 19.0 us, 49 14.6).
+// chunks 19.9 us, 49 16.3).
 Plan make_plan(int N, int P, int C, int V) {
     Plan p;
     const int cv = (C + V - 1) / V;
@@ -1427,15 +1427,16 @@ struct Joined {
 // Vectors of a thread: with 16 four workgroups fit a compute unit's registers,
 // with 7 of x and 7 of dz (as fp32) three.  Shorter chunks, of which more fit,
 // wait more often (56x56x256 over 64 images backward: 7 vectors 103 us, 4
-// vectors at four workgroups 127; forward 112x112x128 over 32: 55.7, at 8
-// vectors and six workgroups 64).
+// vectors at four workgroups 127; forward 112x112x128 over 32, with fp32 sums:
+// 55.7, at 8 vectors and six workgroups 64).
 constexpr int kJoinedMost = 16, kJoinedMostBwd = 7;
 
 // Bytes of x from which one read saves more than the clearing launch and the
-// exchange cost (bf16, 256 channels of 56x56).  Forward: 8 MB 14.5 us against
-// 18.1 streaming, but 112x112x64 14.1 against 14.5, 4 MB 12.5 against 12.8.
-// Quantised: 16 MB even, 32 MB ahead by 2 us.  Backward: 32 MB 45.7 against
-// 41.7, 64 MB 70 against 74, 128 MB 123 against 148.
+// exchange cost (bf16, 256 channels of 56x56).  Forward: 3 MB 13.0 us against
+// 12.5 streaming, 8 MB 13.3 against 17.0 (112x112x64 12.7 against 15.1), 16 MB 15.9
+// against 19.4.  Quantised: 16 MB 19.6 against 21.0, 24 MB 25.1 against 25.4, 32
+// MB 26.0 against 29.0.  Backward: 32 MB 44.5 against 38.2, 48 MB 57.9 against
+// 56.7, 64 MB 70 against 75, 128 MB 123 against 146.
 constexpr long long kJoinedBytes = 12 << 20, kJoinedBytesQuant = 24 << 20, kJoinedBytesBwd = 48 << 20;
 
 // Every workgroup reads its image's words: at most a quarter of what it reads of x.

@@ -12,8 +12,9 @@
 //   skinny  up to 64 rows: the weights stream from memory straight into the
 //           matrix unit's registers, 16 or 32 channels per workgroup, the waves
 //           split k and join in LDS.  Bound by reading the weights (one row of
-//           4096, 16384 channels: 67 MB in 17.4 us, 3.9 TB/s) and, with more
-//           rows, by every workgroup reading all of them.
+//           4096, 16384 channels: 67 MB in 18.0 us, 3.7 TB/s, from memory, in
+//           14.6 where the last-level cache holds them) and, with more rows, by
+//           every workgroup reading all of them.
 //   tiled   BM rows x BN channels per workgroup, 128 bytes of k per stage,
 //           copied from memory into two LDS buffers without passing through
 //           registers.  Bound by the matrix unit.
@@ -56,8 +57,10 @@ __device__ __forceinline__ float finish(int acc, float scale, float bias, bool r
 
 // One workgroup: NG * 16 channels, MT * 16 rows, all of k.  Channels are the
 // rows of the 16x16 result, so a lane ends with 4 consecutive channels of one
-// row.  128 bytes of k per wave and step, so that a step reads whole lines; U
-// steps are in flight.
+// row.  128 bytes of k per wave and step, so that a step reads whole lines.  The
+// loads of U steps stand before their products; the compiler sinks part of them
+// (67 registers at U = 8, where all of them would take 128), so that fewer are in
+// flight.
 template <int MT, int NG, int U, typename OUT>
 __global__ void int8_skinny_kernel(Int8Args a) {
     extern __shared__ i32x4 red[];   // [wave][NG][MT][64]
@@ -420,8 +423,8 @@ __global__ __launch_bounds__(WM * WN * 64) void int8_tile_kernel(Int8Args a, int
 // channels, a wave 64 of them and every WM-th group of 16 * TJ rows; row tiles
 // of BM rows come through three LDS buffers, two tiles ahead of their use, and
 // results leave as whole 128-byte lines while the next tiles arrive.  The tile
-// kernel at one or two workgroups per compute unit loads, then stores: 28.2 us
-// where this takes 20.5 (100352 x 256 rows, 256 channels, bf16 results).
+// kernel at one or two workgroups per compute unit loads, then stores: 30.7 us
+// where this takes 20.3 (100352 x 256 rows, 256 channels, bf16 results).
 template <int KS, int WN, int TJ, typename OUT> struct StreamShape {
     static constexpr int WM = 8 / WN, BM = WM * 16 * TJ, BN = WN * 64;
     static constexpr int PR = KS * 4;                 // 16-byte pieces of a row
@@ -842,9 +845,9 @@ Int8Plan make_int8_plan(int M, int K, int N, bool aligned) {
         p.tn = (N + p.bn - 1) / p.bn;
         // enough tiles for each workgroup to earn the load of its weights:
         // 6 a compute unit up to k = 256 (16384 x 256 -> 1024, 4 each: 15.9 us
-        // against 14.3 tiled; 100352 x 256 -> 256, 6 each: 21.7 against 28.5),
+        // against 14.3 tiled; 100352 x 256 -> 256, 6 each: 20.3 against 30.7),
         // 16 above, where a tile is half as long (16384 x 512 -> 1024, 8 each:
-        // 22.4 against 17.0; 65536 x 512 -> 512, 16 each: 35.1 against 38.1)
+        // 22.4 against 17.0; 65536 x 512 -> 512, 16 each: 30.4 against 37.6)
         if ((long long)p.tm * p.tn >= (K <= 256 ? 6 : 16) * kUnits && (K <= 256 || N > 64)) return p;
     }
     auto tiles = [&](int b) { return (long long)((M + b - 1) / b) * ((N + b - 1) / b); };
@@ -880,13 +883,14 @@ template <int MT, int NG, int U, typename OUT> hipError_t skinny_instance(const 
 }
 
 // Two groups of 16 channels per workgroup use a row's values twice, where half
-// the workgroups still fill the chip and the rows are more than 16 (40 rows of
-// 4096, 16384 channels: 28.4 us against 38; 64 rows of 8192, 8192 channels: 34
-// against 45; but 4096 channels 18.2 against 16.3, and one row 20.6 against
-// 17.4).  Waves that split k: 4, or up to 16 where that leaves the chip few, of
-// at least 128 bytes of k each.  Up to 16 rows the steps in flight follow what
-// is left for a wave: 1 x 4096 -> 16384 takes 17.4 us with 8 and 21.2 with 4,
-// 1 x 2048 -> 2048 5.1 with 2 and 5.6 with 4.
+// the workgroups still fill the chip and the rows are more than 16 (weights from
+// memory: 40 rows of 4096, 16384 channels 28.4 us against 38.0; 64 rows of 8192,
+// 8192 channels 34.4 against 45.2; but 64 rows of 4096, 4096 channels 18.2 against
+// 16.4, and one row of 4096, 16384 channels 22.2 against 18.0).  Waves that split
+// k: 4, or up to 16 where that leaves the chip few, of at least 128 bytes of k
+// each.  Up to 16 rows the steps whose loads stand together follow what is left
+// for a wave: 1 x 4096 -> 16384 takes 18.0 us with 8 and 22.9 with 4, 1 x 2048 ->
+// 2048 4.9 with 2 and 5.7 with 4.
 template <typename OUT> hipError_t skinny(const Int8Args& a, hipStream_t st) {
     const int mt = a.M <= 16 ? 1 : a.M <= 32 ? 2 : 4;
     const bool pairs = mt > 1 && a.N >= 32 * kUnits;

@@ -366,6 +366,7 @@ int conv2d_group_norm_bwd_nhwc(const void* dy, const void* x, const float* gamma
  *   q int8 [M][K] (ldq apart) and scale fp32 [M]:
  *     a = max(max_k |x|, 2^-100),  q = round(x * (127 / a)) (to nearest even),
  *     scale = a / 127
+ *   in fp32: where x * 127 / a lies half way between two integers, either.
  *   A row that holds a NaN or an infinity gets scale NaN and q = 0, so every
  *   product with it is NaN.  q must not overlap x.  Also the way to quantise
  *   weights, whose rows are output channels.
