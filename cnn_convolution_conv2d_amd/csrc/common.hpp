@@ -33,40 +33,6 @@ struct SepShape {
     int dw_epilogue, pw_epilogue;  // CONV2D_EPI_* bits of each stage
 };
 
-// One group-norm call on channels-last data, validated on the host.  P pixels
-// per image; ld*: elements from one pixel to the next.  y is the output: the
-// activations, their 8-bit form (then q_scale holds a scale per pixel) or dx.
-struct NormArgs {
-    const void* x;
-    const void* dy;        // backward only
-    const float* gamma;    // null: 1
-    const float* beta;     // null: 0
-    void* y;
-    float* q_scale;
-    float* mean;           // [N][G]; forward: written unless null, backward: read
-    float* rstd;
-    float* dgamma;         // backward only; null: not wanted
-    float* dbeta;
-    int N, P, C, G;
-    long long ldx, ldy, lddy;
-    float eps;
-    int dtype;             // CONV2D_F32 / CONV2D_BF16
-};
-
-// One int8 product, validated on the host: q [M][K], w [N][K], y [M][N], with
-// ld*: elements from one row to the next.
-struct Int8Args {
-    const int8_t* q;
-    const int8_t* w;
-    const float* q_scale;
-    const float* w_scale;
-    const float* bias;     // null: none
-    void* y;
-    int M, K, N;
-    long long ldq, ldw, ldy;
-    bool relu;
-};
-
 enum Layout { NCHW = 0, NHWC = 1 };
 // raw [Cout][Cin/G][Kh][Kw], packed [Cout][Kh][Kw][Cin/G], depthwise [Kh][Kw][C],
 // transposed-convolution raw [Cin][Cout/G][Kh][Kw]
@@ -159,10 +125,6 @@ inline bool buffer_addressable(const Shape& s) {
 // workgroups and walk their items in a grid-stride loop, so any cap >= 1 is
 // valid; a small one makes every workgroup walk several items.
 int grid_limit();
-
-// Looks at another workgroup's result before a workgroup computes it itself, set
-// by conv2d_set_wait_limit.
-int wait_limit();
 inline long long persistent_slots(long long resident) {
     const int lim = grid_limit();
     return (lim > 0 && lim < resident) ? lim : resident;
@@ -233,20 +195,6 @@ bool winograd_supports(const Shape& s);
 hipError_t launch_winograd(const Shape& s, const void* x, const void* w_wino, const float* bias, void* y,
                            hipStream_t st);
 hipError_t launch_winograd_weights(const void* w, void* w_wino, int Cout, int Cin, hipStream_t st);
-
-// Group norm: the bytes of workspace and the three passes (one to four launches
-// each; act: CONV2D_ACT_*).
-size_t group_norm_workspace(int N, int P, int C, int G, int backward);
-hipError_t launch_group_norm(const NormArgs& a, int act, void* ws, hipStream_t st);
-hipError_t launch_group_norm_quant(const NormArgs& a, int act, void* ws, hipStream_t st);
-hipError_t launch_group_norm_bwd(const NormArgs& a, int act, void* ws, hipStream_t st);
-
-// 8-bit integer products.
-size_t int8_matmul_workspace(int M, int K, int N);
-bool int8_matmul_supports(int M, int K, int N, long long ldq, long long ldw);
-hipError_t launch_int8_matmul(const Int8Args& a, int out_f32, void* ws, hipStream_t st);
-hipError_t launch_quantize_rows(const void* x, void* q, float* scale, int M, int K, long long ldx, long long ldq,
-                                int dtype, hipStream_t st);
 
 hipError_t launch_transpose(const void* src, void* dst, int batch, int rows, int cols,
                             int elem_bytes, hipStream_t st);

@@ -13,6 +13,7 @@
 
 #include "../../include/conv2d.h"
 #include "common.hpp"
+#include "operators.hpp"
 
 using namespace conv2d;
 

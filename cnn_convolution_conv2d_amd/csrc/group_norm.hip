@@ -48,6 +48,7 @@
 // Resident: the mean from an fp64 sum, then the deviations from it in a second
 // pass over the registers.
 #include "mfma.hpp"
+#include "operators.hpp"
 #include "rowvec.hpp"
 
 namespace conv2d {

@@ -28,6 +28,7 @@
 #include <type_traits>
 
 #include "mfma.hpp"
+#include "operators.hpp"
 #include "rowvec.hpp"
 
 namespace conv2d {
