@@ -166,7 +166,7 @@ template <typename T, int V> struct Moments {
         for (int j = 0; j < V; ++j) {
             const double d = s[j] * inv;
             const float m2 = (float)(ss[j] - s[j] * d);
-            out[j] = make_float2(cnt > 0 ? (float)(k[j] + d) : 0.0f, m2 < 0.0f ? 0.0f : m2);  // a NaN stays
+            out[j] = cnt > 0 ? make_float2((float)(k[j] + d), m2 < 0.0f ? 0.0f : m2) : make_float2(0.0f, 0.0f);  // a NaN stays
         }
     }
 };
