@@ -19,7 +19,7 @@ LIB_PATH = os.environ.get("CONV2D_LIBRARY") or os.path.join(_HERE, "libconv2d.so
 
 F32, BF16 = 0, 1
 EPI_NONE, EPI_BIAS, EPI_RELU = 0, 1, 2
-ACT_NONE, ACT_RELU, ACT_SILU = 0, 1, 2
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU = 0, 1, 2, 3
 PATH_AUTO, PATH_DIRECT, PATH_DEPTHWISE, PATH_GEMM1X1, PATH_IGEMM = 0, 1, 2, 3, 4
 PATH_IGEMM_GATHER, PATH_IGEMM_HALO = 5, 6
 PATH_NAMES = {PATH_DIRECT: "direct", PATH_DEPTHWISE: "depthwise", PATH_GEMM1X1: "gemm1x1",
@@ -38,6 +38,9 @@ EXPORTS = ("conv2d_fwd", "conv2d_fwd_noalloc", "conv2d_fwd_nhwc_packed", "conv2d
            "conv2d_group_norm_workspace_bytes", "conv2d_group_norm_nhwc", "conv2d_group_norm_quant_nhwc",
            "conv2d_group_norm_bwd_nhwc", "conv2d_quantize_rows", "conv2d_int8_matmul_workspace_bytes",
            "conv2d_int8_matmul",
+           "conv2d_rms_norm", "conv2d_rms_norm_quant", "conv2d_rms_norm_bwd_workspace_bytes", "conv2d_rms_norm_bwd",
+           "conv2d_matmul_workspace_bytes", "conv2d_matmul", "conv2d_matmul_bwd_workspace_bytes", "conv2d_matmul_bwd",
+           "conv2d_dropout",
            "conv2d_packed_weight_bytes",
            "conv2d_pack_weights", "conv2d_nchw_to_nhwc", "conv2d_nhwc_to_nchw",
            "conv2d_out_dim", "conv2d_check_args", "conv2d_select_path",
@@ -92,8 +95,19 @@ def _load() -> ctypes.CDLL:
     lib.conv2d_quantize_rows.argtypes = [P] * 3 + [I] * 5 + [P]
     lib.conv2d_int8_matmul_workspace_bytes.argtypes, lib.conv2d_int8_matmul_workspace_bytes.restype = [I] * 3, Z
     lib.conv2d_int8_matmul.argtypes = [P] * 7 + [Z] + [I] * 8 + [P]
+    lib.conv2d_rms_norm.argtypes = [P] * 6 + [I] * 6 + [F, I, P]
+    lib.conv2d_rms_norm_quant.argtypes = [P] * 7 + [I] * 6 + [F, I, P]
+    lib.conv2d_rms_norm_bwd_workspace_bytes.argtypes, lib.conv2d_rms_norm_bwd_workspace_bytes.restype = [I] * 2, Z
+    lib.conv2d_rms_norm_bwd.argtypes = [P] * 8 + [Z] + [I] * 7 + [P]
+    for name in ("conv2d_matmul_workspace_bytes", "conv2d_matmul_bwd_workspace_bytes"):
+        f = getattr(lib, name)
+        f.argtypes, f.restype = [I] * 4, Z
+    lib.conv2d_matmul.argtypes = [P] * 7 + [Z] + [I] * 10 + [P]
+    lib.conv2d_matmul_bwd.argtypes = [P] * 8 + [Z] + [I] * 11 + [P]
+    lib.conv2d_dropout.argtypes = [P] * 4 + [F] + [I] * 6 + [P]
     for name in ("conv2d_group_norm_nhwc", "conv2d_group_norm_quant_nhwc", "conv2d_group_norm_bwd_nhwc",
-                 "conv2d_quantize_rows", "conv2d_int8_matmul"):
+                 "conv2d_quantize_rows", "conv2d_int8_matmul", "conv2d_rms_norm", "conv2d_rms_norm_quant",
+                 "conv2d_rms_norm_bwd", "conv2d_matmul", "conv2d_matmul_bwd", "conv2d_dropout"):
         getattr(lib, name).restype = I
     lib.conv2d_packed_weight_bytes.argtypes = [I] * 6
     lib.conv2d_packed_weight_bytes.restype = ctypes.c_size_t
@@ -158,6 +172,12 @@ _group_norm_quant = _address("conv2d_group_norm_quant_nhwc")
 _group_norm_bwd = _address("conv2d_group_norm_bwd_nhwc")
 _quantize_rows = _address("conv2d_quantize_rows")
 _int8_matmul = _address("conv2d_int8_matmul")
+_rms_norm = _address("conv2d_rms_norm")
+_rms_norm_quant = _address("conv2d_rms_norm_quant")
+_rms_norm_bwd = _address("conv2d_rms_norm_bwd")
+_matmul = _address("conv2d_matmul")
+_matmul_bwd = _address("conv2d_matmul_bwd")
+_dropout = _address("conv2d_dropout")
 
 
 def _ptr(t) -> int | None:
@@ -368,6 +388,78 @@ def conv2d_int8_matmul(q, q_scale, w, w_scale, bias, y, workspace, workspace_byt
                               ldw, ldy, dtype, epilogue, _raw_stream() if stream is None else _stream(stream))
     if rc < 0:
         raise Conv2dError(rc, "conv2d_int8_matmul")
+
+
+def conv2d_rms_norm(x, residual, gamma, h, y, rstd, M, C, ldx, ldr, ldh, ldy, eps, dtype, stream=None) -> None:
+    """h = x + residual (or None) and its root-mean-square norm y = h rstd gamma;
+    fp32 gamma [C] or None; h and rstd (fp32 [M]) written, or None."""
+    rc = _binding.rms_norm(_rms_norm, x, residual, gamma, h, y, rstd, M, C, ldx, ldr, ldh, ldy, eps, dtype,
+                           _raw_stream() if stream is None else _stream(stream))
+    if rc < 0:
+        raise Conv2dError(rc, "conv2d_rms_norm")
+
+
+def conv2d_rms_norm_quant(x, residual, gamma, h, q, q_scale, rstd, M, C, ldx, ldr, ldh, ldq, eps, dtype,
+                          stream=None) -> None:
+    """The norm quantised for each row: int8 q and fp32 q_scale [M], the rows of
+    conv2d_int8_matmul."""
+    rc = _binding.rms_norm_quant(_rms_norm_quant, x, residual, gamma, h, q, q_scale, rstd, M, C, ldx, ldr, ldh, ldq, eps,
+                                 dtype, _raw_stream() if stream is None else _stream(stream))
+    if rc < 0:
+        raise Conv2dError(rc, "conv2d_rms_norm_quant")
+
+
+def conv2d_rms_norm_bwd_workspace_bytes(M, C) -> int:
+    return int(lib.conv2d_rms_norm_bwd_workspace_bytes(M, C))
+
+
+def conv2d_rms_norm_bwd(dy, dh, h, gamma, rstd, dx, dgamma, workspace, workspace_bytes, M, C, lddy, lddh, ldh, lddx,
+                        dtype, stream=None) -> None:
+    """Gradients of conv2d_rms_norm from dy, the saved h and rstd and dh (the
+    gradient that reaches h from elsewhere, or None): dx, of x and the residual
+    alike, and fp32 dgamma [C] or None."""
+    rc = _binding.rms_norm_bwd(_rms_norm_bwd, dy, dh, h, gamma, rstd, dx, dgamma, workspace, workspace_bytes, M, C, lddy,
+                               lddh, ldh, lddx, dtype, _raw_stream() if stream is None else _stream(stream))
+    if rc < 0:
+        raise Conv2dError(rc, "conv2d_rms_norm_bwd")
+
+
+def conv2d_matmul_workspace_bytes(M, K, N, dtype) -> int:
+    return int(lib.conv2d_matmul_workspace_bytes(M, K, N, dtype))
+
+
+def conv2d_matmul(x, w, bias, residual, z, y, workspace, workspace_bytes, M, K, N, ldx, ldw, ldr, ldz, ldy, dtype, act,
+                  stream=None) -> None:
+    """y = act(z) + residual with z = x [M][K] w [N][K]^T + bias; bias (fp32 [N]),
+    residual and z (written) may be None."""
+    rc = _binding.matmul(_matmul, x, w, bias, residual, z, y, workspace, workspace_bytes, M, K, N, ldx, ldw, ldr, ldz, ldy,
+                         dtype, act, _raw_stream() if stream is None else _stream(stream))
+    if rc < 0:
+        raise Conv2dError(rc, "conv2d_matmul")
+
+
+def conv2d_matmul_bwd_workspace_bytes(M, K, N, dtype) -> int:
+    return int(lib.conv2d_matmul_bwd_workspace_bytes(M, K, N, dtype))
+
+
+def conv2d_matmul_bwd(dy, z, x, w, dx, dw, dbias, workspace, workspace_bytes, M, K, N, lddy, ldz, ldx, ldw, lddx, lddw,
+                      dtype, act, stream=None) -> None:
+    """Gradients of conv2d_matmul from dy, the kept z (None without an activation),
+    x and w: dx, dw and fp32 dbias [N], each or None."""
+    rc = _binding.matmul_bwd(_matmul_bwd, dy, z, x, w, dx, dw, dbias, workspace, workspace_bytes, M, K, N, lddy, ldz, ldx,
+                             ldw, lddx, lddw, dtype, act, _raw_stream() if stream is None else _stream(stream))
+    if rc < 0:
+        raise Conv2dError(rc, "conv2d_matmul_bwd")
+
+
+def conv2d_dropout(x, residual, y, rng, p, M, C, ldx, ldr, ldy, dtype, stream=None) -> None:
+    """y = residual (or None) + x with each element dropped with probability p, the
+    others divided by 1 - p; rng: two 64-bit words on the device, seed and offset.
+    On dy, without a residual, it is the gradient."""
+    rc = _binding.dropout(_dropout, x, residual, y, rng, p, M, C, ldx, ldr, ldy, dtype,
+                          _raw_stream() if stream is None else _stream(stream))
+    if rc < 0:
+        raise Conv2dError(rc, "conv2d_dropout")
 
 
 def conv2d_packed_weight_bytes(Cout, Cin, Kh, Kw, groups, dtype) -> int:

@@ -1,5 +1,5 @@
 /* binding.c -- a small C extension that calls the library's operator entries
- * (group norm, rows in 8 bits, integer products) from Python.
+ * (norms, rows in 8 bits, products, dropout) from Python.
  *
  * These calls take a few microseconds of GPU time for small inputs, and
  * marshalling 17 to 20 arguments through ctypes took 8 to 9 microseconds of
@@ -122,9 +122,84 @@ static PyObject* int8_matmul(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     CALL(((product_fn)p0)(p1, p2, p3, p4, p5, p6, p7, bytes, i9, i10, i11, i12, i13, i14, i15, i16, p17));
 }
 
+typedef int (*rms_fn)(void*, void*, void*, void*, void*, void*, int, int, int, int, int, int, float, int, void*);
+
+static PyObject* rms_norm(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    if (!arity("rms_norm", n, 16)) return NULL;
+    P(0); P(1); P(2); P(3); P(4); P(5); P(6);
+    I(7); I(8); I(9); I(10); I(11); I(12);
+    const float eps = as_float(a[13]);
+    I(14); P(15);
+    CALL(((rms_fn)p0)(p1, p2, p3, p4, p5, p6, i7, i8, i9, i10, i11, i12, eps, i14, p15));
+}
+
+typedef int (*rms_quant_fn)(void*, void*, void*, void*, void*, void*, void*, int, int, int, int, int, int, float, int,
+                            void*);
+
+static PyObject* rms_norm_quant(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    if (!arity("rms_norm_quant", n, 17)) return NULL;
+    P(0); P(1); P(2); P(3); P(4); P(5); P(6); P(7);
+    I(8); I(9); I(10); I(11); I(12); I(13);
+    const float eps = as_float(a[14]);
+    I(15); P(16);
+    CALL(((rms_quant_fn)p0)(p1, p2, p3, p4, p5, p6, p7, i8, i9, i10, i11, i12, i13, eps, i15, p16));
+}
+
+typedef int (*rms_bwd_fn)(void*, void*, void*, void*, void*, void*, void*, void*, size_t, int, int, int, int, int, int,
+                          int, void*);
+
+static PyObject* rms_norm_bwd(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    if (!arity("rms_norm_bwd", n, 18)) return NULL;
+    P(0); P(1); P(2); P(3); P(4); P(5); P(6); P(7); P(8);
+    const size_t bytes = as_size(a[9]);
+    I(10); I(11); I(12); I(13); I(14); I(15); I(16); P(17);
+    CALL(((rms_bwd_fn)p0)(p1, p2, p3, p4, p5, p6, p7, p8, bytes, i10, i11, i12, i13, i14, i15, i16, p17));
+}
+
+typedef int (*matmul_fn)(void*, void*, void*, void*, void*, void*, void*, size_t, int, int, int, int, int, int, int, int,
+                         int, int, void*);
+
+static PyObject* matmul(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    if (!arity("matmul", n, 20)) return NULL;
+    P(0); P(1); P(2); P(3); P(4); P(5); P(6); P(7);
+    const size_t bytes = as_size(a[8]);
+    I(9); I(10); I(11); I(12); I(13); I(14); I(15); I(16); I(17); I(18); P(19);
+    CALL(((matmul_fn)p0)(p1, p2, p3, p4, p5, p6, p7, bytes, i9, i10, i11, i12, i13, i14, i15, i16, i17, i18, p19));
+}
+
+typedef int (*matmul_bwd_fn)(void*, void*, void*, void*, void*, void*, void*, void*, size_t, int, int, int, int, int, int,
+                             int, int, int, int, int, void*);
+
+static PyObject* matmul_bwd(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    if (!arity("matmul_bwd", n, 22)) return NULL;
+    P(0); P(1); P(2); P(3); P(4); P(5); P(6); P(7); P(8);
+    const size_t bytes = as_size(a[9]);
+    I(10); I(11); I(12); I(13); I(14); I(15); I(16); I(17); I(18); I(19); I(20); P(21);
+    CALL(((matmul_bwd_fn)p0)(p1, p2, p3, p4, p5, p6, p7, p8, bytes, i10, i11, i12, i13, i14, i15, i16, i17, i18, i19, i20,
+                             p21));
+}
+
+typedef int (*dropout_fn)(void*, void*, void*, void*, float, int, int, int, int, int, int, void*);
+
+static PyObject* dropout(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    if (!arity("dropout", n, 13)) return NULL;
+    P(0); P(1); P(2); P(3); P(4);
+    const float p = as_float(a[5]);
+    I(6); I(7); I(8); I(9); I(10); I(11); P(12);
+    CALL(((dropout_fn)p0)(p1, p2, p3, p4, p, i6, i7, i8, i9, i10, i11, p12));
+}
+
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {METHOD(group_norm), METHOD(group_norm_quant), METHOD(group_norm_bwd),
-                                METHOD(quantize_rows), METHOD(int8_matmul), {NULL, NULL, 0, NULL}};
+                                METHOD(quantize_rows), METHOD(int8_matmul), METHOD(rms_norm),
+                                METHOD(rms_norm_quant), METHOD(rms_norm_bwd), METHOD(matmul), METHOD(matmul_bwd),
+                                METHOD(dropout), {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {.m_base = PyModuleDef_HEAD_INIT, .m_name = "_binding", .m_size = -1,
                                     .m_methods = methods};
 

@@ -482,6 +482,60 @@ int validate_norm(const NormArgs& a, int H, int W, int act, const void* ws, size
     return CONV2D_OK;
 }
 
+// A workspace of at least `need` bytes.
+int check_workspace(const void* ws, size_t bytes, size_t need) {
+    if (!need) return CONV2D_OK;
+    if (!ws) return set_error(CONV2D_ERR_NULL, "the workspace is NULL (%zu bytes needed)", need);
+    if (reinterpret_cast<uintptr_t>(ws) & 15u) return set_error(CONV2D_ERR_ALIGN, "the workspace must be 16-byte aligned");
+    if (bytes < need) return set_error(CONV2D_ERR_ARG, "the workspace has %zu bytes, %zu are needed", bytes, need);
+    return CONV2D_OK;
+}
+
+// A tensor of rows (null: not given): its stride holds a row, its address is
+// aligned to its elements.
+int check_rows(const char* name, const void* p, long long ld, int row, size_t eb) {
+    if (!p) return CONV2D_OK;
+    if (ld < row) return set_error(CONV2D_ERR_ARG, "the row stride %lld of %s is below %d", ld, name, row);
+    if (reinterpret_cast<uintptr_t>(p) % eb) return set_error(CONV2D_ERR_ALIGN, "%s is not aligned to its elements", name);
+    return CONV2D_OK;
+}
+
+// An output over an input needs the input's stride.
+bool shifted_over(const void* out, long long ldo, const void* in, long long ldi) { return out && out == in && ldo != ldi; }
+
+// What the three RMS-norm entries check alike.
+int validate_rms(const RmsArgs& a, bool quant) {
+    if (a.dtype != CONV2D_F32 && a.dtype != CONV2D_BF16) return set_error(CONV2D_ERR_DTYPE, "unknown dtype %d", a.dtype);
+    if (a.M < 1 || a.C < 1) return set_error(CONV2D_ERR_ARG, "sizes must be >= 1 (M=%d C=%d)", a.M, a.C);
+    if (!(a.eps >= 0.0f) || a.eps > 3e38f) return set_error(CONV2D_ERR_ARG, "eps must be >= 0 and finite");
+    if (!a.x || !a.y) return set_error(CONV2D_ERR_NULL, "the rows and the output must be non-NULL");
+    const size_t eb = elem_bytes(a.dtype);
+    int rc = check_rows("the first tensor", a.x, a.ldx, a.C, eb);
+    if (!rc) rc = check_rows("the second tensor", a.residual, a.ldr, a.C, eb);
+    if (!rc) rc = check_rows("h", a.h, a.ldh, a.C, eb);
+    if (!rc) rc = check_rows("the output", a.y, a.ldy, a.C, quant ? 1 : eb);
+    if (!rc && (reinterpret_cast<uintptr_t>(a.gamma) | reinterpret_cast<uintptr_t>(a.rstd) |
+                reinterpret_cast<uintptr_t>(a.q_scale) | reinterpret_cast<uintptr_t>(a.dgamma)) % 4)
+        rc = set_error(CONV2D_ERR_ALIGN, "an fp32 array is not aligned to its elements");
+    if (!rc && a.C > kRmsMostC) rc = set_error(CONV2D_ERR_UNSUPPORTED, "RMS norm takes C <= %d", kRmsMostC);
+    return rc;
+}
+
+int validate_matmul(int M, int K, int N, int dtype, int act) {
+    if (dtype != CONV2D_F32 && dtype != CONV2D_BF16) return set_error(CONV2D_ERR_DTYPE, "unknown dtype %d", dtype);
+    if (act < CONV2D_ACT_NONE || act > CONV2D_ACT_GELU) return set_error(CONV2D_ERR_EPILOGUE, "unknown activation %d", act);
+    if (M < 1 || K < 1 || N < 1) return set_error(CONV2D_ERR_ARG, "sizes must be >= 1 (M=%d K=%d N=%d)", M, K, N);
+    return CONV2D_OK;
+}
+
+// An operand of a product: a tensor that is read with 32-bit offsets in a tile.
+int check_operand(const char* name, const void* p, long long ld, int row, size_t eb) {
+    const int rc = check_rows(name, p, ld, row, eb);
+    if (!rc && p && ld > kMatmulMostLd)
+        return set_error(CONV2D_ERR_UNSUPPORTED, "the row stride %lld of %s is above %d", ld, name, kMatmulMostLd);
+    return rc;
+}
+
 }  // namespace
 
 int conv2d::grid_limit() { return __atomic_load_n(&g_grid_limit, __ATOMIC_RELAXED); }
@@ -894,6 +948,153 @@ int conv2d_int8_matmul(const void* q, const float* q_scale, const void* w, const
     a.relu = (epilogue & CONV2D_EPI_RELU) != 0;
     const hipError_t e = launch_int8_matmul(a, dtype == CONV2D_F32, workspace, stream);
     return e == hipSuccess ? CONV2D_OK : hip_fail(e, "int8 product launch");
+}
+
+int conv2d_rms_norm(const void* x, const void* residual, const float* gamma, void* h, void* y, float* rstd, int M, int C,
+                    int ldx, int ldr, int ldh, int ldy, float eps, int dtype, hipStream_t stream) {
+    RmsArgs a = {};
+    a.x = x; a.residual = residual; a.gamma = gamma; a.h = h; a.y = y; a.rstd = rstd;
+    a.M = M; a.C = C; a.ldx = ldx; a.ldr = ldr; a.ldh = ldh; a.ldy = ldy; a.eps = eps; a.dtype = dtype;
+    const int rc = validate_rms(a, false);
+    if (rc) return rc;
+    if (h == y) return set_error(CONV2D_ERR_ARG, "h must not be y");
+    if (shifted_over(y, ldy, x, ldx) || shifted_over(y, ldy, residual, ldr) || shifted_over(h, ldh, x, ldx) ||
+        shifted_over(h, ldh, residual, ldr))
+        return set_error(CONV2D_ERR_ARG, "an output over an input needs its row stride");
+    const hipError_t e = launch_rms_norm(a, stream);
+    return e == hipSuccess ? CONV2D_OK : hip_fail(e, "RMS norm launch");
+}
+
+int conv2d_rms_norm_quant(const void* x, const void* residual, const float* gamma, void* h, void* q, float* q_scale,
+                          float* rstd, int M, int C, int ldx, int ldr, int ldh, int ldq, float eps, int dtype,
+                          hipStream_t stream) {
+    RmsArgs a = {};
+    a.x = x; a.residual = residual; a.gamma = gamma; a.h = h; a.y = q; a.q_scale = q_scale; a.rstd = rstd;
+    a.M = M; a.C = C; a.ldx = ldx; a.ldr = ldr; a.ldh = ldh; a.ldy = ldq; a.eps = eps; a.dtype = dtype;
+    if (!q_scale) return set_error(CONV2D_ERR_NULL, "q_scale must be non-NULL");
+    const int rc = validate_rms(a, true);
+    if (rc) return rc;
+    // a row's bytes lie over other rows' values, which other workgroups still read
+    if (q == x || q == residual || q == h) return set_error(CONV2D_ERR_ARG, "q must not be x, the residual or h");
+    if (shifted_over(h, ldh, x, ldx) || shifted_over(h, ldh, residual, ldr))
+        return set_error(CONV2D_ERR_ARG, "an output over an input needs its row stride");
+    const hipError_t e = launch_rms_norm_quant(a, stream);
+    return e == hipSuccess ? CONV2D_OK : hip_fail(e, "quantised RMS norm launch");
+}
+
+size_t conv2d_rms_norm_bwd_workspace_bytes(int M, int C) {
+    if (M < 1 || C < 1 || C > kRmsMostC) return 0;
+    return round_up(rms_norm_bwd_workspace(M, C), 16);
+}
+
+int conv2d_rms_norm_bwd(const void* dy, const void* dh, const void* h, const float* gamma, const float* rstd, void* dx,
+                        float* dgamma, void* workspace, size_t workspace_bytes, int M, int C, int lddy, int lddh, int ldh,
+                        int lddx, int dtype, hipStream_t stream) {
+    RmsArgs a = {};
+    a.x = dy; a.residual = dh; a.gamma = gamma; a.h = const_cast<void*>(h); a.y = dx;
+    a.rstd = const_cast<float*>(rstd); a.dgamma = dgamma;
+    a.M = M; a.C = C; a.ldx = lddy; a.ldr = lddh; a.ldh = ldh; a.ldy = lddx; a.dtype = dtype;
+    if (!h || !rstd) return set_error(CONV2D_ERR_NULL, "h and rstd must be non-NULL");
+    int rc = validate_rms(a, false);
+    if (!rc) rc = check_workspace(workspace, workspace_bytes, dgamma ? conv2d_rms_norm_bwd_workspace_bytes(M, C) : 0);
+    if (rc) return rc;
+    if (shifted_over(dx, lddx, dy, lddy) || shifted_over(dx, lddx, dh, lddh) || shifted_over(dx, lddx, h, ldh))
+        return set_error(CONV2D_ERR_ARG, "an output over an input needs its row stride");
+    const hipError_t e = launch_rms_norm_bwd(a, workspace, stream);
+    return e == hipSuccess ? CONV2D_OK : hip_fail(e, "RMS norm backward launch");
+}
+
+size_t conv2d_matmul_workspace_bytes(int M, int K, int N, int dtype) {
+    if (M < 1 || K < 1 || N < 1 || (dtype != CONV2D_F32 && dtype != CONV2D_BF16) || !matmul_supports(M, K, N)) return 0;
+    return round_up(matmul_workspace(M, K, N, dtype), 16);
+}
+
+int conv2d_matmul(const void* x, const void* w, const float* bias, const void* residual, void* z, void* y, void* workspace,
+                  size_t workspace_bytes, int M, int K, int N, int ldx, int ldw, int ldr, int ldz, int ldy, int dtype,
+                  int act, hipStream_t stream) {
+    int rc = validate_matmul(M, K, N, dtype, act);
+    if (rc) return rc;
+    if (!x || !w || !y) return set_error(CONV2D_ERR_NULL, "x, w and y must be non-NULL");
+    const size_t eb = elem_bytes(dtype);
+    rc = check_operand("x", x, ldx, K, eb);
+    if (!rc) rc = check_operand("w", w, ldw, K, eb);
+    if (!rc) rc = check_rows("the residual", residual, ldr, N, eb);
+    if (!rc) rc = check_rows("z", z, ldz, N, eb);
+    if (!rc) rc = check_rows("y", y, ldy, N, eb);
+    if (!rc) rc = check_rows("the bias", bias, N, N, 4);
+    if (rc) return rc;
+    if (y == x || y == w || z == y || (z && (z == x || z == w || z == residual)))
+        return set_error(CONV2D_ERR_ARG, "z and y must not be an operand or each other");
+    if (shifted_over(y, ldy, residual, ldr)) return set_error(CONV2D_ERR_ARG, "y over the residual needs its row stride");
+    if (!matmul_supports(M, K, N)) return set_error(CONV2D_ERR_UNSUPPORTED, "too many results (M=%d K=%d N=%d)", M, K, N);
+    rc = check_workspace(workspace, workspace_bytes, conv2d_matmul_workspace_bytes(M, K, N, dtype));
+    if (rc) return rc;
+    MatmulArgs a = {};
+    a.x = x; a.w = w; a.bias = bias; a.residual = residual; a.z = z; a.y = y;
+    a.M = M; a.K = K; a.N = N; a.ldx = ldx; a.ldw = ldw; a.ldr = ldr; a.ldz = ldz; a.ldy = ldy; a.dtype = dtype; a.act = act;
+    const hipError_t e = launch_matmul(a, workspace, stream);
+    return e == hipSuccess ? CONV2D_OK : hip_fail(e, "product launch");
+}
+
+size_t conv2d_matmul_bwd_workspace_bytes(int M, int K, int N, int dtype) {
+    if (M < 1 || K < 1 || N < 1 || (dtype != CONV2D_F32 && dtype != CONV2D_BF16) || !matmul_supports(M, K, N)) return 0;
+    return round_up(matmul_bwd_workspace(M, K, N, dtype), 16);
+}
+
+int conv2d_matmul_bwd(const void* dy, const void* z, const void* x, const void* w, void* dx, void* dw, float* dbias,
+                      void* workspace, size_t workspace_bytes, int M, int K, int N, int lddy, int ldz, int ldx, int ldw,
+                      int lddx, int lddw, int dtype, int act, hipStream_t stream) {
+    int rc = validate_matmul(M, K, N, dtype, act);
+    if (rc) return rc;
+    if (act == CONV2D_ACT_NONE) z = nullptr;
+    if (!dy || !x || !w) return set_error(CONV2D_ERR_NULL, "dy, x and w must be non-NULL");
+    if (act != CONV2D_ACT_NONE && !z) return set_error(CONV2D_ERR_NULL, "z is NULL but the activation needs it");
+    if (!dx && !dw && !dbias) return set_error(CONV2D_ERR_NULL, "one of dx, dw and dbias must be non-NULL");
+    const size_t eb = elem_bytes(dtype);
+    rc = check_operand("dy", dy, lddy, N, eb);
+    if (!rc) rc = check_operand("z", z, ldz, N, eb);
+    if (!rc) rc = check_operand("x", x, ldx, K, eb);
+    if (!rc) rc = check_operand("w", w, ldw, K, eb);
+    if (!rc) rc = check_rows("dx", dx, lddx, K, eb);
+    if (!rc) rc = check_rows("dw", dw, lddw, K, eb);
+    if (!rc) rc = check_rows("dbias", dbias, N, N, 4);
+    if (rc) return rc;
+    for (const void* out : {(const void*)dx, (const void*)dw, (const void*)dbias})
+        if (out && (out == dy || out == z || out == x || out == w))
+            return set_error(CONV2D_ERR_ARG, "an output must not be an input");
+    if (dx && dx == dw) return set_error(CONV2D_ERR_ARG, "dx must not be dw");
+    if (!matmul_supports(M, K, N)) return set_error(CONV2D_ERR_UNSUPPORTED, "too many results (M=%d K=%d N=%d)", M, K, N);
+    rc = check_workspace(workspace, workspace_bytes, conv2d_matmul_bwd_workspace_bytes(M, K, N, dtype));
+    if (rc) return rc;
+    MatmulBwdArgs a = {};
+    a.dy = dy; a.z = z; a.x = x; a.w = w; a.dx = dx; a.dw = dw; a.dbias = dbias;
+    a.M = M; a.K = K; a.N = N; a.lddy = lddy; a.ldz = ldz; a.ldx = ldx; a.ldw = ldw; a.lddx = lddx; a.lddw = lddw;
+    a.dtype = dtype; a.act = act;
+    const hipError_t e = launch_matmul_bwd(a, workspace, stream);
+    return e == hipSuccess ? CONV2D_OK : hip_fail(e, "product backward launch");
+}
+
+int conv2d_dropout(const void* x, const void* residual, void* y, const unsigned long long* rng, float p, int M, int C,
+                   int ldx, int ldr, int ldy, int dtype, hipStream_t stream) {
+    if (dtype != CONV2D_F32 && dtype != CONV2D_BF16) return set_error(CONV2D_ERR_DTYPE, "unknown dtype %d", dtype);
+    if (M < 1 || C < 1) return set_error(CONV2D_ERR_ARG, "sizes must be >= 1 (M=%d C=%d)", M, C);
+    if (!(p >= 0.0f && p < 1.0f)) return set_error(CONV2D_ERR_ARG, "p must be in [0, 1)");
+    if (!x || !y || !rng) return set_error(CONV2D_ERR_NULL, "x, y and rng must be non-NULL");
+    const size_t eb = elem_bytes(dtype);
+    int rc = check_rows("x", x, ldx, C, eb);
+    if (!rc) rc = check_rows("the residual", residual, ldr, C, eb);
+    if (!rc) rc = check_rows("y", y, ldy, C, eb);
+    if (!rc) rc = check_rows("rng", rng, 2, 2, 8);
+    if (rc) return rc;
+    if (shifted_over(y, ldy, x, ldx) || shifted_over(y, ldy, residual, ldr))
+        return set_error(CONV2D_ERR_ARG, "an output over an input needs its row stride");
+    DropoutArgs a = {};
+    a.x = x; a.residual = residual; a.y = y; a.rng = rng;
+    a.threshold = (uint32_t)((double)p * 0x1p32);
+    a.scale = (float)(1.0 / (1.0 - (double)p));
+    a.M = M; a.C = C; a.ldx = ldx; a.ldr = ldr; a.ldy = ldy; a.dtype = dtype;
+    const hipError_t e = launch_dropout(a, stream);
+    return e == hipSuccess ? CONV2D_OK : hip_fail(e, "dropout launch");
 }
 
 void conv2d_release_scratch(void) {

@@ -30,15 +30,11 @@
 #include "mfma.hpp"
 #include "operators.hpp"
 #include "rowvec.hpp"
+#include "tiles.hpp"
 
 namespace conv2d {
 
 namespace {
-
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
-typedef u32x4 u32x4_unaligned __attribute__((aligned(2)));
-typedef __attribute__((address_space(3))) void* lds_ptr_t;
 
 // Descriptor of rows [r0, rows) of a row-major byte matrix, starting at row
 // r0: reads past its last byte (rows and k beyond the end) return 0.
@@ -128,33 +124,6 @@ __global__ void int8_skinny_kernel(Int8Args a) {
 
 // ------------------------------------------------------------------ tiles
 
-constexpr int kStageK = 128;  // bytes of k per stage: one line of every row
-
-// 16-byte slot of a stage's (row, 16-byte piece): the pieces of a row are
-// permuted so that 16 consecutive rows read at one piece hit all banks.
-__device__ __forceinline__ int slot_of(int row, int piece) { return row * 8 + (piece ^ ((row >> 1) & 7)); }
-
-struct TileAt {
-    int m0, n0, split;
-};
-
-// Block -> tile: every XCD walks a contiguous run (its L2 keeps the shared
-// rows), and within it tiles go down groups of 8 row tiles, channel tile by
-// channel tile.
-__device__ __forceinline__ TileAt tile_at(int tm, int tn, int BM, int BN) {
-    const int per = tm * tn;
-    int i = xcd_tile_index();
-    TileAt t;
-    t.split = i / per;
-    i %= per;
-    constexpr int GM = 8;
-    const int group = i / (GM * tn), first = group * GM, rows = min(GM, tm - first);
-    i -= group * GM * tn;
-    t.m0 = (first + i % rows) * BM;
-    t.n0 = (i / rows) * BN;
-    return t;
-}
-
 // The matrix products of a 64-byte step of k: TI x TJ blocks of 16 channels x
 // 16 rows.  The 16x16x64 form, not 32x32x32: on random bytes the matrix unit
 // is held back by power, not by issue, and the small form, which moves half
@@ -170,31 +139,6 @@ __device__ __forceinline__ void products(i32x4 (&acc)[TI][TJ], const i32x4 (&w)[
             const int i = j & 1 ? TI - 1 - n : n;
             acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[i], q[j], acc[i][j], 0, 0, 0);
         }
-}
-
-// The wave's accesses to its own piece of LDS before this are done before
-// those after it.
-__device__ __forceinline__ void wave_lds_fence() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
-// 16 bytes of results (8 bf16, 4 fp32 or int) to channels n .. of a row, fewer
-// at the row's end.  The address is aligned to an element only (a row may have
-// any length): one store all the same.
-template <typename OUT> __device__ __forceinline__ void store_piece(OUT* row, int n, int N, const uint4& v) {
-    constexpr int E = 16 / (int)sizeof(OUT);
-    if (n + E <= N) {
-        *reinterpret_cast<u32x4_unaligned*>(row + n) = __builtin_bit_cast(u32x4, v);
-    } else {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (n + e < N)
-                row[n + e] = sizeof(OUT) == 4 ? __builtin_bit_cast(OUT, (typename RawBytes<sizeof(OUT)>::type)w[e * (int)sizeof(OUT) / 4])
-                                              : __builtin_bit_cast(OUT, (typename RawBytes<sizeof(OUT)>::type)(w[e / 2] >> (16 * (e & 1))));
-    }
 }
 
 // Four channels of a row: scaled, biased, ReLU.
@@ -278,12 +222,6 @@ template <int BM, int BN> struct Scales {
 
 template <typename OUT> __device__ __forceinline__ OUT* out_of(const Int8Args& a, int split) {
     return static_cast<OUT*>(a.y) + (std::is_same_v<OUT, int> ? (long long)split * a.M * a.N : 0);
-}
-
-// A wave's copy of 1 KB into LDS, 16 bytes a lane: no registers, no LDS
-// instruction; an offset outside the matrix writes zeros.
-__device__ __forceinline__ void copy_kb(__amdgpu_buffer_rsrc_t r, char* dst, int off) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)dst, 16, off, 0, 0, 0);
 }
 
 __device__ __forceinline__ void copy_words(__amdgpu_buffer_rsrc_t r, char* dst, int off) {
@@ -449,8 +387,6 @@ __device__ __forceinline__ void stream_barrier() {
     __builtin_amdgcn_s_barrier();
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
-
-constexpr int vmcnt_of(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0f70; }  // lgkmcnt, expcnt: no wait
 
 // Block j of 16 rows of a wave's results to memory, straight from registers:
 // fp32 lanes hold 16 bytes already; bf16 ones hold 8, and the exchange of

@@ -1,0 +1,530 @@
+// matmul.hip -- products of fp32 or bf16 rows with bias, activation and residual
+// in the epilogue, and their gradients.
+//
+//   forward    z = x w^T + bias,  y = act(z) + residual      sums over k
+//   backward   dz = dy act'(z),   dx = dz w                  sums over n
+//                                 dw = dz^T x,  dbias = sum dz   sums over m
+//
+// All three are one product, C[r][c] = sum_s B(r, s) A(c, s), whose operands lie
+// in memory with the summed index s either contiguous (rows of s) or strided (a
+// row for every s): forward A = w and B = x contiguous; dx A = w strided; dw A = x
+// and B = dz both strided.  An operand comes into LDS as it lies in memory, and is
+// turned on the way to the registers.
+//
+// A workgroup has a tile of C and walks s in stages of 128 bytes.  The matrix unit
+// takes 16 bytes of s of a lane: 8 bf16 in one 16x16x32 product, 4 fp32 in
+// four 16x16x4 (which see s in another order, the same for both operands).  Tiles
+// of few results and a long s are split along s; the pieces' fp32 sums go to the
+// workspace and a second launch adds them, in order, and finishes.
+#include <type_traits>
+
+#include "operators.hpp"
+#include "tiles.hpp"
+
+namespace conv2d {
+
+namespace {
+
+enum { kGelu = 3 };   // CONV2D_ACT_GELU; the others as in rowvec.hpp
+
+constexpr float kRoot1_2 = 0.707106781186547524f, kRoot1_2Pi = 0.398942280401432678f;
+
+// The complement of erf keeps the digits of GELU's negative side.
+__device__ __forceinline__ float activate(float z, int act) {
+    if (act == kActRelu) return z < 0.0f ? 0.0f : z;
+    if (act == kActSilu) return z * sigmoid(z);
+    if (act == kGelu) return 0.5f * z * erfcf(-z * kRoot1_2);
+    return z;
+}
+
+__device__ __forceinline__ float activation_slope(float z, int act) {
+    if (act == kActRelu) return z > 0.0f ? 1.0f : z <= 0.0f ? 0.0f : z;   // of a NaN: NaN
+    if (act == kActSilu) {
+        const float e = sigmoid(z);
+        return e * (1.0f + z * (1.0f - e));
+    }
+    return 0.5f * erfcf(-z * kRoot1_2) + z * kRoot1_2Pi * __expf(-0.5f * z * z);
+}
+
+// One product C[r][c], r < rows, c < cols, sums over s < K.
+struct Product {
+    const void* a;          // columns' operand: [cols][K], or [K][cols] strided
+    const void* b;          // rows' operand: [rows][K], or [K][rows] strided
+    long long lda, ldb;
+    int rows, cols, K;
+    const float* bias;      // the epilogue: null where there is none
+    const void* residual;
+    void* z;
+    void* y;
+    long long ldr, ldz, ldy;
+    int act;
+};
+
+template <typename T> constexpr int kPiece = 16 / (int)sizeof(T);   // elements of 16 bytes
+
+// ------------------------------------------------------------------ fragments
+
+// A lane's 16 bytes of s of one row of a 16x16 block.
+template <typename T> struct Frag;
+template <> struct Frag<bf16_t> {
+    bf16x8 v;
+};
+template <> struct Frag<float> {
+    f32x4 v;
+};
+
+__device__ __forceinline__ void multiply(f32x4& acc, const Frag<bf16_t>& a, const Frag<bf16_t>& b) {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.v, acc, 0, 0, 0);
+}
+__device__ __forceinline__ void multiply(f32x4& acc, const Frag<float>& a, const Frag<float>& b) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[j], b.v[j], acc, 0, 0, 0);
+}
+
+// Neighbours share an operand, the turns of the order included.
+template <typename T, int TI, int TJ>
+__device__ __forceinline__ void products(f32x4 (&acc)[TI][TJ], const Frag<T> (&a)[TI], const Frag<T> (&b)[TJ]) {
+#pragma unroll
+    for (int j = 0; j < TJ; ++j)
+#pragma unroll
+        for (int n = 0; n < TI; ++n) {
+            const int i = j & 1 ? TI - 1 - n : n;
+            multiply(acc[i][j], a[i], b[j]);
+        }
+}
+
+// ---- a stage of an operand in LDS: 128 bytes of s of B indexes.
+//
+// Contiguous: a row of 128 bytes for every index, its 16-byte pieces permuted
+// (slot_of).  Strided: a row of B elements for every s, in blocks of 16 indexes;
+// the blocks of a row are permuted by a few bits of s, so that the rows that are
+// read together (bf16: 8 of them half a wave, 32 bytes of each; fp32: 4 of a
+// wave, 64 bytes of each) lie in different banks.
+template <typename T, int B> __device__ __forceinline__ int block_swizzle(int s) {
+    if constexpr (sizeof(T) == 4) return (s >> 2) & 3;
+    else if constexpr (B >= 128) return (s & 3) | ((s >> 1) & 4);   // rows 0-3 and 8-11, or 4-7 and 12-15
+    else return ((s >> 1) & 1) | ((s >> 2) & 2);                    // two rows to a line of the banks
+}
+
+// Byte of element c (a multiple of 16 bytes) of row s of a strided stage.
+template <typename T, int B> __device__ __forceinline__ int strided_byte(int s, int c) {
+    constexpr int ES = (int)sizeof(T);
+    return s * B * ES + ((c >> 4) ^ block_swizzle<T, B>(s)) * 16 * ES + (c & 15) * ES;
+}
+
+// Where a lane reads its fragments: block `block` of 16 indexes, step `step` (0
+// or 1) of 64 bytes of s.
+template <typename T, int B, bool STRIDED>
+__device__ __forceinline__ Frag<T> fragment(const char* stage, int block, int step) {
+    const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+    Frag<T> f;
+    if constexpr (!STRIDED) {
+        f.v = *reinterpret_cast<const decltype(f.v)*>(stage + block * 16 * kStageK + slot_of(i, 4 * step + g) * 16);
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int s = 16 * step + 4 * g + j;
+            f.v[j] = *reinterpret_cast<const float*>(stage + s * B * 4 + (block ^ block_swizzle<T, B>(s)) * 64 + i * 4);
+        }
+    } else {
+        // the transposing read: 16 lanes name the 8-byte parts of 4 rows of 16
+        // elements, and each gets one column
+        typedef short s16x4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
+        s16x4 h[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int s = 32 * step + 8 * g + 4 * j + (i >> 2);
+            h[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lds_s16x4)(stage + s * B * 2 + (block ^ block_swizzle<T, B>(s)) * 32 + (i & 3) * 8));
+        }
+        f.v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+    return f;
+}
+
+// ------------------------------------------------------------------ epilogue
+
+// V consecutive results of row r from column c on: from the sums (and their
+// biases) to z and y.
+template <typename T, int V>
+__device__ __forceinline__ void finish(const Product& p, long long r, int c, float (&v)[V], const float (&bias)[V]) {
+    const T* const residual = static_cast<const T*>(p.residual) + (p.residual ? r * p.ldr + c : 0);
+    const bool whole = c + V <= p.cols;
+    float rv[V] = {};
+    if (p.residual) {
+        if (whole) {
+            Vec<T, V>::unpack(Vec<T, V>::load(residual), rv);
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e) rv[e] = c + e < p.cols ? load_f32<T>(residual, e) : 0.0f;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] += bias[e];
+    if (p.z) store_piece<T>(static_cast<T*>(p.z) + r * p.ldz, c, p.cols, __builtin_bit_cast(uint4, Vec<T, V>::pack(v)));
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = activate(v[e], p.act) + rv[e];
+    store_piece<T>(static_cast<T*>(p.y) + r * p.ldy, c, p.cols, __builtin_bit_cast(uint4, Vec<T, V>::pack(v)));
+}
+
+// A wave's results, TI*16 columns x TJ*16 rows from (m0, n0): block by block of
+// 16 rows through the wave's own piece of LDS (16 x TI*16 fp32), so that whole
+// rows leave, 16 bytes of the output type a lane.  In the 16x16 result lane l
+// holds, in register r, column 4 (l >> 4) + r of row l & 15.  SUMS: the sums
+// themselves, of a part of s, to `sums`.
+template <typename T, int TI, int TJ, bool SUMS>
+__device__ __forceinline__ void write_results(const Product& p, f32x4 (&acc)[TI][TJ], char* lds, int m0, int n0, float* sums) {
+    using OUT = std::conditional_t<SUMS, float, T>;
+    constexpr int V = kPiece<OUT>, PIECES = TI * 16 / V, ROW = TI * 64, MASK = (TI * 4 < 16 ? TI * 4 : 16) - 1;
+    const int lane = threadIdx.x & 63;
+    float bias[V];
+    const int c = n0 + lane % PIECES * V;   // 64 is a multiple of PIECES: a lane's columns stay
+    static_assert(64 % PIECES == 0 || PIECES % 64 == 0, "a lane's columns stay");
+#pragma unroll
+    for (int e = 0; e < V; ++e) bias[e] = !SUMS && p.bias && c + e < p.cols ? p.bias[c + e] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+#pragma unroll
+        for (int i = 0; i < TI; ++i)
+            *reinterpret_cast<f32x4*>(lds + (lane & 15) * ROW + ((i * 4 + (lane >> 4)) ^ (lane & 15 & MASK)) * 16) = acc[i][j];
+        wave_lds_fence();
+#pragma unroll
+        for (int it = 0; it < 16 * PIECES / 64; ++it) {
+            const int e = it * 64 + lane, r = e / PIECES, q = e % PIECES * (V / 4);
+            float v[V];
+#pragma unroll
+            for (int h = 0; h < V / 4; ++h) {
+                const f32x4 u = *reinterpret_cast<const f32x4*>(lds + r * ROW + ((q + h) ^ (r & MASK)) * 16);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[4 * h + k] = u[k];
+            }
+            const int m = m0 + j * 16 + r;
+            if (m < p.rows && c < p.cols) {
+                if constexpr (SUMS) store_piece<float>(sums + (long long)m * p.cols, c, p.cols, __builtin_bit_cast(uint4, Vec<float, V>::pack(v)));
+                else finish<T, V>(p, m, c, v, bias);
+            }
+        }
+        wave_lds_fence();
+    }
+}
+
+// ------------------------------------------------------------------ any alignment
+
+// E elements from p on, of which `left` exist (the others: 0).
+template <typename T> __device__ __forceinline__ uint4 load_piece(const T* p, long long left) {
+    if (left >= kPiece<T>) return load_bytes<16>(p);
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < kPiece<T>; ++e)
+        if (e < left) {
+            if constexpr (sizeof(T) == 4) w[e] = __builtin_bit_cast(uint32_t, p[e]);
+            else w[e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
+        }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A thread's pieces of an operand's stage: in registers, then in LDS.
+template <typename T, int B, int NT, bool STRIDED> struct Staged {
+    static constexpr int N = B * 8 / NT, E = kPiece<T>, S = kStageK / (int)sizeof(T);
+    static_assert(N * NT == B * 8, "pieces split evenly");
+    uint4 v[N];
+    // indexes i0 .. of `count`, s from s0 to `send`
+    __device__ __forceinline__ void load(const T* p, long long ld, int i0, int count, int s0, int send) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int e = n * NT + threadIdx.x;
+            const int i = i0 + (STRIDED ? e % (B / E) * E : e / 8), s = s0 + (STRIDED ? e / (B / E) : e % 8 * E);
+            const long long left = i < count && s < send ? (STRIDED ? count - i : send - s) : 0;
+            v[n] = left > 0 ? load_piece<T>(p + (STRIDED ? s * ld + i : i * ld + s), left) : make_uint4(0, 0, 0, 0);
+        }
+    }
+    __device__ __forceinline__ void store(char* stage) const {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int e = n * NT + threadIdx.x;
+            const int at = STRIDED ? strided_byte<T, B>(e / (B / E), e % (B / E) * E) : slot_of(e / 8, e % 8) * 16;
+            *reinterpret_cast<uint4*>(stage + at) = v[n];
+        }
+    }
+};
+
+// Operands of any alignment pass through registers: the loads of a stage are in
+// flight during the products of the one before.
+template <typename T, int BM, int BN, int WM, int WN, bool TA, bool TB, bool SUMS>
+__global__ __launch_bounds__(WM * WN * 64) void matmul_staged_kernel(Product p, int tm, int tn, int stages, float* sums) {
+    constexpr int NT = WM * WN * 64, TI = BN / WN / 16, TJ = BM / WM / 16, S = kStageK / (int)sizeof(T);
+    constexpr int STAGE = (BM + BN) * kStageK, OUTB = WM * WN * 16 * TI * 64;
+    __shared__ uint4 lds[(STAGE > OUTB ? STAGE : OUTB) / 16];
+    char* const sa = reinterpret_cast<char*>(lds);
+    char* const sb = sa + BN * kStageK;
+    const int wave = threadIdx.x >> 6, wm = wave / WN, wn = wave % WN;
+    const TileAt t = tile_at(tm, tn, BM, BN);
+    const int s0 = t.split * stages * S, send = min(p.K, s0 + stages * S);
+    f32x4 acc[TI][TJ];
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    Staged<T, BN, NT, TA> a;
+    Staged<T, BM, NT, TB> b;
+    const T* const pa = static_cast<const T*>(p.a);
+    const T* const pb = static_cast<const T*>(p.b);
+    a.load(pa, p.lda, t.n0, p.cols, s0, send);
+    b.load(pb, p.ldb, t.m0, p.rows, s0, send);
+    for (int s = s0; s < send; s += S) {
+        __syncthreads();
+        a.store(sa);
+        b.store(sb);
+        __syncthreads();
+        if (s + S < send) {
+            a.load(pa, p.lda, t.n0, p.cols, s + S, send);
+            b.load(pb, p.ldb, t.m0, p.rows, s + S, send);
+        }
+#pragma unroll
+        for (int step = 0; step < 2; ++step) {
+            Frag<T> fa[TI], fb[TJ];
+#pragma unroll
+            for (int i = 0; i < TI; ++i) fa[i] = fragment<T, BN, TA>(sa, wn * TI + i, step);
+#pragma unroll
+            for (int j = 0; j < TJ; ++j) fb[j] = fragment<T, BM, TB>(sb, wm * TJ + j, step);
+            products<T, TI, TJ>(acc, fa, fb);
+        }
+    }
+    __syncthreads();
+    write_results<T, TI, TJ, SUMS>(p, acc, sa + wave * (16 * TI * 64), t.m0 + wm * TJ * 16, t.n0 + wn * TI * 16,
+                                   sums + (long long)t.split * p.rows * p.cols);
+}
+
+// Adds the parts of a product that was split along s, in order, and finishes.
+template <typename T>
+__global__ __launch_bounds__(256) void matmul_join_kernel(Product p, const float* sums, int splits) {
+    constexpr int V = kPiece<T>;
+    const int pieces = (p.cols + V - 1) / V;
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x, total = (long long)p.rows * p.cols;
+    if (i >= (long long)p.rows * pieces) return;
+    const long long r = i / pieces;
+    const int c = (int)(i - r * pieces) * V;
+    float v[V] = {}, bias[V];
+    const float* at = sums + r * p.cols + c;
+    if (c + V <= p.cols) {
+        for (int k = 0; k < splits; ++k, at += total) {
+#pragma unroll
+            for (int h = 0; h < V; h += 4) {
+                float u[4];
+                Vec<float, 4>::unpack(Vec<float, 4>::load(at + h), u);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[h + e] += u[e];
+            }
+        }
+    } else {
+        for (int k = 0; k < splits; ++k, at += total)
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (c + e < p.cols) v[e] += at[e];
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) bias[e] = p.bias && c + e < p.cols ? p.bias[c + e] : 0.0f;
+    finish<T, V>(p, r, c, v, bias);
+}
+
+// ------------------------------------------------------------------ dz
+
+// dz = dy act'(z) (rounded to T; null: not wanted), rows padded with zeros to ldd
+// elements, and the sums of its columns over a workgroup's rows before the
+// rounding, [row chunk][N] (null: not wanted).  256 threads: `lanes` vectors of a
+// row, 256 / lanes rows at a time.
+template <typename T, bool ACT>
+__global__ __launch_bounds__(256) void matmul_dz_kernel(MatmulBwdArgs a, T* dz, int ldd, float* sums, int lanes, int chunk) {
+    constexpr int V = kPiece<T>;
+    __shared__ float part[256][V + 1];
+    const int l = threadIdx.x % lanes, group = threadIdx.x / lanes, groups = 256 / lanes;
+    const int c = (blockIdx.x * lanes + l) * V;
+    const long long m0 = (long long)blockIdx.y * chunk, m1 = m0 + chunk < a.M ? m0 + chunk : a.M;
+    float s[V] = {};
+    if (c < a.N) {
+        for (long long m = m0 + group; m < m1; m += groups) {
+            const T* const py = static_cast<const T*>(a.dy) + m * a.lddy + c;
+            const T* const pz = static_cast<const T*>(a.z) + (ACT ? m * a.ldz + c : 0);
+            float v[V], z[V];
+            Vec<T, V>::unpack(__builtin_bit_cast(typename Vec<T, V>::raw, load_piece<T>(py, a.N - c)), v);
+            if constexpr (ACT) {
+                Vec<T, V>::unpack(__builtin_bit_cast(typename Vec<T, V>::raw, load_piece<T>(pz, a.N - c)), z);
+#pragma unroll
+                for (int e = 0; e < V; ++e) v[e] = c + e < a.N ? v[e] * activation_slope(z[e], a.act) : 0.0f;
+            }
+#pragma unroll
+            for (int e = 0; e < V; ++e) s[e] += v[e];
+            if (dz) Vec<T, V>::store(dz + m * ldd + c, v);
+        }
+    }
+    if (!sums) return;
+#pragma unroll
+    for (int e = 0; e < V; ++e) part[threadIdx.x][e] = s[e];
+    __syncthreads();
+    for (int i = threadIdx.x; i < lanes * V; i += 256) {
+        const int n = blockIdx.x * lanes * V + i;
+        float t = 0.0f;
+        for (int g = 0; g < groups; ++g) t += part[g * lanes + i / V][i % V];
+        if (n < a.N) sums[(long long)blockIdx.y * a.N + n] = t;
+    }
+}
+
+// ------------------------------------------------------------------ host
+
+constexpr int kUnits = 256;
+
+struct Plan {
+    int b, tm, tn, splits, stages;   // square tiles of b
+};
+
+// The larger tile where it gives every compute unit one and the columns fill it;
+// few tiles of a long s are split along it until they do.
+Plan make_plan(int rows, int cols, int K, int es) {
+    auto tiles = [&](int b) { return (long long)((rows + b - 1) / b) * ((cols + b - 1) / b); };
+    Plan p;
+    p.b = cols > 64 && rows > 64 && tiles(128) >= kUnits ? 128 : 64;
+    p.tm = (rows + p.b - 1) / p.b;
+    p.tn = (cols + p.b - 1) / p.b;
+    const int all = (int)(((long long)K * es + kStageK - 1) / kStageK);
+    const long long t = (long long)p.tm * p.tn;
+    // a part is at least 4 stages long
+    const long long want = t >= kUnits ? 1 : kUnits / t, most = all / 4;
+    p.splits = (int)(want < most ? want : most);
+    if (p.splits < 1) p.splits = 1;
+    p.stages = (all + p.splits - 1) / p.splits;
+    p.splits = (all + p.stages - 1) / p.stages;
+    return p;
+}
+
+size_t split_bytes(const Plan& p, int rows, int cols) {
+    return p.splits > 1 ? (size_t)p.splits * rows * cols * 4 : 0;
+}
+
+template <typename T, bool TA, bool TB, bool SUMS>
+hipError_t tiled(const Product& p, const Plan& q, float* sums, hipStream_t st) {
+    const unsigned blocks = (unsigned)(q.tm * q.tn * q.splits);
+    if (q.b == 128)
+        matmul_staged_kernel<T, 128, 128, 2, 2, TA, TB, SUMS><<<blocks, 256, 0, st>>>(p, q.tm, q.tn, q.stages, sums);
+    else
+        matmul_staged_kernel<T, 64, 64, 2, 2, TA, TB, SUMS><<<blocks, 256, 0, st>>>(p, q.tm, q.tn, q.stages, sums);
+    return hipGetLastError();
+}
+
+template <typename T, bool TA, bool TB> hipError_t product(const Product& p, void* ws, hipStream_t st) {
+    const Plan q = make_plan(p.rows, p.cols, p.K, (int)sizeof(T));
+    float* const sums = static_cast<float*>(ws);
+    if (q.splits == 1) return tiled<T, TA, TB, false>(p, q, nullptr, st);
+    const hipError_t e = tiled<T, TA, TB, true>(p, q, sums, st);
+    if (e != hipSuccess) return e;
+    const long long pieces = (long long)p.rows * ((p.cols + kPiece<T> - 1) / kPiece<T>);
+    matmul_join_kernel<T><<<(unsigned)((pieces + 255) / 256), 256, 0, st>>>(p, sums, q.splits);
+    return hipGetLastError();
+}
+
+// ---- the backward pass's workspace: dz, the parts of dbias, the parts of dx or dw
+
+// Rows of dz are whole 16-byte pieces.
+template <typename T> int dz_stride(int N) { return (N + kPiece<T> - 1) / kPiece<T> * kPiece<T>; }
+
+struct DzShape {
+    int lanes, chunk, cols, chunks;
+};
+
+DzShape dz_shape(int M, int N, int es) {
+    DzShape d;
+    const int vecs = (N + 16 / es - 1) / (16 / es);
+    d.lanes = 1;
+    while (d.lanes < 64 && d.lanes < vecs) d.lanes <<= 1;
+    d.cols = (vecs + d.lanes - 1) / d.lanes;
+    // 8 workgroups a compute unit, and up to 512 rows a thread, which sums them in fp32
+    const int groups = 256 / d.lanes;
+    long long chunks = (8 * kUnits + d.cols - 1) / d.cols, least = ((long long)M + groups * 512 - 1) / (groups * 512);
+    const long long most = ((long long)M + groups * 4 - 1) / (groups * 4);
+    if (chunks > most) chunks = most;
+    if (chunks < least) chunks = least;
+    if (chunks > 65535) chunks = 65535;
+    d.chunk = (int)(((long long)M + chunks - 1) / chunks);
+    d.chunks = (int)(((long long)M + d.chunk - 1) / d.chunk);
+    return d;
+}
+
+size_t round256(size_t v) { return (v + 255) / 256 * 256; }
+
+struct BwdSpace {
+    size_t dz, sums, parts;   // offsets; the end
+    size_t end;
+};
+
+template <typename T> BwdSpace bwd_space(int M, int K, int N) {
+    const DzShape d = dz_shape(M, N, (int)sizeof(T));
+    BwdSpace b;
+    b.dz = 0;
+    b.sums = round256((size_t)M * dz_stride<T>(N) * sizeof(T));
+    b.parts = b.sums + round256((size_t)d.chunks * N * 4);
+    const size_t u = split_bytes(make_plan(M, K, N, (int)sizeof(T)), M, K), v = split_bytes(make_plan(N, K, M, (int)sizeof(T)), N, K);
+    b.end = b.parts + (u > v ? u : v);
+    return b;
+}
+
+template <typename T> hipError_t gradients(const MatmulBwdArgs& a, char* ws, hipStream_t st) {
+    const BwdSpace b = bwd_space<T>(a.M, a.K, a.N);
+    const DzShape d = dz_shape(a.M, a.N, (int)sizeof(T));
+    const int ldd = dz_stride<T>(a.N);
+    const bool products = a.dx || a.dw;
+    T* const dz = a.z && products ? reinterpret_cast<T*>(ws + b.dz) : nullptr;
+    float* const sums = a.dbias ? reinterpret_cast<float*>(ws + b.sums) : nullptr;
+    hipError_t e = hipSuccess;
+    if (dz || sums) {
+        const dim3 grid(d.cols, d.chunks);
+        if (a.z) matmul_dz_kernel<T, true><<<grid, 256, 0, st>>>(a, dz, ldd, sums, d.lanes, d.chunk);
+        else matmul_dz_kernel<T, false><<<grid, 256, 0, st>>>(a, dz, ldd, sums, d.lanes, d.chunk);
+        e = hipGetLastError();
+        if (e == hipSuccess && sums) e = launch_join_columns(sums, a.dbias, d.chunks, a.N, st);
+        if (e != hipSuccess) return e;
+    }
+    Product p = {};
+    p.b = dz ? dz : a.dy;
+    p.ldb = dz ? ldd : a.lddy;
+    if (a.dx) {
+        p.a = a.w; p.lda = a.ldw; p.rows = a.M; p.cols = a.K; p.K = a.N; p.y = a.dx; p.ldy = a.lddx;
+        e = product<T, true, false>(p, ws + b.parts, st);
+        if (e != hipSuccess) return e;
+    }
+    if (a.dw) {
+        p.a = a.x; p.lda = a.ldx; p.rows = a.N; p.cols = a.K; p.K = a.M; p.y = a.dw; p.ldy = a.lddw;
+        e = product<T, true, true>(p, ws + b.parts, st);
+    }
+    return e;
+}
+
+}  // namespace
+
+// A launch counts its threads in 32 bits: 2^24 tiles of 64 x 64 at 256 threads.
+bool matmul_supports(int M, int K, int N) {
+    auto tiles = [](int v) { return ((long long)v + 63) / 64; };
+    constexpr long long most = 1 << 24;
+    return tiles(M) * tiles(N) < most && tiles(M) * tiles(K) < most && tiles(N) * tiles(K) < most;
+}
+
+size_t matmul_workspace(int M, int K, int N, int dtype) {
+    return split_bytes(make_plan(M, N, K, dtype == 0 ? 4 : 2), M, N);
+}
+
+size_t matmul_bwd_workspace(int M, int K, int N, int dtype) {
+    return dtype == 0 ? bwd_space<float>(M, K, N).end : bwd_space<bf16_t>(M, K, N).end;
+}
+
+hipError_t launch_matmul(const MatmulArgs& a, void* ws, hipStream_t st) {
+    Product p = {};
+    p.a = a.w; p.b = a.x; p.lda = a.ldw; p.ldb = a.ldx; p.rows = a.M; p.cols = a.N; p.K = a.K;
+    p.bias = a.bias; p.residual = a.residual; p.z = a.z; p.y = a.y; p.ldr = a.ldr; p.ldz = a.ldz; p.ldy = a.ldy; p.act = a.act;
+    return a.dtype == 0 /* CONV2D_F32 */ ? product<float, false, false>(p, ws, st) : product<bf16_t, false, false>(p, ws, st);
+}
+
+hipError_t launch_matmul_bwd(const MatmulBwdArgs& a, void* ws, hipStream_t st) {
+    return a.dtype == 0 /* CONV2D_F32 */ ? gradients<float>(a, static_cast<char*>(ws), st)
+                                         : gradients<bf16_t>(a, static_cast<char*>(ws), st);
+}
+
+}  // namespace conv2d

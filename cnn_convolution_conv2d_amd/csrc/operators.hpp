@@ -1,5 +1,5 @@
 // operators.hpp -- what the C entries and the kernels of the operators beside the
-// convolutions share (group norm, rows in 8 bits, int8 products).  Apart from
+// convolutions share (norms, rows in 8 bits, products, dropout).  Apart from
 // common.hpp, which every convolution kernel's measured traffic is tied to.
 #pragma once
 
@@ -41,6 +41,64 @@ struct Int8Args {
     bool relu;
 };
 
+// One RMS-norm call on rows, validated on the host: M rows of C, ld*: elements
+// from one row to the next.
+struct RmsArgs {
+    const void* x;         // backward: dy
+    const void* residual;  // null: none; backward: dh
+    const float* gamma;    // null: 1
+    void* h;               // x + residual, null: not wanted; backward: read
+    void* y;               // the norm, its 8-bit form or dx
+    float* q_scale;        // with the 8-bit form
+    float* rstd;           // [M]; forward: written unless null, backward: read
+    float* dgamma;         // backward only; null: not wanted
+    int M, C;
+    long long ldx, ldr, ldh, ldy;
+    float eps;
+    int dtype;
+};
+
+// One product with its epilogue, validated on the host:
+// y [M][N] = act(z) + residual, z = x [M][K] w [N][K]^T + bias.
+struct MatmulArgs {
+    const void* x;
+    const void* w;
+    const float* bias;     // null: none
+    const void* residual;  // null: none
+    void* z;               // null: not wanted
+    void* y;
+    int M, K, N;
+    long long ldx, ldw, ldr, ldz, ldy;
+    int dtype, act;
+};
+
+// Its gradients: dz = dy act'(z), dx = dz w, dw = dz^T x, dbias = sum_m dz.
+struct MatmulBwdArgs {
+    const void* dy;
+    const void* z;         // null: the activation is none
+    const void* x;
+    const void* w;
+    void* dx;              // each of the three: null: not wanted
+    void* dw;
+    float* dbias;
+    int M, K, N;
+    long long lddy, ldz, ldx, ldw, lddx, lddw;
+    int dtype, act;
+};
+
+// One dropout call, validated on the host.
+struct DropoutArgs {
+    const void* x;
+    const void* residual;             // null: none
+    void* y;
+    const unsigned long long* rng;    // seed, offset
+    uint32_t threshold;               // words below it drop their element
+    float scale;
+    int M, C;
+    long long ldx, ldr, ldy;
+    int dtype;
+};
+
 // Looks at another workgroup's result before a workgroup computes it itself, set
 // by conv2d_set_wait_limit.
 int wait_limit();
@@ -58,5 +116,26 @@ bool int8_matmul_supports(int M, int K, int N, long long ldq, long long ldw);
 hipError_t launch_int8_matmul(const Int8Args& a, int out_f32, void* ws, hipStream_t st);
 hipError_t launch_quantize_rows(const void* x, void* q, float* scale, int M, int K, long long ldx, long long ldq,
                                 int dtype, hipStream_t st);
+
+// RMS norm; C up to kRmsMostC.
+constexpr int kRmsMostC = 16384;
+size_t rms_norm_bwd_workspace(int M, int C);
+hipError_t launch_rms_norm(const RmsArgs& a, hipStream_t st);
+hipError_t launch_rms_norm_quant(const RmsArgs& a, hipStream_t st);
+hipError_t launch_rms_norm_bwd(const RmsArgs& a, void* ws, hipStream_t st);
+
+// out[c] = sum of sums[i][c] over i < count, in fp64, in a fixed order.
+hipError_t launch_join_columns(const float* sums, float* out, int count, int C, hipStream_t st);
+
+// Products with an epilogue and their gradients; strides of what they read up to kMatmulMostLd.
+constexpr int kMatmulMostLd = 1 << 20;
+bool matmul_supports(int M, int K, int N);
+size_t matmul_workspace(int M, int K, int N, int dtype);
+size_t matmul_bwd_workspace(int M, int K, int N, int dtype);
+hipError_t launch_matmul(const MatmulArgs& a, void* ws, hipStream_t st);
+hipError_t launch_matmul_bwd(const MatmulBwdArgs& a, void* ws, hipStream_t st);
+
+// Dropout.
+hipError_t launch_dropout(const DropoutArgs& a, hipStream_t st);
 
 }  // namespace conv2d

@@ -1,0 +1,76 @@
+// tiles.hpp -- device helpers shared by the tiled products (8-bit integers, bf16
+// and fp32): the stages' layout in LDS, copies into it, the order of the tiles
+// and the stores of their results.
+#pragma once
+
+#include "mfma.hpp"
+#include "rowvec.hpp"
+
+namespace conv2d {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_unaligned __attribute__((aligned(2)));
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+
+constexpr int kStageK = 128;  // bytes of k per stage: one line of every row
+
+// 16-byte slot of a stage's (row, 16-byte piece): the pieces of a row are
+// permuted so that 16 consecutive rows read at one piece hit all banks.
+__device__ __forceinline__ int slot_of(int row, int piece) { return row * 8 + (piece ^ ((row >> 1) & 7)); }
+
+struct TileAt {
+    int m0, n0, split;
+};
+
+// Block -> tile: every XCD walks a contiguous run (its L2 keeps the shared
+// rows), and within it tiles go down groups of 8 row tiles, channel tile by
+// channel tile.
+__device__ __forceinline__ TileAt tile_at(int tm, int tn, int BM, int BN) {
+    const int per = tm * tn;
+    int i = xcd_tile_index();
+    TileAt t;
+    t.split = i / per;
+    i %= per;
+    constexpr int GM = 8;
+    const int group = i / (GM * tn), first = group * GM, rows = min(GM, tm - first);
+    i -= group * GM * tn;
+    t.m0 = (first + i % rows) * BM;
+    t.n0 = (i / rows) * BN;
+    return t;
+}
+
+// The wave's accesses to its own piece of LDS before this are done before
+// those after it.
+__device__ __forceinline__ void wave_lds_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// 16 bytes of results (8 bf16, 4 fp32 or int) to channels n .. of a row, fewer
+// at the row's end.  The address is aligned to an element only (a row may have
+// any length): one store all the same.
+template <typename OUT> __device__ __forceinline__ void store_piece(OUT* row, int n, int N, const uint4& v) {
+    constexpr int E = 16 / (int)sizeof(OUT);
+    if (n + E <= N) {
+        *reinterpret_cast<u32x4_unaligned*>(row + n) = __builtin_bit_cast(u32x4, v);
+    } else {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (n + e < N)
+                row[n + e] = sizeof(OUT) == 4 ? __builtin_bit_cast(OUT, (typename RawBytes<sizeof(OUT)>::type)w[e * (int)sizeof(OUT) / 4])
+                                              : __builtin_bit_cast(OUT, (typename RawBytes<sizeof(OUT)>::type)(w[e / 2] >> (16 * (e & 1))));
+    }
+}
+
+// A wave's copy of 1 KB into LDS, 16 bytes a lane: no registers, no LDS
+// instruction; an offset outside the matrix writes zeros.
+__device__ __forceinline__ void copy_kb(__amdgpu_buffer_rsrc_t r, char* dst, int off) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)dst, 16, off, 0, 0, 0);
+}
+
+constexpr int vmcnt_of(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0f70; }  // lgkmcnt, expcnt: no wait
+
+}  // namespace conv2d

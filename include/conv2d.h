@@ -340,7 +340,8 @@ int conv2d_transpose_select_path(int N, int Cin, int H, int W, int Cout, int Kh,
  * contents need no clearing.  Too small a workspace returns CONV2D_ERR_ARG.
  * The calls allocate nothing and may be captured into a graph.
  */
-enum { CONV2D_ACT_NONE = 0, CONV2D_ACT_RELU = 1, CONV2D_ACT_SILU = 2 };
+/* group norm takes the first three */
+enum { CONV2D_ACT_NONE = 0, CONV2D_ACT_RELU = 1, CONV2D_ACT_SILU = 2, CONV2D_ACT_GELU = 3 };
 
 /* 0 on bad arguments */
 size_t conv2d_group_norm_workspace_bytes(int N, int C, int H, int W, int G, int backward);
@@ -391,6 +392,108 @@ int conv2d_int8_matmul(const void* q, const float* q_scale, const void* w, const
                        const float* bias, void* y, void* workspace, size_t workspace_bytes,
                        int M, int K, int N, int ldq, int ldw, int ldy,
                        int dtype, int epilogue, hipStream_t stream);
+
+/*
+ * Root-mean-square norm of M rows (tokens, or channels-last pixels) of C
+ * elements, with the addition of a residual before it:
+ *   h = x + residual,   rstd = 1 / sqrt(sum_c h^2 / C + eps),   y = h * rstd * gamma[c]
+ * x, residual, h, y, dy, dh, dx are fp32 or bf16 (dtype), ld*: elements from one
+ * row to the next (>= C).  Everything in between is fp32 (the squares' sum fp64
+ * where it would overflow or vanish), each output is rounded once: y and rstd are
+ * those of the sum before h's rounding.
+ *
+ * conv2d_rms_norm -- h, y and rstd (fp32 [M]).  residual may be NULL (0), h and
+ *   rstd may be NULL when they are not wanted.  h and y may each lie over x or the
+ *   residual (same pointer and stride), not over each other.
+ * conv2d_rms_norm_quant -- y in 8 bits instead, ready to be the rows of
+ *   conv2d_int8_matmul: q int8 [M][C] (ldq apart) and q_scale fp32 [M], as
+ *   conv2d_quantize_rows makes them of the unrounded y.  q must not overlap x,
+ *   the residual or h.
+ * conv2d_rms_norm_bwd -- the gradients, from dy, h and rstd of the forward pass
+ *   (h: x itself where there was no residual) and dh, the gradient that reaches h
+ *   from elsewhere (NULL: none):
+ *     dx = rstd * (t - xh * sum_c(t xh) / C) + dh,   t = gamma dy,  xh = h rstd
+ *     dgamma[c] = sum_m dy * xh
+ *   dx is the gradient of x and of the residual alike; dgamma fp32 [C] is written
+ *   (not added to), or NULL.  dx may lie over dy, dh or h (same stride).
+ *
+ * gamma: fp32 [C]; NULL means 1.  eps >= 0 and finite.  C <= 16384, any M, stride
+ * and alignment; C, the strides and the pointers as multiples of 16 bytes are
+ * fastest.  Sums have a fixed order: equal calls give equal bits.  A NaN or
+ * infinity stays in its row (and its columns of dgamma).
+ *
+ * workspace: as for the group norm, conv2d_rms_norm_bwd_workspace_bytes(M, C)
+ * bytes; not needed (NULL) when dgamma is NULL.  The calls allocate nothing and
+ * may be captured into a graph.
+ */
+int conv2d_rms_norm(const void* x, const void* residual, const float* gamma, void* h, void* y, float* rstd,
+                    int M, int C, int ldx, int ldr, int ldh, int ldy, float eps, int dtype, hipStream_t stream);
+int conv2d_rms_norm_quant(const void* x, const void* residual, const float* gamma, void* h, void* q, float* q_scale,
+                          float* rstd, int M, int C, int ldx, int ldr, int ldh, int ldq, float eps, int dtype,
+                          hipStream_t stream);
+size_t conv2d_rms_norm_bwd_workspace_bytes(int M, int C);   /* 0 on bad arguments */
+int conv2d_rms_norm_bwd(const void* dy, const void* dh, const void* h, const float* gamma, const float* rstd,
+                        void* dx, float* dgamma, void* workspace, size_t workspace_bytes,
+                        int M, int C, int lddy, int lddh, int ldh, int lddx, int dtype, hipStream_t stream);
+
+/*
+ * Matrix products of rows with bias, activation and residual in the epilogue (a
+ * 1x1 convolution over channels-last pixels, or a linear layer over tokens):
+ *   z[m][n] = sum_k x[m][k] * w[n][k] [+ bias[n]],   y = act(z) [+ residual[m][n]]
+ * with act none, ReLU, SiLU or GELU (z/2 * (1 + erf(z / sqrt 2))).  x [M][K], w
+ * [N][K], residual, z and y [M][N] are fp32 or bf16 (dtype), ld* elements from
+ * one row to the next; bias is fp32 [N].  Products are exact, sums and everything
+ * after them fp32 (fp32 operands: fp32 fused multiply-adds), each output is rounded
+ * once, y from the unrounded z.
+ *
+ * conv2d_matmul -- y, and z where it is not NULL (what the gradients need when
+ *   there is an activation).  bias and residual may be NULL.  y may lie over the
+ *   residual (same pointer and stride), z and y must not overlap x, w or each
+ *   other.
+ * conv2d_matmul_bwd -- the gradients from dy, z (ignored without an activation), x
+ *   and w:
+ *     dz = dy * act'(z),  dx = dz w,  dw = dz^T x,  dbias[n] = sum_m dz
+ *   ReLU's derivative at 0 is 0.  dx [M][K], dw [N][K] of dtype, dbias fp32 [N]: written
+ *   (not added to), each may be NULL when it is not wanted.  bf16: dz is rounded to bf16 before the two products, as
+ *   the matrix unit takes it; dbias is the sum of the unrounded dz.  (The
+ *   residual's gradient is dy.)  The outputs must not overlap the inputs.
+ *
+ * K >= 1, M, N >= 1; strides of dy, z, x and w up to 2^20 elements, and of M, K and N no product of two
+ * 64-wide tile counts above 2^24 (CONV2D_ERR_UNSUPPORTED).  Any stride and
+ * alignment works; 16-byte aligned pointers with strides (and, of what is summed
+ * along a row, lengths) that are multiples of 16 bytes are fastest.  Sums have a
+ * fixed order: equal calls give equal bits.
+ *
+ * workspace: as for the group norm, conv2d_matmul_workspace_bytes and
+ * conv2d_matmul_bwd_workspace_bytes (0: none is needed, NULL will do).  The calls
+ * allocate nothing and may be captured into a graph.
+ */
+size_t conv2d_matmul_workspace_bytes(int M, int K, int N, int dtype);
+int conv2d_matmul(const void* x, const void* w, const float* bias, const void* residual, void* z, void* y,
+                  void* workspace, size_t workspace_bytes, int M, int K, int N, int ldx, int ldw, int ldr, int ldz,
+                  int ldy, int dtype, int act, hipStream_t stream);
+size_t conv2d_matmul_bwd_workspace_bytes(int M, int K, int N, int dtype);
+int conv2d_matmul_bwd(const void* dy, const void* z, const void* x, const void* w, void* dx, void* dw, float* dbias,
+                      void* workspace, size_t workspace_bytes, int M, int K, int N, int lddy, int ldz, int ldx, int ldw,
+                      int lddx, int lddw, int dtype, int act, hipStream_t stream);
+
+/*
+ * Dropout of rows with the addition of a residual:
+ *   y[m][c] = residual[m][c] + (word(m, c) >= floor(p * 2^32) ? x[m][c] / (1 - p) : 0)
+ * The mask is computed from a counter and never stored: word(m, c) is word c % 4
+ * of Philox4x32-10 of the counter (c / 4, m, offset low, offset high) under the
+ * key (seed low, seed high), so it does not depend on M, C or a stride.  The
+ * gradient of x is the same call on dy with no residual; the residual's is dy.
+ *
+ * rng: two 64-bit words in device memory, seed and offset, read when the call
+ * runs (so that a captured call takes a new mask when the program writes them
+ * between replays); every value of them gives a mask of its own.  0 <= p < 1.
+ * x, residual (NULL: 0) and y are fp32 or bf16, ld* elements from one row to the
+ * next; y may lie over x or the residual (same pointer and stride).  A dropped
+ * NaN or infinity is gone.  Nothing is allocated; the call may be captured.
+ */
+int conv2d_dropout(const void* x, const void* residual, void* y, const unsigned long long* rng, float p,
+                   int M, int C, int ldx, int ldr, int ldy, int dtype, hipStream_t stream);
 
 /*
  * Packed weight layout (the reduction order the NHWC kernels walk: tap
