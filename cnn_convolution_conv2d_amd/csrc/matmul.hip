@@ -112,32 +112,30 @@ template <typename T, int B> __device__ __forceinline__ int strided_byte(int s, 
     return s * B * ES + ((c >> 4) ^ block_swizzle<T, B>(s)) * 16 * ES + (c & 15) * ES;
 }
 
-// Where a lane reads its fragments: block `block` of 16 indexes, step `step` (0
-// or 1) of 64 bytes of s.
+// A lane's fragment of block `block` of 16 indexes, step `step` (0 or 1) of 64 bytes
+// of s, of the operand `base` bytes into a stage.  The whole offset is one sum: the
+// compiler follows a short chain of additions from a buffer to an access, and takes a
+// read at the end of a longer one to need every copy in flight.
 template <typename T, int B, bool STRIDED>
-__device__ __forceinline__ Frag<T> fragment(const char* stage, int block, int step) {
+__device__ __forceinline__ Frag<T> fragment(const char* stage, int base, int block, int step) {
     const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
     Frag<T> f;
     if constexpr (!STRIDED) {
-        f.v = *reinterpret_cast<const decltype(f.v)*>(stage + block * 16 * kStageK + slot_of(i, 4 * step + g) * 16);
+        f.v = *reinterpret_cast<const decltype(f.v)*>(stage + (base + block * 16 * kStageK + slot_of(i, 4 * step + g) * 16));
     } else if constexpr (sizeof(T) == 4) {
+        const int at = base + 4 * g * B * 4 + (block ^ block_swizzle<T, B>(4 * g)) * 64 + i * 4;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int s = 16 * step + 4 * g + j;
-            f.v[j] = *reinterpret_cast<const float*>(stage + s * B * 4 + (block ^ block_swizzle<T, B>(s)) * 64 + i * 4);
-        }
+        for (int j = 0; j < 4; ++j) f.v[j] = *reinterpret_cast<const float*>(stage + (at + (16 * step + j) * B * 4));
     } else {
         // the transposing read: 16 lanes name the 8-byte parts of 4 rows of 16
         // elements, and each gets one column
         typedef short s16x4 __attribute__((ext_vector_type(4)));
         typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
+        const int s = 8 * g + (i >> 2), at = base + s * B * 2 + (block ^ block_swizzle<T, B>(s)) * 32 + (i & 3) * 8;
         s16x4 h[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int s = 32 * step + 8 * g + 4 * j + (i >> 2);
-            h[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lds_s16x4)(stage + s * B * 2 + (block ^ block_swizzle<T, B>(s)) * 32 + (i & 3) * 8));
-        }
+        for (int j = 0; j < 2; ++j)
+            h[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(stage + (at + (32 * step + 4 * j) * B * 2)));
         f.v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
     }
     return f;
@@ -209,7 +207,7 @@ __device__ __forceinline__ void write_results(const Product& p, f32x4 (&acc)[TI]
     }
 }
 
-// ------------------------------------------------------------------ any alignment
+// ------------------------------------------------------------------ operands of any alignment
 
 // E elements from p on, of which `left` exist (the others: 0).
 template <typename T> __device__ __forceinline__ uint4 load_piece(const T* p, long long left) {
@@ -285,15 +283,160 @@ __global__ __launch_bounds__(WM * WN * 64) void matmul_staged_kernel(Product p, 
         for (int step = 0; step < 2; ++step) {
             Frag<T> fa[TI], fb[TJ];
 #pragma unroll
-            for (int i = 0; i < TI; ++i) fa[i] = fragment<T, BN, TA>(sa, wn * TI + i, step);
+            for (int i = 0; i < TI; ++i) fa[i] = fragment<T, BN, TA>(sa, 0, wn * TI + i, step);
 #pragma unroll
-            for (int j = 0; j < TJ; ++j) fb[j] = fragment<T, BM, TB>(sb, wm * TJ + j, step);
+            for (int j = 0; j < TJ; ++j) fb[j] = fragment<T, BM, TB>(sa, BN * kStageK, wm * TJ + j, step);
             products<T, TI, TJ>(acc, fa, fb);
         }
     }
     __syncthreads();
     write_results<T, TI, TJ, SUMS>(p, acc, sa + wave * (16 * TI * 64), t.m0 + wm * TJ * 16, t.n0 + wn * TI * 16,
                                    sums + (long long)t.split * p.rows * p.cols);
+}
+
+// ------------------------------------------------------------------ aligned operands
+
+// A wave's copies of an operand's stage into LDS, 1 KB each, straight from
+// memory: a lane's slot in LDS is fixed (16 bytes times its number), so it fetches
+// what belongs there.
+template <typename T, int B, int NW, bool STRIDED> struct Copies {
+    static constexpr int N = B / 8 / NW, ES = (int)sizeof(T), S = kStageK / ES;
+    static_assert(N * NW * 8 == B, "copies split evenly");
+    const char* base;
+    long long step;          // bytes of a stage
+    int off[N];              // of this lane's pieces, within the stage
+    uint32_t row, tail;      // strided: bytes of a row, and of the tile's part of one
+    __amdgpu_buffer_rsrc_t r;
+    int piece;               // contiguous: this lane's first s
+    // indexes i0 .. of `count`, from s0 on
+    __device__ __forceinline__ void init(const void* p, long long ld, int i0, int count, int K, int s0, int wave, int lane) {
+        const int n = min(count - i0, B);
+        if constexpr (STRIDED) {
+            base = static_cast<const char*>(p) + ((long long)s0 * ld + i0) * ES;
+            step = (long long)S * ld * ES;
+            row = (uint32_t)(ld * ES);
+            tail = ((uint32_t)n * ES + 15) & ~15u;   // whole pieces: an aligned one that holds an element is read whole
+#pragma unroll
+            for (int c = 0; c < N; ++c) {
+                const int at = (c * NW + wave) * 1024 + lane * 16, s = at / (B * ES), in = at % (B * ES);
+                const int block = (in / (16 * ES)) ^ block_swizzle<T, B>(s);
+                off[c] = s * (int)row + block * (16 * ES) + in % (16 * ES);
+            }
+        } else {
+            // row (c * NW + wave) * 8 + lane / 8: its bits 1 to 3 are those of wave * 8 + lane / 8 for even NW
+            static_assert(NW % 2 == 0, "a wave's copies share their rows' bit 3");
+            const int lr = lane >> 3;
+            piece = ((lane & 7) ^ (((wave * 8 + lr) >> 1) & 7)) * (16 / ES) + s0;
+            r = make_rsrc(static_cast<const char*>(p) + (long long)i0 * ld * ES,
+                          (uint32_t)((long long)(n - 1) * ld * ES + ((long long)K * ES + 15 & ~15LL)));
+#pragma unroll
+            for (int c = 0; c < N; ++c) off[c] = (int)(((c * NW + wave) * 8 + lr) * ld + piece) * ES;
+        }
+    }
+    // stage `n` from the first, of s below send; past it zeros are written
+    __device__ __forceinline__ void copy(char* stage, int n, int s0, int send, int wave) const {
+        if constexpr (STRIDED) {
+            // bytes of the rows that are left, with no branch between the products
+            const int left = min(send - s0 - n * S, S);
+            const auto rs = make_rsrc(base + n * step, ((uint32_t)(left - 1) * row + tail) & (uint32_t)~((left - 1) >> 31));
+#pragma unroll
+            for (int c = 0; c < N; ++c) copy_kb(rs, stage + (c * NW + wave) * 1024, off[c]);
+        } else {
+            const bool in = piece + n * S < send;
+#pragma unroll
+            for (int c = 0; c < N; ++c) copy_kb(r, stage + (c * NW + wave) * 1024, in ? off[c] + n * kStageK : kOOB);
+        }
+    }
+};
+
+// Stage n + 2 is copied into the buffer that stage n has just been read from, a
+// whole stage ahead of its use; the reads of a step are issued one step before its
+// products, across the stages' border too, so there is one barrier per stage.
+template <typename T, int BM, int BN, int WM, int WN, bool TA, bool TB, bool SUMS>
+__global__ __launch_bounds__(WM * WN * 64) void matmul_tile_kernel(Product p, int tm, int tn, int stages, float* sums) {
+    constexpr int NW = WM * WN, TI = BN / WN / 16, TJ = BM / WM / 16, S = kStageK / (int)sizeof(T);
+    constexpr int STAGE = (BM + BN) * kStageK;
+    static_assert(NW * 16 * TI * 64 <= STAGE, "results fit a stage");
+    __shared__ uint4 lds0[STAGE / 16], lds1[STAGE / 16];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const TileAt t = tile_at(tm, tn, BM, BN);
+    const int s0 = t.split * stages * S, send = min(p.K, s0 + stages * S), count = (send - s0 + S - 1) / S;
+    Copies<T, BN, NW, TA> ca;
+    Copies<T, BM, NW, TB> cb;
+    ca.init(p.a, p.lda, t.n0, p.cols, p.K, s0, wave, lane);
+    cb.init(p.b, p.ldb, t.m0, p.rows, p.K, s0, wave, lane);
+    f32x4 acc[TI][TJ];
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    Frag<T> fa[2][TI], fb[2][TJ];
+    // every buffer a restrict argument of one function: the compiler then does not
+    // make the reads of one wait for the copies into the other
+    auto loop = [&](char* __restrict__ b0, char* __restrict__ b1) __attribute__((always_inline)) {
+        auto copy = [&](char* stage, int n) __attribute__((always_inline)) {
+            ca.copy(stage, n, s0, send, wave);
+            cb.copy(stage + BN * kStageK, n, s0, send, wave);
+        };
+        auto read = [&](const char* stage, int step, int set) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < TI; ++i) fa[set][i] = fragment<T, BN, TA>(stage, 0, wn * TI + i, step);
+#pragma unroll
+            for (int j = 0; j < TJ; ++j) fb[set][j] = fragment<T, BM, TB>(stage, BN * kStageK, wm * TJ + j, step);
+        };
+        // the products of a set, with the reads (and copies) issued before them in the
+        // source spread between them: the compiler would otherwise sink the reads below
+        // the products to save registers, and the next step would wait for them
+        constexpr int READS = (TA ? (sizeof(T) == 4 ? 4 : 2) : 1) * TI + (TB ? (sizeof(T) == 4 ? 4 : 2) : 1) * TJ;
+        constexpr int MATH = TI * TJ * (sizeof(T) == 4 ? 4 : 1), PER = MATH / READS > 0 ? MATH / READS : 1;
+        auto multiply_set = [&](int set, bool copies) __attribute__((always_inline)) {
+            products<T, TI, TJ>(acc, fa[set], fb[set]);
+#pragma unroll
+            for (int i = 0; i < READS; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, PER, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                if (copies) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        // From the second step of stage n, whose operands have been read, to the second
+        // step of the next.  At the barrier this wave's reads of `cur` are complete and its
+        // copies of the next stage have landed.  (The loop turns here, where no copy is in
+        // flight: after the turn the compiler cannot tell the buffers of copies and
+        // transposing reads apart.)
+        auto stage = [&](char* cur, char* next, int n) __attribute__((always_inline)) {
+            __atomic_signal_fence(__ATOMIC_SEQ_CST);
+            __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0)
+            __builtin_amdgcn_s_barrier();
+            __atomic_signal_fence(__ATOMIC_SEQ_CST);
+            read(next, 0, 0);
+            copy(cur, n + 2);
+            multiply_set(1, true);
+            read(next, 1, 1);
+            multiply_set(0, false);
+        };
+        ca.copy(b0, 0, s0, send, wave);
+        ca.copy(b1, 1, s0, send, wave);
+        cb.copy(b0 + BN * kStageK, 0, s0, send, wave);
+        cb.copy(b1 + BN * kStageK, 1, s0, send, wave);
+        __builtin_amdgcn_s_waitcnt(0x0070);
+        __builtin_amdgcn_s_barrier();
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        read(b0, 0, 0);
+        read(b0, 1, 1);
+        multiply_set(0, false);
+        for (int n = 0; n + 1 < count; n += 2) {
+            stage(b0, b1, n);
+            if (n + 2 < count) stage(b1, b0, n + 1);
+        }
+        multiply_set(1, false);
+    };
+    loop(reinterpret_cast<char*>(lds0), reinterpret_cast<char*>(lds1));
+    __builtin_amdgcn_s_waitcnt(0x0070);   // no copy is in flight when the buffers take the results
+    __syncthreads();
+    write_results<T, TI, TJ, SUMS>(p, acc, reinterpret_cast<char*>(lds0) + wave * (16 * TI * 64), t.m0 + wm * TJ * 16,
+                                   t.n0 + wn * TI * 16, sums + (long long)t.split * p.rows * p.cols);
 }
 
 // Adds the parts of a product that was split along s, in order, and finishes.
@@ -378,12 +521,13 @@ struct Plan {
     int b, tm, tn, splits, stages;   // square tiles of b
 };
 
-// The larger tile where it gives every compute unit one and the columns fill it;
-// few tiles of a long s are split along it until they do.
-Plan make_plan(int rows, int cols, int K, int es) {
+// The largest tile that still gives every compute unit one and that the columns
+// fill (256: aligned operands only); few tiles of a long s are split along it until
+// they do.
+Plan make_plan(int rows, int cols, int K, int es, bool aligned) {
     auto tiles = [&](int b) { return (long long)((rows + b - 1) / b) * ((cols + b - 1) / b); };
     Plan p;
-    p.b = cols > 64 && rows > 64 && tiles(128) >= kUnits ? 128 : 64;
+    p.b = aligned && cols > 128 && rows > 128 && tiles(256) >= kUnits ? 256 : cols > 64 && rows > 64 && tiles(128) >= kUnits ? 128 : 64;
     p.tm = (rows + p.b - 1) / p.b;
     p.tn = (cols + p.b - 1) / p.b;
     const int all = (int)(((long long)K * es + kStageK - 1) / kStageK);
@@ -397,25 +541,42 @@ Plan make_plan(int rows, int cols, int K, int es) {
     return p;
 }
 
-size_t split_bytes(const Plan& p, int rows, int cols) {
-    return p.splits > 1 ? (size_t)p.splits * rows * cols * 4 : 0;
+// One figure for either alignment.
+size_t split_bytes(int rows, int cols, int K, int es) {
+    const Plan u = make_plan(rows, cols, K, es, false), v = make_plan(rows, cols, K, es, true);
+    const int splits = u.splits > v.splits ? u.splits : v.splits;
+    return splits > 1 ? (size_t)splits * rows * cols * 4 : 0;
+}
+
+// Whole 16-byte pieces at aligned addresses; along s too where it is contiguous
+// (`padded`: with zeros, up to a whole piece).
+bool aligned_operand(const void* p, long long ld, int K, int es, bool strided, bool padded) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * es % 16 == 0 && (strided || padded || (long long)K * es % 16 == 0);
 }
 
 template <typename T, bool TA, bool TB, bool SUMS>
-hipError_t tiled(const Product& p, const Plan& q, float* sums, hipStream_t st) {
+hipError_t tiled(const Product& p, const Plan& q, bool aligned, float* sums, hipStream_t st) {
     const unsigned blocks = (unsigned)(q.tm * q.tn * q.splits);
-    if (q.b == 128)
+    if (q.b == 256) matmul_tile_kernel<T, 256, 256, 2, 4, TA, TB, SUMS><<<blocks, 512, 0, st>>>(p, q.tm, q.tn, q.stages, sums);
+    else if (q.b == 128 && aligned)
+        matmul_tile_kernel<T, 128, 128, 2, 2, TA, TB, SUMS><<<blocks, 256, 0, st>>>(p, q.tm, q.tn, q.stages, sums);
+    else if (q.b == 128)
         matmul_staged_kernel<T, 128, 128, 2, 2, TA, TB, SUMS><<<blocks, 256, 0, st>>>(p, q.tm, q.tn, q.stages, sums);
+    else if (aligned)
+        matmul_tile_kernel<T, 64, 64, 2, 2, TA, TB, SUMS><<<blocks, 256, 0, st>>>(p, q.tm, q.tn, q.stages, sums);
     else
         matmul_staged_kernel<T, 64, 64, 2, 2, TA, TB, SUMS><<<blocks, 256, 0, st>>>(p, q.tm, q.tn, q.stages, sums);
     return hipGetLastError();
 }
 
-template <typename T, bool TA, bool TB> hipError_t product(const Product& p, void* ws, hipStream_t st) {
-    const Plan q = make_plan(p.rows, p.cols, p.K, (int)sizeof(T));
+// `padded`: the rows of b end in zeros, up to a whole piece.
+template <typename T, bool TA, bool TB> hipError_t product(const Product& p, bool padded, void* ws, hipStream_t st) {
+    constexpr int ES = (int)sizeof(T);
+    const bool aligned = aligned_operand(p.a, p.lda, p.K, ES, TA, false) && aligned_operand(p.b, p.ldb, p.K, ES, TB, padded);
+    const Plan q = make_plan(p.rows, p.cols, p.K, ES, aligned);
     float* const sums = static_cast<float*>(ws);
-    if (q.splits == 1) return tiled<T, TA, TB, false>(p, q, nullptr, st);
-    const hipError_t e = tiled<T, TA, TB, true>(p, q, sums, st);
+    if (q.splits == 1) return tiled<T, TA, TB, false>(p, q, aligned, nullptr, st);
+    const hipError_t e = tiled<T, TA, TB, true>(p, q, aligned, sums, st);
     if (e != hipSuccess) return e;
     const long long pieces = (long long)p.rows * ((p.cols + kPiece<T> - 1) / kPiece<T>);
     matmul_join_kernel<T><<<(unsigned)((pieces + 255) / 256), 256, 0, st>>>(p, sums, q.splits);
@@ -462,7 +623,7 @@ template <typename T> BwdSpace bwd_space(int M, int K, int N) {
     b.dz = 0;
     b.sums = round256((size_t)M * dz_stride<T>(N) * sizeof(T));
     b.parts = b.sums + round256((size_t)d.chunks * N * 4);
-    const size_t u = split_bytes(make_plan(M, K, N, (int)sizeof(T)), M, K), v = split_bytes(make_plan(N, K, M, (int)sizeof(T)), N, K);
+    const size_t u = split_bytes(M, K, N, (int)sizeof(T)), v = split_bytes(N, K, M, (int)sizeof(T));
     b.end = b.parts + (u > v ? u : v);
     return b;
 }
@@ -488,12 +649,12 @@ template <typename T> hipError_t gradients(const MatmulBwdArgs& a, char* ws, hip
     p.ldb = dz ? ldd : a.lddy;
     if (a.dx) {
         p.a = a.w; p.lda = a.ldw; p.rows = a.M; p.cols = a.K; p.K = a.N; p.y = a.dx; p.ldy = a.lddx;
-        e = product<T, true, false>(p, ws + b.parts, st);
+        e = product<T, true, false>(p, dz, ws + b.parts, st);
         if (e != hipSuccess) return e;
     }
     if (a.dw) {
         p.a = a.x; p.lda = a.ldx; p.rows = a.N; p.cols = a.K; p.K = a.M; p.y = a.dw; p.ldy = a.lddw;
-        e = product<T, true, true>(p, ws + b.parts, st);
+        e = product<T, true, true>(p, dz, ws + b.parts, st);
     }
     return e;
 }
@@ -508,7 +669,7 @@ bool matmul_supports(int M, int K, int N) {
 }
 
 size_t matmul_workspace(int M, int K, int N, int dtype) {
-    return split_bytes(make_plan(M, N, K, dtype == 0 ? 4 : 2), M, N);
+    return split_bytes(M, N, K, dtype == 0 ? 4 : 2);
 }
 
 size_t matmul_bwd_workspace(int M, int K, int N, int dtype) {
@@ -519,7 +680,8 @@ hipError_t launch_matmul(const MatmulArgs& a, void* ws, hipStream_t st) {
     Product p = {};
     p.a = a.w; p.b = a.x; p.lda = a.ldw; p.ldb = a.ldx; p.rows = a.M; p.cols = a.N; p.K = a.K;
     p.bias = a.bias; p.residual = a.residual; p.z = a.z; p.y = a.y; p.ldr = a.ldr; p.ldz = a.ldz; p.ldy = a.ldy; p.act = a.act;
-    return a.dtype == 0 /* CONV2D_F32 */ ? product<float, false, false>(p, ws, st) : product<bf16_t, false, false>(p, ws, st);
+    return a.dtype == 0 /* CONV2D_F32 */ ? product<float, false, false>(p, false, ws, st)
+                                         : product<bf16_t, false, false>(p, false, ws, st);
 }
 
 hipError_t launch_matmul_bwd(const MatmulBwdArgs& a, void* ws, hipStream_t st) {
