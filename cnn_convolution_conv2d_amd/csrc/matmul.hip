@@ -143,6 +143,16 @@ __device__ __forceinline__ Frag<T> fragment(const char* stage, int base, int blo
 
 // ------------------------------------------------------------------ epilogue
 
+template <typename T, int V> __device__ __forceinline__ void store_values(T* p, int left, const float (&v)[V]) {
+    if (left >= V) {
+        Vec<T, V>::store(p, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            if (e < left) store_f32<T>(p, e, v[e]);
+    }
+}
+
 // V consecutive results of row r from column c on: from the sums (and their
 // biases) to z and y.
 template <typename T, int V>
@@ -160,10 +170,10 @@ __device__ __forceinline__ void finish(const Product& p, long long r, int c, flo
     }
 #pragma unroll
     for (int e = 0; e < V; ++e) v[e] += bias[e];
-    if (p.z) store_piece<T>(static_cast<T*>(p.z) + r * p.ldz, c, p.cols, __builtin_bit_cast(uint4, Vec<T, V>::pack(v)));
+    if (p.z) store_values<T, V>(static_cast<T*>(p.z) + r * p.ldz + c, p.cols - c, v);
 #pragma unroll
     for (int e = 0; e < V; ++e) v[e] = activate(v[e], p.act) + rv[e];
-    store_piece<T>(static_cast<T*>(p.y) + r * p.ldy, c, p.cols, __builtin_bit_cast(uint4, Vec<T, V>::pack(v)));
+    store_values<T, V>(static_cast<T*>(p.y) + r * p.ldy + c, p.cols - c, v);
 }
 
 // A wave's results, TI*16 columns x TJ*16 rows from (m0, n0): block by block of
@@ -199,7 +209,7 @@ __device__ __forceinline__ void write_results(const Product& p, f32x4 (&acc)[TI]
             }
             const int m = m0 + j * 16 + r;
             if (m < p.rows && c < p.cols) {
-                if constexpr (SUMS) store_piece<float>(sums + (long long)m * p.cols, c, p.cols, __builtin_bit_cast(uint4, Vec<float, V>::pack(v)));
+                if constexpr (SUMS) store_values<float, V>(sums + (long long)m * p.cols + c, p.cols - c, v);
                 else finish<T, V>(p, m, c, v, bias);
             }
         }
@@ -471,6 +481,79 @@ __global__ __launch_bounds__(256) void matmul_join_kernel(Product p, const float
     finish<T, V>(p, r, c, v, bias);
 }
 
+// ------------------------------------------------------------------ few rows
+
+// Up to 64 rows of the forward product, which reading the weights bounds: they stream
+// from memory straight into the matrix unit's registers.  One workgroup: NG * 16
+// columns, MT * 16 rows, all of s; its waves split s, 128 bytes of a row at a time (so
+// that a step reads whole lines), and join in LDS.  Columns are the rows of the 16x16
+// result, so a lane ends with 4 consecutive ones of one row.  The loads of U steps
+// stand before their products.
+template <typename T, int MT, int NG, int U, bool ALIGNED>
+__global__ __launch_bounds__(1024) void matmul_skinny_kernel(Product p) {
+    extern __shared__ f32x4 joined[];   // [wave][NG][MT][64]
+    constexpr int ES = (int)sizeof(T), E = kPiece<T>, S = kStageK / ES;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    const int n0 = blockIdx.x * (NG * 16), row = lane & 15, c = lane >> 4;
+    const T* const pa = static_cast<const T*>(p.a) + (long long)n0 * p.lda;
+    const T* const pb = static_cast<const T*>(p.b);
+    const auto ra = make_rsrc(pa, (uint32_t)(((min(p.cols - n0, NG * 16) - 1) * p.lda + p.K) * ES));
+    const auto rb = make_rsrc(pb, (uint32_t)(((p.rows - 1) * p.ldb + p.K) * ES));
+    f32x4 acc[NG][MT];
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[g][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // 16 bytes of row r of an operand, 0 past its last row and past K
+    auto fetch = [&](const T* base, __amdgpu_buffer_rsrc_t rs, long long ld, int r, bool in, int s) __attribute__((always_inline)) {
+        Frag<T> f;
+        if constexpr (ALIGNED) f.v = __builtin_bit_cast(decltype(f.v), load16(rs, in && s < p.K ? (int)(r * ld + s) * ES : kOOB));
+        else f.v = __builtin_bit_cast(decltype(f.v), in && s < p.K ? load_piece<T>(base + r * ld + s, p.K - s) : make_uint4(0, 0, 0, 0));
+        return f;
+    };
+    const int stride = waves * S;
+    for (int s0 = wave * S; s0 < p.K; s0 += stride * U) {
+        Frag<T> a[U][2][NG], b[U][2][MT];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int s = s0 + u * stride + h * (S / 2) + c * E;
+#pragma unroll
+                for (int g = 0; g < NG; ++g) a[u][h][g] = fetch(pa, ra, p.lda, g * 16 + row, n0 + g * 16 + row < p.cols, s);
+#pragma unroll
+                for (int t = 0; t < MT; ++t) b[u][h][t] = fetch(pb, rb, p.ldb, t * 16 + row, t * 16 + row < p.rows, s);
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) multiply(acc[g][t], a[u][h][g], b[u][h][t]);
+    }
+    constexpr int COUNT = NG * MT * 64;
+#pragma unroll
+    for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) joined[wave * COUNT + (g * MT + t) * 64 + lane] = acc[g][t];
+    __syncthreads();
+    for (int e = threadIdx.x; e < COUNT; e += blockDim.x) {
+        f32x4 sum = joined[e];
+        for (int k = 1; k < waves; ++k) sum += joined[k * COUNT + e];
+        const int tile = e >> 6, m = tile % MT * 16 + (e & 15), n = n0 + tile / MT * 16 + ((e & 63) >> 4) * 4;
+        if (m >= p.rows || n >= p.cols) continue;
+        float v[4], bias[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v[k] = sum[k];
+            bias[k] = p.bias && n + k < p.cols ? p.bias[n + k] : 0.0f;
+        }
+        finish<T, 4>(p, m, n, v, bias);
+    }
+}
+
 // ------------------------------------------------------------------ dz
 
 // dz = dy act'(z) (rounded to T; null: not wanted), rows padded with zeros to ldd
@@ -583,6 +666,37 @@ template <typename T, bool TA, bool TB> hipError_t product(const Product& p, boo
     return hipGetLastError();
 }
 
+// Rows up to kSkinnyRows read the weights once whatever the tile, so the skinny
+// kernel, which does nothing else, takes them.
+constexpr int kSkinnyRows = 64;
+
+template <typename T, int MT, int NG, int U> hipError_t skinny_instance(const Product& p, bool aligned, int waves, hipStream_t st) {
+    const unsigned blocks = (unsigned)(((long long)p.cols + NG * 16 - 1) / (NG * 16));
+    const int lds = waves * NG * MT * 1024;
+    // any alignment: pieces that end with their row take registers, so fewer at a time
+    if (aligned) matmul_skinny_kernel<T, MT, NG, U, true><<<blocks, waves * 64, lds, st>>>(p);
+    else matmul_skinny_kernel<T, MT, NG, (MT * NG > 1 ? 1 : U < 4 ? U : 4), false><<<blocks, waves * 64, lds, st>>>(p);
+    return hipGetLastError();
+}
+
+template <typename T> hipError_t skinny(const Product& p, hipStream_t st) {
+    constexpr int ES = (int)sizeof(T);
+    const bool aligned = aligned_operand(p.a, p.lda, p.K, ES, false, false) && aligned_operand(p.b, p.ldb, p.K, ES, false, false);
+    const int mt = p.rows <= 16 ? 1 : p.rows <= 32 ? 2 : 4;
+    const bool pairs = mt > 1 && p.cols >= 32 * kUnits;
+    const int blocks = (int)(((long long)p.cols + (pairs ? 31 : 15)) / (pairs ? 32 : 16));
+    const long long bytes = (long long)p.K * ES;
+    int waves = 4;   // 8 of 4 x 2 blocks: 64 KB of LDS
+    while (waves < (pairs && mt == 4 ? 8 : 16) && (long long)blocks * waves < 16 * kUnits && waves * 2 * kStageK <= bytes) waves *= 2;
+    const long long steps = (bytes + waves * kStageK - 1) / (waves * kStageK);
+    if (mt == 1)
+        return steps > 4   ? skinny_instance<T, 1, 1, 8>(p, aligned, waves, st)
+               : steps > 2 ? skinny_instance<T, 1, 1, 4>(p, aligned, waves, st)
+                           : skinny_instance<T, 1, 1, 2>(p, aligned, waves, st);
+    if (mt == 2) return pairs ? skinny_instance<T, 2, 2, 2>(p, aligned, waves, st) : skinny_instance<T, 2, 1, 2>(p, aligned, waves, st);
+    return pairs ? skinny_instance<T, 4, 2, 2>(p, aligned, waves, st) : skinny_instance<T, 4, 1, 2>(p, aligned, waves, st);
+}
+
 // ---- the backward pass's workspace: dz, the parts of dbias, the parts of dx or dw
 
 // Rows of dz are whole 16-byte pieces.
@@ -669,6 +783,7 @@ bool matmul_supports(int M, int K, int N) {
 }
 
 size_t matmul_workspace(int M, int K, int N, int dtype) {
+    if (M <= kSkinnyRows) return 0;
     return split_bytes(M, N, K, dtype == 0 ? 4 : 2);
 }
 
@@ -680,6 +795,7 @@ hipError_t launch_matmul(const MatmulArgs& a, void* ws, hipStream_t st) {
     Product p = {};
     p.a = a.w; p.b = a.x; p.lda = a.ldw; p.ldb = a.ldx; p.rows = a.M; p.cols = a.N; p.K = a.K;
     p.bias = a.bias; p.residual = a.residual; p.z = a.z; p.y = a.y; p.ldr = a.ldr; p.ldz = a.ldz; p.ldy = a.ldy; p.act = a.act;
+    if (a.M <= kSkinnyRows) return a.dtype == 0 /* CONV2D_F32 */ ? skinny<float>(p, st) : skinny<bf16_t>(p, st);
     return a.dtype == 0 /* CONV2D_F32 */ ? product<float, false, false>(p, false, ws, st)
                                          : product<bf16_t, false, false>(p, false, ws, st);
 }
