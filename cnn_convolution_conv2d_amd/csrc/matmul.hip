@@ -27,14 +27,42 @@ namespace {
 
 enum { kGelu = 3 };   // CONV2D_ACT_GELU; the others as in rowvec.hpp
 
-constexpr float kRoot1_2 = 0.707106781186547524f, kRoot1_2Pi = 0.398942280401432678f;
+// 1 - Phi(x), Phi the standard normal's distribution function, for x >= 0:
+// exp(-x^2 / 2) times a polynomial in 1 / (1 + 0.3 x), fitted by least squares of the
+// relative error, weighted towards its maximum, up to x = 15 (6e-8; 7 u in fp32 with
+// the reciprocal's and the exponential's).  So GELU keeps its digits on the negative
+// side, where 1 + erf has none left.
+__device__ __forceinline__ float normal_above(float x) {
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.3f, x, 1.0f));
+    float q = 3.842540085315704e-2f;
+    q = fmaf(q, t, -1.6939479112625122e-1f);
+    q = fmaf(q, t, 2.2913166880607605e-1f);
+    q = fmaf(q, t, -7.704469561576843e-2f);
+    q = fmaf(q, t, 1.429063081741333e-1f);
+    q = fmaf(q, t, 9.452608972787857e-2f);
+    q = fmaf(q, t, 1.2196046113967896e-1f);
+    q = fmaf(q, t, 1.1948209255933762e-1f);
+    q = fmaf(q, t, 7.495440513594076e-6f);
+    return q * __builtin_amdgcn_exp2f(x * x * -0.72134752044448170f);   // log2(e) / 2
+}
 
-// The complement of erf keeps the digits of GELU's negative side.
-__device__ __forceinline__ float activate(float z, int act) {
-    if (act == kActRelu) return z < 0.0f ? 0.0f : z;
-    if (act == kActSilu) return z * sigmoid(z);
-    if (act == kGelu) return 0.5f * z * erfcf(-z * kRoot1_2);
-    return z;
+__device__ __forceinline__ float normal_below(float z) {
+    const float above = normal_above(fabsf(z));
+    return z > 0.0f ? 1.0f - above : above;
+}
+
+// V values; one choice for all of them.
+template <int V> __device__ __forceinline__ void activate(float (&v)[V], int act) {
+    if (act == kActRelu) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = v[e] < 0.0f ? 0.0f : v[e];
+    } else if (act == kActSilu) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] *= sigmoid(v[e]);
+    } else if (act == kGelu) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] *= normal_below(v[e]);
+    }
 }
 
 __device__ __forceinline__ float activation_slope(float z, int act) {
@@ -43,7 +71,8 @@ __device__ __forceinline__ float activation_slope(float z, int act) {
         const float e = sigmoid(z);
         return e * (1.0f + z * (1.0f - e));
     }
-    return 0.5f * erfcf(-z * kRoot1_2) + z * kRoot1_2Pi * __expf(-0.5f * z * z);
+    // Phi(z) + z phi(z)
+    return normal_below(z) + z * 0.398942280401432678f * __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f);
 }
 
 // One product C[r][c], r < rows, c < cols, sums over s < K.
@@ -143,9 +172,17 @@ __device__ __forceinline__ Frag<T> fragment(const char* stage, int base, int blo
 
 // ------------------------------------------------------------------ epilogue
 
+// V consecutive results.  Those of 16 bytes pass the caches by, which the next
+// workgroups need for operands.
+template <typename T, int V> __device__ __forceinline__ void store_whole(T* p, const float (&v)[V]) {
+    if constexpr (sizeof(T) * V == 16)
+        __builtin_nontemporal_store(__builtin_bit_cast(u32x4, Vec<T, V>::pack(v)), reinterpret_cast<u32x4_unaligned*>(p));
+    else Vec<T, V>::store(p, v);
+}
+// `left` of them, at most V.
 template <typename T, int V> __device__ __forceinline__ void store_values(T* p, int left, const float (&v)[V]) {
     if (left >= V) {
-        Vec<T, V>::store(p, v);
+        store_whole<T, V>(p, v);
     } else {
 #pragma unroll
         for (int e = 0; e < V; ++e)
@@ -153,65 +190,129 @@ template <typename T, int V> __device__ __forceinline__ void store_values(T* p, 
     }
 }
 
-// V consecutive results of row r from column c on: from the sums (and their
-// biases) to z and y.
+// The biases of columns c ..: 0 where there is none.
+template <int V> __device__ __forceinline__ void load_bias(const Product& p, int c, float (&v)[V]) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = p.bias && c + e < p.cols ? p.bias[c + e] : 0.0f;
+}
+
+// V consecutive results of row r from column c on: from the sums (biases added) to z and y.
 template <typename T, int V>
-__device__ __forceinline__ void finish(const Product& p, long long r, int c, float (&v)[V], const float (&bias)[V]) {
-    const T* const residual = static_cast<const T*>(p.residual) + (p.residual ? r * p.ldr + c : 0);
-    const bool whole = c + V <= p.cols;
-    float rv[V] = {};
+__device__ __forceinline__ void finish(const Product& p, long long r, int c, float (&v)[V]) {
+    const int left = p.cols - c;
+    if (p.z) store_values<T, V>(static_cast<T*>(p.z) + r * p.ldz + c, left, v);
+    activate<V>(v, p.act);
     if (p.residual) {
-        if (whole) {
-            Vec<T, V>::unpack(Vec<T, V>::load(residual), rv);
+        const T* const at = static_cast<const T*>(p.residual) + r * p.ldr + c;
+        if (left >= V) {
+            float u[V];
+            Vec<T, V>::unpack(Vec<T, V>::load(at), u);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] += u[e];
         } else {
 #pragma unroll
-            for (int e = 0; e < V; ++e) rv[e] = c + e < p.cols ? load_f32<T>(residual, e) : 0.0f;
+            for (int e = 0; e < V; ++e)
+                if (e < left) v[e] += load_f32<T>(at, e);
         }
     }
-#pragma unroll
-    for (int e = 0; e < V; ++e) v[e] += bias[e];
-    if (p.z) store_values<T, V>(static_cast<T*>(p.z) + r * p.ldz + c, p.cols - c, v);
-#pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = activate(v[e], p.act) + rv[e];
-    store_values<T, V>(static_cast<T*>(p.y) + r * p.ldy + c, p.cols - c, v);
+    store_values<T, V>(static_cast<T*>(p.y) + r * p.ldy + c, left, v);
 }
 
 // A wave's results, TI*16 columns x TJ*16 rows from (m0, n0): block by block of
-// 16 rows through the wave's own piece of LDS (16 x TI*16 fp32), so that whole
-// rows leave, 16 bytes of the output type a lane.  In the 16x16 result lane l
-// holds, in register r, column 4 (l >> 4) + r of row l & 15.  SUMS: the sums
-// themselves, of a part of s, to `sums`.
-template <typename T, int TI, int TJ, bool SUMS>
+// 16 rows through the wave's own two pieces of LDS (16 x TI*16 fp32 each, the next
+// block is written before one is read), so that whole rows leave, 16 bytes of the
+// output type a lane.  In the 16x16 result lane l holds, in register r, column
+// 4 (l >> 4) + r of row l & 15.  kSums: the sums themselves, of a part of s, to `sums`;
+// kPlain: no bias, activation, residual and z (the gradients).
+//
+// A wave whose results all exist, all but those at the matrix's edges, needs no
+// conditions, and issues the residual's loads together, ahead of the first block (as
+// many as 48 registers hold).
+enum Output { kEpilogue, kPlain, kSums };
+
+template <typename T, int TI, int TJ, Output MODE>
 __device__ __forceinline__ void write_results(const Product& p, f32x4 (&acc)[TI][TJ], char* lds, int m0, int n0, float* sums) {
-    using OUT = std::conditional_t<SUMS, float, T>;
+    using OUT = std::conditional_t<MODE == kSums, float, T>;
     constexpr int V = kPiece<OUT>, PIECES = TI * 16 / V, ROW = TI * 64, MASK = (TI * 4 < 16 ? TI * 4 : 16) - 1;
-    const int lane = threadIdx.x & 63;
-    float bias[V];
-    const int c = n0 + lane % PIECES * V;   // 64 is a multiple of PIECES: a lane's columns stay
-    static_assert(64 % PIECES == 0 || PIECES % 64 == 0, "a lane's columns stay");
-#pragma unroll
-    for (int e = 0; e < V; ++e) bias[e] = !SUMS && p.bias && c + e < p.cols ? p.bias[c + e] : 0.0f;
-#pragma unroll
-    for (int j = 0; j < TJ; ++j) {
+    constexpr int ITS = 16 * PIECES / 64, STEP = 64 / PIECES;   // rows between a lane's in a block
+    static_assert(64 % PIECES == 0, "a lane's columns stay");
+    const int lane = threadIdx.x & 63, r0 = lane / PIECES, q0 = lane % PIECES * (V / 4);
+    const int c = n0 + lane % PIECES * V;
+    float bias[V] = {};
+    if constexpr (MODE == kEpilogue) load_bias<V>(p, c, bias);
+    auto put = [&](int j) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < TI; ++i)
-            *reinterpret_cast<f32x4*>(lds + (lane & 15) * ROW + ((i * 4 + (lane >> 4)) ^ (lane & 15 & MASK)) * 16) = acc[i][j];
+            *reinterpret_cast<f32x4*>(lds + ((j & 1) * 16 + (lane & 15)) * ROW + ((i * 4 + (lane >> 4)) ^ (lane & 15 & MASK)) * 16) = acc[i][j];
+    };
+    auto get = [&](int j, int it, float (&v)[V]) __attribute__((always_inline)) {
+        const int r = r0 + it * STEP;
+#pragma unroll
+        for (int h = 0; h < V / 4; ++h) {
+            const f32x4 u = *reinterpret_cast<const f32x4*>(lds + ((j & 1) * 16 + r) * ROW + ((q0 + h) ^ (r & MASK)) * 16);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[4 * h + k] = MODE == kEpilogue ? u[k] + bias[4 * h + k] : u[k];
+        }
+    };
+    if (m0 + TJ * 16 <= p.rows && n0 + TI * 16 <= p.cols) {
+        const long long row = m0 + r0;
+        OUT* const y = MODE == kSums ? reinterpret_cast<OUT*>(sums) + row * p.cols + c : static_cast<OUT*>(p.y) + row * p.ldy + c;
+        const long long ldy = MODE == kSums ? p.cols : p.ldy;
+        constexpr int AHEAD = TJ * ITS <= 12 ? TJ : 12 / ITS;
+        typename Vec<T, V>::raw residual[AHEAD][ITS] = {};
+        const T* const pr = static_cast<const T*>(p.residual) + (p.residual ? row * p.ldr + c : 0);
+        auto fetch = [&](int j) __attribute__((always_inline)) {
+            if (MODE != kEpilogue || !p.residual) return;
+#pragma unroll
+            for (int it = 0; it < ITS; ++it) residual[j % AHEAD][it] = Vec<T, V>::load(pr + (j * 16 + it * STEP) * p.ldr);
+        };
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) fetch(j);
+        put(0);
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) {
+            if (j + 1 < TJ) put(j + 1);
+            wave_lds_fence();
+            float v[ITS][V];
+#pragma unroll
+            for (int it = 0; it < ITS; ++it) get(j, it, v[it]);
+            if constexpr (MODE == kEpilogue) {
+                if (p.z) {
+#pragma unroll
+                    for (int it = 0; it < ITS; ++it)
+                        store_whole<T, V>(static_cast<T*>(p.z) + (row + j * 16 + it * STEP) * p.ldz + c, v[it]);
+                }
+                activate<ITS * V>(reinterpret_cast<float(&)[ITS * V]>(v), p.act);
+            }
+#pragma unroll
+            for (int it = 0; it < ITS; ++it) {
+                if constexpr (MODE == kEpilogue) {
+                    float u[V];
+                    Vec<T, V>::unpack(residual[j % AHEAD][it], u);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) v[it][e] += u[e];
+                }
+                store_whole<OUT, V>(y + (j * 16 + it * STEP) * ldy, v[it]);
+            }
+            if (j + AHEAD < TJ) fetch(j + AHEAD);
+            wave_lds_fence();
+        }
+        return;
+    }
+    put(0);
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+        if (j + 1 < TJ) put(j + 1);
         wave_lds_fence();
-#pragma unroll
-        for (int it = 0; it < 16 * PIECES / 64; ++it) {
-            const int e = it * 64 + lane, r = e / PIECES, q = e % PIECES * (V / 4);
+#pragma unroll 1
+        for (int it = 0; it < ITS; ++it) {
+            const int m = m0 + j * 16 + r0 + it * STEP;
             float v[V];
-#pragma unroll
-            for (int h = 0; h < V / 4; ++h) {
-                const f32x4 u = *reinterpret_cast<const f32x4*>(lds + r * ROW + ((q + h) ^ (r & MASK)) * 16);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v[4 * h + k] = u[k];
-            }
-            const int m = m0 + j * 16 + r;
-            if (m < p.rows && c < p.cols) {
-                if constexpr (SUMS) store_values<float, V>(sums + (long long)m * p.cols + c, p.cols - c, v);
-                else finish<T, V>(p, m, c, v, bias);
-            }
+            get(j, it, v);
+            if (m >= p.rows || c >= p.cols) continue;
+            if constexpr (MODE == kSums) store_values<float, V>(sums + (long long)m * p.cols + c, p.cols - c, v);
+            else if constexpr (MODE == kPlain) store_values<T, V>(static_cast<T*>(p.y) + m * p.ldy + c, p.cols - c, v);
+            else finish<T, V>(p, m, c, v);
         }
         wave_lds_fence();
     }
@@ -259,10 +360,10 @@ template <typename T, int B, int NT, bool STRIDED> struct Staged {
 
 // Operands of any alignment pass through registers: the loads of a stage are in
 // flight during the products of the one before.
-template <typename T, int BM, int BN, int WM, int WN, bool TA, bool TB, bool SUMS>
+template <typename T, int BM, int BN, int WM, int WN, bool TA, bool TB, Output MODE>
 __global__ __launch_bounds__(WM * WN * 64) void matmul_staged_kernel(Product p, int tm, int tn, int stages, float* sums) {
     constexpr int NT = WM * WN * 64, TI = BN / WN / 16, TJ = BM / WM / 16, S = kStageK / (int)sizeof(T);
-    constexpr int STAGE = (BM + BN) * kStageK, OUTB = WM * WN * 16 * TI * 64;
+    constexpr int STAGE = (BM + BN) * kStageK, OUTB = WM * WN * 32 * TI * 64;
     __shared__ uint4 lds[(STAGE > OUTB ? STAGE : OUTB) / 16];
     char* const sa = reinterpret_cast<char*>(lds);
     char* const sb = sa + BN * kStageK;
@@ -300,7 +401,7 @@ __global__ __launch_bounds__(WM * WN * 64) void matmul_staged_kernel(Product p, 
         }
     }
     __syncthreads();
-    write_results<T, TI, TJ, SUMS>(p, acc, sa + wave * (16 * TI * 64), t.m0 + wm * TJ * 16, t.n0 + wn * TI * 16,
+    write_results<T, TI, TJ, MODE>(p, acc, sa + wave * (32 * TI * 64), t.m0 + wm * TJ * 16, t.n0 + wn * TI * 16,
                                    sums + (long long)t.split * p.rows * p.cols);
 }
 
@@ -362,11 +463,11 @@ template <typename T, int B, int NW, bool STRIDED> struct Copies {
 // Stage n + 2 is copied into the buffer that stage n has just been read from, a
 // whole stage ahead of its use; the reads of a step are issued one step before its
 // products, across the stages' border too, so there is one barrier per stage.
-template <typename T, int BM, int BN, int WM, int WN, bool TA, bool TB, bool SUMS>
+template <typename T, int BM, int BN, int WM, int WN, bool TA, bool TB, Output MODE>
 __global__ __launch_bounds__(WM * WN * 64) void matmul_tile_kernel(Product p, int tm, int tn, int stages, float* sums) {
     constexpr int NW = WM * WN, TI = BN / WN / 16, TJ = BM / WM / 16, S = kStageK / (int)sizeof(T);
     constexpr int STAGE = (BM + BN) * kStageK;
-    static_assert(NW * 16 * TI * 64 <= STAGE, "results fit a stage");
+    static_assert(NW * 32 * TI * 64 <= STAGE, "results fit a stage");
     __shared__ uint4 lds0[STAGE / 16], lds1[STAGE / 16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
@@ -445,7 +546,7 @@ __global__ __launch_bounds__(WM * WN * 64) void matmul_tile_kernel(Product p, in
     loop(reinterpret_cast<char*>(lds0), reinterpret_cast<char*>(lds1));
     __builtin_amdgcn_s_waitcnt(0x0070);   // no copy is in flight when the buffers take the results
     __syncthreads();
-    write_results<T, TI, TJ, SUMS>(p, acc, reinterpret_cast<char*>(lds0) + wave * (16 * TI * 64), t.m0 + wm * TJ * 16,
+    write_results<T, TI, TJ, MODE>(p, acc, reinterpret_cast<char*>(lds0) + wave * (32 * TI * 64), t.m0 + wm * TJ * 16,
                                    t.n0 + wn * TI * 16, sums + (long long)t.split * p.rows * p.cols);
 }
 
@@ -476,9 +577,10 @@ __global__ __launch_bounds__(256) void matmul_join_kernel(Product p, const float
             for (int e = 0; e < V; ++e)
                 if (c + e < p.cols) v[e] += at[e];
     }
+    load_bias<V>(p, c, bias);
 #pragma unroll
-    for (int e = 0; e < V; ++e) bias[e] = p.bias && c + e < p.cols ? p.bias[c + e] : 0.0f;
-    finish<T, V>(p, r, c, v, bias);
+    for (int e = 0; e < V; ++e) v[e] += bias[e];
+    finish<T, V>(p, r, c, v);
 }
 
 // ------------------------------------------------------------------ few rows
@@ -545,12 +647,10 @@ __global__ __launch_bounds__(1024) void matmul_skinny_kernel(Product p) {
         const int tile = e >> 6, m = tile % MT * 16 + (e & 15), n = n0 + tile / MT * 16 + ((e & 63) >> 4) * 4;
         if (m >= p.rows || n >= p.cols) continue;
         float v[4], bias[4];
+        load_bias<4>(p, n, bias);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            v[k] = sum[k];
-            bias[k] = p.bias && n + k < p.cols ? p.bias[n + k] : 0.0f;
-        }
-        finish<T, 4>(p, m, n, v, bias);
+        for (int k = 0; k < 4; ++k) v[k] = sum[k] + bias[k];
+        finish<T, 4>(p, m, n, v);
     }
 }
 
@@ -605,12 +705,18 @@ struct Plan {
 };
 
 // The largest tile that still gives every compute unit one and that the columns
-// fill (256: aligned operands only); few tiles of a long s are split along it until
-// they do.
+// fill.  256, of aligned operands only, has the compute unit to itself, so its
+// results leave while nothing else is done: two workgroups of 128 are faster where s
+// is short (16384 x 1024 -> 4096 bf16 with a residual 185 us against 192, x 128 93
+// against 116; but 16384 x 2048 -> 1024 78 against 70).  Few tiles of a long s are
+// split along it until they are enough.
+constexpr int kLongBytes = 2048;
+
 Plan make_plan(int rows, int cols, int K, int es, bool aligned) {
     auto tiles = [&](int b) { return (long long)((rows + b - 1) / b) * ((cols + b - 1) / b); };
     Plan p;
-    p.b = aligned && cols > 128 && rows > 128 && tiles(256) >= kUnits ? 256 : cols > 64 && rows > 64 && tiles(128) >= kUnits ? 128 : 64;
+    const bool large = aligned && (long long)K * es > kLongBytes && cols > 128 && rows > 128 && tiles(256) >= kUnits;
+    p.b = large ? 256 : cols > 64 && rows > 64 && tiles(128) >= kUnits ? 128 : 64;
     p.tm = (rows + p.b - 1) / p.b;
     p.tn = (cols + p.b - 1) / p.b;
     const int all = (int)(((long long)K * es + kStageK - 1) / kStageK);
@@ -637,18 +743,18 @@ bool aligned_operand(const void* p, long long ld, int K, int es, bool strided, b
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * es % 16 == 0 && (strided || padded || (long long)K * es % 16 == 0);
 }
 
-template <typename T, bool TA, bool TB, bool SUMS>
+template <typename T, bool TA, bool TB, Output MODE>
 hipError_t tiled(const Product& p, const Plan& q, bool aligned, float* sums, hipStream_t st) {
     const unsigned blocks = (unsigned)(q.tm * q.tn * q.splits);
-    if (q.b == 256) matmul_tile_kernel<T, 256, 256, 2, 4, TA, TB, SUMS><<<blocks, 512, 0, st>>>(p, q.tm, q.tn, q.stages, sums);
+    if (q.b == 256) matmul_tile_kernel<T, 256, 256, 2, 4, TA, TB, MODE><<<blocks, 512, 0, st>>>(p, q.tm, q.tn, q.stages, sums);
     else if (q.b == 128 && aligned)
-        matmul_tile_kernel<T, 128, 128, 2, 2, TA, TB, SUMS><<<blocks, 256, 0, st>>>(p, q.tm, q.tn, q.stages, sums);
+        matmul_tile_kernel<T, 128, 128, 2, 2, TA, TB, MODE><<<blocks, 256, 0, st>>>(p, q.tm, q.tn, q.stages, sums);
     else if (q.b == 128)
-        matmul_staged_kernel<T, 128, 128, 2, 2, TA, TB, SUMS><<<blocks, 256, 0, st>>>(p, q.tm, q.tn, q.stages, sums);
+        matmul_staged_kernel<T, 128, 128, 2, 2, TA, TB, MODE><<<blocks, 256, 0, st>>>(p, q.tm, q.tn, q.stages, sums);
     else if (aligned)
-        matmul_tile_kernel<T, 64, 64, 2, 2, TA, TB, SUMS><<<blocks, 256, 0, st>>>(p, q.tm, q.tn, q.stages, sums);
+        matmul_tile_kernel<T, 64, 64, 2, 2, TA, TB, MODE><<<blocks, 256, 0, st>>>(p, q.tm, q.tn, q.stages, sums);
     else
-        matmul_staged_kernel<T, 64, 64, 2, 2, TA, TB, SUMS><<<blocks, 256, 0, st>>>(p, q.tm, q.tn, q.stages, sums);
+        matmul_staged_kernel<T, 64, 64, 2, 2, TA, TB, MODE><<<blocks, 256, 0, st>>>(p, q.tm, q.tn, q.stages, sums);
     return hipGetLastError();
 }
 
@@ -658,8 +764,8 @@ template <typename T, bool TA, bool TB> hipError_t product(const Product& p, boo
     const bool aligned = aligned_operand(p.a, p.lda, p.K, ES, TA, false) && aligned_operand(p.b, p.ldb, p.K, ES, TB, padded);
     const Plan q = make_plan(p.rows, p.cols, p.K, ES, aligned);
     float* const sums = static_cast<float*>(ws);
-    if (q.splits == 1) return tiled<T, TA, TB, false>(p, q, aligned, nullptr, st);
-    const hipError_t e = tiled<T, TA, TB, true>(p, q, aligned, sums, st);
+    if (q.splits == 1) return tiled<T, TA, TB, TA ? kPlain : kEpilogue>(p, q, aligned, nullptr, st);
+    const hipError_t e = tiled<T, TA, TB, kSums>(p, q, aligned, sums, st);
     if (e != hipSuccess) return e;
     const long long pieces = (long long)p.rows * ((p.cols + kPiece<T> - 1) / kPiece<T>);
     matmul_join_kernel<T><<<(unsigned)((pieces + 255) / 256), 256, 0, st>>>(p, sums, q.splits);
