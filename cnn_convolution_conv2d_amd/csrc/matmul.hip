@@ -550,33 +550,53 @@ __global__ __launch_bounds__(WM * WN * 64) void matmul_tile_kernel(Product p, in
                                    t.n0 + wn * TI * 16, sums + (long long)t.split * p.rows * p.cols);
 }
 
-// Adds the parts of a product that was split along s, in order, and finishes.
+// Adds the parts of a product that was split along s and finishes.  `groups` (a power
+// of two up to 8) threads share a piece of 16 bytes of results, each adds every
+// groups-th part, and the first adds theirs: a fixed order, and enough loads in
+// flight where the results are few.
 template <typename T>
-__global__ __launch_bounds__(256) void matmul_join_kernel(Product p, const float* sums, int splits) {
+__global__ __launch_bounds__(256) void matmul_join_kernel(Product p, const float* sums, int splits, int groups) {
     constexpr int V = kPiece<T>;
+    __shared__ float part[256][V + 1];
+    const int per = 256 / groups, group = threadIdx.x / per;
     const int pieces = (p.cols + V - 1) / V;
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x, total = (long long)p.rows * p.cols;
-    if (i >= (long long)p.rows * pieces) return;
+    const long long i = (long long)blockIdx.x * per + threadIdx.x % per, total = (long long)p.rows * p.cols;
     const long long r = i / pieces;
     const int c = (int)(i - r * pieces) * V;
-    float v[V] = {}, bias[V];
-    const float* at = sums + r * p.cols + c;
-    if (c + V <= p.cols) {
-        for (int k = 0; k < splits; ++k, at += total) {
+    const bool in = r < p.rows;
+    float v[V] = {};
+    if (in) {
+        const float* at = sums + group * total + r * p.cols + c;
+        const long long step = groups * total;
+        if (c + V <= p.cols) {
+#pragma unroll 4
+            for (int k = group; k < splits; k += groups, at += step) {
 #pragma unroll
-            for (int h = 0; h < V; h += 4) {
-                float u[4];
-                Vec<float, 4>::unpack(Vec<float, 4>::load(at + h), u);
+                for (int h = 0; h < V; h += 4) {
+                    float u[4];
+                    Vec<float, 4>::unpack(Vec<float, 4>::load(at + h), u);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[h + e] += u[e];
+                    for (int e = 0; e < 4; ++e) v[h + e] += u[e];
+                }
             }
-        }
-    } else {
-        for (int k = 0; k < splits; ++k, at += total)
+        } else {
+            for (int k = group; k < splits; k += groups, at += step)
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                if (c + e < p.cols) v[e] += at[e];
+                for (int e = 0; e < V; ++e)
+                    if (c + e < p.cols) v[e] += at[e];
+        }
     }
+    if (groups > 1) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) part[threadIdx.x][e] = v[e];
+        __syncthreads();
+        if (group) return;
+        for (int g = 1; g < groups; ++g)
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] += part[g * per + threadIdx.x][e];
+    }
+    if (!in) return;
+    float bias[V];
     load_bias<V>(p, c, bias);
 #pragma unroll
     for (int e = 0; e < V; ++e) v[e] += bias[e];
@@ -708,23 +728,26 @@ struct Plan {
 // fill.  256, of aligned operands only, has the compute unit to itself, so its
 // results leave while nothing else is done: two workgroups of 128 are faster where s
 // is short (16384 x 1024 -> 4096 bf16 with a residual 185 us against 192, x 128 93
-// against 116; but 16384 x 2048 -> 1024 78 against 70).  Few tiles of a long s are
-// split along it until they are enough.
+// against 116; but 16384 x 2048 -> 1024 78 against 70).
+//
+// Few tiles are split along s until every compute unit has two.  A part of 128 is at
+// least 16 stages long: 256 x 4096 -> 4096 takes 27 us in 8 parts of 128 and 46 in tiles
+// of 64, but 2048 x 1024 -> 1024 18 in parts of 8 stages and 11 in tiles of 64.  A part of
+// 64 is at least 4 (dw of 100352 x 256 -> 64: 22.7 us with two a unit, 27.7 with one).
 constexpr int kLongBytes = 2048;
 
 Plan make_plan(int rows, int cols, int K, int es, bool aligned) {
     auto tiles = [&](int b) { return (long long)((rows + b - 1) / b) * ((cols + b - 1) / b); };
+    const int all = (int)(((long long)K * es + kStageK - 1) / kStageK);
+    auto parts = [&](int stages) { return all / stages > 1 ? all / stages : 1; };
     Plan p;
     const bool large = aligned && (long long)K * es > kLongBytes && cols > 128 && rows > 128 && tiles(256) >= kUnits;
-    p.b = large ? 256 : cols > 64 && rows > 64 && tiles(128) >= kUnits ? 128 : 64;
+    p.b = large ? 256 : cols > 64 && rows > 64 && tiles(128) * parts(16) >= kUnits ? 128 : 64;
     p.tm = (rows + p.b - 1) / p.b;
     p.tn = (cols + p.b - 1) / p.b;
-    const int all = (int)(((long long)K * es + kStageK - 1) / kStageK);
-    const long long t = (long long)p.tm * p.tn;
-    // a part is at least 4 stages long
-    const long long want = t >= kUnits ? 1 : kUnits / t, most = all / 4;
+    const long long t = (long long)p.tm * p.tn, want = t >= kUnits ? 1 : 2 * kUnits / t;
+    const int most = parts(p.b == 64 ? 4 : 16);
     p.splits = (int)(want < most ? want : most);
-    if (p.splits < 1) p.splits = 1;
     p.stages = (all + p.splits - 1) / p.splits;
     p.splits = (all + p.stages - 1) / p.stages;
     return p;
@@ -768,7 +791,9 @@ template <typename T, bool TA, bool TB> hipError_t product(const Product& p, boo
     const hipError_t e = tiled<T, TA, TB, kSums>(p, q, aligned, sums, st);
     if (e != hipSuccess) return e;
     const long long pieces = (long long)p.rows * ((p.cols + kPiece<T> - 1) / kPiece<T>);
-    matmul_join_kernel<T><<<(unsigned)((pieces + 255) / 256), 256, 0, st>>>(p, sums, q.splits);
+    int groups = 1;
+    while (groups < 8 && groups * 4 <= q.splits) groups *= 2;
+    matmul_join_kernel<T><<<(unsigned)((pieces * groups + 255) / 256), 256, 0, st>>>(p, sums, q.splits, groups);
     return hipGetLastError();
 }
 
