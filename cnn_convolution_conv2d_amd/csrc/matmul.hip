@@ -366,7 +366,6 @@ __global__ __launch_bounds__(WM * WN * 64) void matmul_staged_kernel(Product p, 
     constexpr int STAGE = (BM + BN) * kStageK, OUTB = WM * WN * 32 * TI * 64;
     __shared__ uint4 lds[(STAGE > OUTB ? STAGE : OUTB) / 16];
     char* const sa = reinterpret_cast<char*>(lds);
-    char* const sb = sa + BN * kStageK;
     const int wave = threadIdx.x >> 6, wm = wave / WN, wn = wave % WN;
     const TileAt t = tile_at(tm, tn, BM, BN);
     const int s0 = t.split * stages * S, send = min(p.K, s0 + stages * S);
@@ -377,19 +376,17 @@ __global__ __launch_bounds__(WM * WN * 64) void matmul_staged_kernel(Product p, 
         for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     Staged<T, BN, NT, TA> a;
     Staged<T, BM, NT, TB> b;
-    const T* const pa = static_cast<const T*>(p.a);
-    const T* const pb = static_cast<const T*>(p.b);
-    a.load(pa, p.lda, t.n0, p.cols, s0, send);
-    b.load(pb, p.ldb, t.m0, p.rows, s0, send);
+    auto load = [&](int s) __attribute__((always_inline)) {
+        a.load(static_cast<const T*>(p.a), p.lda, t.n0, p.cols, s, send);
+        b.load(static_cast<const T*>(p.b), p.ldb, t.m0, p.rows, s, send);
+    };
+    load(s0);
     for (int s = s0; s < send; s += S) {
         __syncthreads();
         a.store(sa);
-        b.store(sb);
+        b.store(sa + BN * kStageK);
         __syncthreads();
-        if (s + S < send) {
-            a.load(pa, p.lda, t.n0, p.cols, s + S, send);
-            b.load(pb, p.ldb, t.m0, p.rows, s + S, send);
-        }
+        if (s + S < send) load(s + S);
 #pragma unroll
         for (int step = 0; step < 2; ++step) {
             Frag<T> fa[TI], fb[TJ];
@@ -551,7 +548,7 @@ __global__ __launch_bounds__(WM * WN * 64) void matmul_tile_kernel(Product p, in
 }
 
 // Adds the parts of a product that was split along s and finishes.  `groups` (a power
-// of two up to 8) threads share a piece of 16 bytes of results, each adds every
+// of two up to 32) threads share a piece of 16 bytes of results, each adds every
 // groups-th part, and the first adds theirs: a fixed order, and enough loads in
 // flight where the results are few.
 template <typename T>
@@ -688,20 +685,31 @@ __global__ __launch_bounds__(256) void matmul_dz_kernel(MatmulBwdArgs a, T* dz, 
     const int c = (blockIdx.x * lanes + l) * V;
     const long long m0 = (long long)blockIdx.y * chunk, m1 = m0 + chunk < a.M ? m0 + chunk : a.M;
     float s[V] = {};
-    if (c < a.N) {
+    auto row = [&](long long m, float (&v)[V], float (&z)[V]) __attribute__((always_inline)) {
+        if constexpr (ACT) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[e] = c + e < a.N ? v[e] * activation_slope(z[e], a.act) : 0.0f;
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) s[e] += v[e];
+        if (dz) Vec<T, V>::store(dz + m * ldd + c, v);
+    };
+    const T* const py = static_cast<const T*>(a.dy) + c;
+    const T* const pz = static_cast<const T*>(a.z) + (ACT ? c : 0);
+    if (c + V <= a.N) {
+#pragma unroll 4
         for (long long m = m0 + group; m < m1; m += groups) {
-            const T* const py = static_cast<const T*>(a.dy) + m * a.lddy + c;
-            const T* const pz = static_cast<const T*>(a.z) + (ACT ? m * a.ldz + c : 0);
             float v[V], z[V];
-            Vec<T, V>::unpack(__builtin_bit_cast(typename Vec<T, V>::raw, load_piece<T>(py, a.N - c)), v);
-            if constexpr (ACT) {
-                Vec<T, V>::unpack(__builtin_bit_cast(typename Vec<T, V>::raw, load_piece<T>(pz, a.N - c)), z);
-#pragma unroll
-                for (int e = 0; e < V; ++e) v[e] = c + e < a.N ? v[e] * activation_slope(z[e], a.act) : 0.0f;
-            }
-#pragma unroll
-            for (int e = 0; e < V; ++e) s[e] += v[e];
-            if (dz) Vec<T, V>::store(dz + m * ldd + c, v);
+            Vec<T, V>::unpack(Vec<T, V>::load(py + m * a.lddy), v);
+            if constexpr (ACT) Vec<T, V>::unpack(Vec<T, V>::load(pz + m * a.ldz), z);
+            row(m, v, z);
+        }
+    } else if (c < a.N) {
+        for (long long m = m0 + group; m < m1; m += groups) {
+            float v[V], z[V];
+            Vec<T, V>::unpack(__builtin_bit_cast(typename Vec<T, V>::raw, load_piece<T>(py + m * a.lddy, a.N - c)), v);
+            if constexpr (ACT) Vec<T, V>::unpack(__builtin_bit_cast(typename Vec<T, V>::raw, load_piece<T>(pz + m * a.ldz, a.N - c)), z);
+            row(m, v, z);
         }
     }
     if (!sums) return;
@@ -792,7 +800,7 @@ template <typename T, bool TA, bool TB> hipError_t product(const Product& p, boo
     if (e != hipSuccess) return e;
     const long long pieces = (long long)p.rows * ((p.cols + kPiece<T> - 1) / kPiece<T>);
     int groups = 1;
-    while (groups < 8 && groups * 4 <= q.splits) groups *= 2;
+    while (groups < 32 && groups * 4 <= q.splits) groups *= 2;
     matmul_join_kernel<T><<<(unsigned)((pieces * groups + 255) / 256), 256, 0, st>>>(p, sums, q.splits, groups);
     return hipGetLastError();
 }
