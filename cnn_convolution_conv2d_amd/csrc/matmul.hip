@@ -602,7 +602,7 @@ __global__ __launch_bounds__(256) void matmul_join_kernel(Product p, const float
 
 // ------------------------------------------------------------------ few rows
 
-// Up to 64 rows of the forward product, which reading the weights bounds: they stream
+// Up to 32 rows of the forward product, which reading the weights bounds: they stream
 // from memory straight into the matrix unit's registers.  One workgroup: NG * 16
 // columns, MT * 16 rows, all of s; its waves split s, 128 bytes of a row at a time (so
 // that a step reads whole lines), and join in LDS.  Columns are the rows of the 16x16
@@ -643,6 +643,7 @@ __global__ __launch_bounds__(1024) void matmul_skinny_kernel(Product p) {
 #pragma unroll
                 for (int t = 0; t < MT; ++t) b[u][h][t] = fetch(pb, rb, p.ldb, t * 16 + row, t * 16 + row < p.rows, s);
             }
+        __builtin_amdgcn_sched_barrier(0);   // or the compiler sinks loads below products, to save registers
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -805,35 +806,51 @@ template <typename T, bool TA, bool TB> hipError_t product(const Product& p, boo
     return hipGetLastError();
 }
 
-// Rows up to kSkinnyRows read the weights once whatever the tile, so the skinny
-// kernel, which does nothing else, takes them.
-constexpr int kSkinnyRows = 64;
+struct SkinnyShape {
+    bool fits, two, pairs;   // two blocks of 16 rows; two of 16 columns
+    int waves;
+    long long steps;         // of 128 bytes of s, for a wave
+};
+
+// Up to 32 rows read the weights once whatever the tile.  Waves that split s: 4, or up
+// to 16 where that leaves the chip few, of at least 128 bytes each.  Two blocks of
+// columns use a row's values twice, where half the workgroups still fill the chip.  Few
+// columns with a long s do not: they are split along s over workgroups instead (bf16,
+// skinny and tiled: 1 x 8192 -> 1024 11.7 and 10.3 us, 1 x 16384 -> 256 20.3 and 9.8, 20 x
+// 4096 -> 1024 11.9 and 9.5; but 1 x 4096 -> 1024 7.4 and 8.9, 1 x 8192 -> 2048 12.2 and
+// 13.4, 20 x 1024 -> 1024 5.6 and 8.0).
+SkinnyShape skinny_shape(int rows, int cols, int K, int es) {
+    SkinnyShape k;
+    k.two = rows > 16;
+    k.pairs = k.two && cols >= 32 * kUnits;
+    const int blocks = (int)(((long long)cols + (k.pairs ? 31 : 15)) / (k.pairs ? 32 : 16));
+    const long long bytes = (long long)K * es;
+    k.waves = 4;
+    while (k.waves < 16 && (long long)blocks * k.waves < 16 * kUnits && k.waves * 2 * kStageK <= bytes) k.waves *= 2;
+    k.steps = (bytes + k.waves * kStageK - 1) / (k.waves * kStageK);
+    k.fits = rows <= 32 && !(blocks <= (rows > 8 ? 128 : 64) && k.steps >= (k.two ? 4 : 8));
+    return k;
+}
 
 template <typename T, int MT, int NG, int U> hipError_t skinny_instance(const Product& p, bool aligned, int waves, hipStream_t st) {
     const unsigned blocks = (unsigned)(((long long)p.cols + NG * 16 - 1) / (NG * 16));
     const int lds = waves * NG * MT * 1024;
     // any alignment: pieces that end with their row take registers, so fewer at a time
     if (aligned) matmul_skinny_kernel<T, MT, NG, U, true><<<blocks, waves * 64, lds, st>>>(p);
-    else matmul_skinny_kernel<T, MT, NG, (MT * NG > 1 ? 1 : U < 4 ? U : 4), false><<<blocks, waves * 64, lds, st>>>(p);
+    else matmul_skinny_kernel<T, MT, NG, (MT * NG > 1 ? 1 : U), false><<<blocks, waves * 64, lds, st>>>(p);
     return hipGetLastError();
 }
 
-template <typename T> hipError_t skinny(const Product& p, hipStream_t st) {
+template <typename T> hipError_t skinny(const Product& p, const SkinnyShape& k, hipStream_t st) {
     constexpr int ES = (int)sizeof(T);
     const bool aligned = aligned_operand(p.a, p.lda, p.K, ES, false, false) && aligned_operand(p.b, p.ldb, p.K, ES, false, false);
-    const int mt = p.rows <= 16 ? 1 : p.rows <= 32 ? 2 : 4;
-    const bool pairs = mt > 1 && p.cols >= 32 * kUnits;
-    const int blocks = (int)(((long long)p.cols + (pairs ? 31 : 15)) / (pairs ? 32 : 16));
-    const long long bytes = (long long)p.K * ES;
-    int waves = 4;   // 8 of 4 x 2 blocks: 64 KB of LDS
-    while (waves < (pairs && mt == 4 ? 8 : 16) && (long long)blocks * waves < 16 * kUnits && waves * 2 * kStageK <= bytes) waves *= 2;
-    const long long steps = (bytes + waves * kStageK - 1) / (waves * kStageK);
-    if (mt == 1)
-        return steps > 4   ? skinny_instance<T, 1, 1, 8>(p, aligned, waves, st)
-               : steps > 2 ? skinny_instance<T, 1, 1, 4>(p, aligned, waves, st)
-                           : skinny_instance<T, 1, 1, 2>(p, aligned, waves, st);
-    if (mt == 2) return pairs ? skinny_instance<T, 2, 2, 2>(p, aligned, waves, st) : skinny_instance<T, 2, 1, 2>(p, aligned, waves, st);
-    return pairs ? skinny_instance<T, 4, 2, 2>(p, aligned, waves, st) : skinny_instance<T, 4, 1, 2>(p, aligned, waves, st);
+    if (k.two) return k.pairs ? skinny_instance<T, 2, 2, 2>(p, aligned, k.waves, st) : skinny_instance<T, 2, 1, 2>(p, aligned, k.waves, st);
+    return k.steps > 2 ? skinny_instance<T, 1, 1, 4>(p, aligned, k.waves, st) : skinny_instance<T, 1, 1, 2>(p, aligned, k.waves, st);
+}
+
+template <typename T> hipError_t forward(const Product& p, void* ws, hipStream_t st) {
+    const SkinnyShape k = skinny_shape(p.rows, p.cols, p.K, (int)sizeof(T));
+    return k.fits ? skinny<T>(p, k, st) : product<T, false, false>(p, false, ws, st);
 }
 
 // ---- the backward pass's workspace: dz, the parts of dbias, the parts of dx or dw
@@ -922,8 +939,8 @@ bool matmul_supports(int M, int K, int N) {
 }
 
 size_t matmul_workspace(int M, int K, int N, int dtype) {
-    if (M <= kSkinnyRows) return 0;
-    return split_bytes(M, N, K, dtype == 0 ? 4 : 2);
+    const int es = dtype == 0 /* CONV2D_F32 */ ? 4 : 2;
+    return skinny_shape(M, N, K, es).fits ? 0 : split_bytes(M, N, K, es);
 }
 
 size_t matmul_bwd_workspace(int M, int K, int N, int dtype) {
@@ -934,9 +951,7 @@ hipError_t launch_matmul(const MatmulArgs& a, void* ws, hipStream_t st) {
     Product p = {};
     p.a = a.w; p.b = a.x; p.lda = a.ldw; p.ldb = a.ldx; p.rows = a.M; p.cols = a.N; p.K = a.K;
     p.bias = a.bias; p.residual = a.residual; p.z = a.z; p.y = a.y; p.ldr = a.ldr; p.ldz = a.ldz; p.ldy = a.ldy; p.act = a.act;
-    if (a.M <= kSkinnyRows) return a.dtype == 0 /* CONV2D_F32 */ ? skinny<float>(p, st) : skinny<bf16_t>(p, st);
-    return a.dtype == 0 /* CONV2D_F32 */ ? product<float, false, false>(p, false, ws, st)
-                                         : product<bf16_t, false, false>(p, false, ws, st);
+    return a.dtype == 0 /* CONV2D_F32 */ ? forward<float>(p, ws, st) : forward<bf16_t>(p, ws, st);
 }
 
 hipError_t launch_matmul_bwd(const MatmulBwdArgs& a, void* ws, hipStream_t st) {
