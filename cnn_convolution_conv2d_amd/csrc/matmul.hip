@@ -338,8 +338,20 @@ template <typename T, int B, int NT, bool STRIDED> struct Staged {
     static constexpr int N = B * 8 / NT, E = kPiece<T>, S = kStageK / (int)sizeof(T);
     static_assert(N * NT == B * 8, "pieces split evenly");
     uint4 v[N];
-    // indexes i0 .. of `count`, s from s0 to `send`
+    // indexes i0 .. of `count`, s from s0 to `send`.  A stage whose pieces are all whole
+    // is read without conditions, contiguous rows past the last being the last again
+    // (their results are not written).
     __device__ __forceinline__ void load(const T* p, long long ld, int i0, int count, int s0, int send) {
+        const bool whole = s0 + S <= send && (!STRIDED || i0 + B <= count);
+        if (whole) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                const int e = n * NT + threadIdx.x;
+                const int i = STRIDED ? i0 + e % (B / E) * E : min(i0 + e / 8, count - 1), s = s0 + (STRIDED ? e / (B / E) : e % 8 * E);
+                v[n] = load_bytes<16>(p + (STRIDED ? s * ld + i : i * ld + s));
+            }
+            return;
+        }
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             const int e = n * NT + threadIdx.x;
@@ -623,26 +635,33 @@ __global__ __launch_bounds__(1024) void matmul_skinny_kernel(Product p) {
     for (int g = 0; g < NG; ++g)
 #pragma unroll
         for (int t = 0; t < MT; ++t) acc[g][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    // 16 bytes of row r of an operand, 0 past its last row and past K
-    auto fetch = [&](const T* base, __amdgpu_buffer_rsrc_t rs, long long ld, int r, bool in, int s) __attribute__((always_inline)) {
+    // 16 bytes of row r of an operand, 0 past its last row and past K.  Unaligned ones
+    // that all end inside their rows (`whole`, the wave's) are plain loads, the rows past
+    // the last its own again (their results are not written).
+    auto fetch = [&](const T* base, __amdgpu_buffer_rsrc_t rs, long long ld, int r, int left, int s, bool whole) __attribute__((always_inline)) {
         Frag<T> f;
-        if constexpr (ALIGNED) f.v = __builtin_bit_cast(decltype(f.v), load16(rs, in && s < p.K ? (int)(r * ld + s) * ES : kOOB));
-        else f.v = __builtin_bit_cast(decltype(f.v), in && s < p.K ? load_piece<T>(base + r * ld + s, p.K - s) : make_uint4(0, 0, 0, 0));
+        if constexpr (ALIGNED) f.v = __builtin_bit_cast(decltype(f.v), load16(rs, r < left && s < p.K ? (int)(r * ld + s) * ES : kOOB));
+        else if (whole) f.v = __builtin_bit_cast(decltype(f.v), load_bytes<16>(base + min(r, left - 1) * ld + s));
+        else f.v = __builtin_bit_cast(decltype(f.v), r < left && s < p.K ? load_piece<T>(base + r * ld + s, p.K - s) : make_uint4(0, 0, 0, 0));
         return f;
     };
     const int stride = waves * S;
     for (int s0 = wave * S; s0 < p.K; s0 += stride * U) {
         Frag<T> a[U][2][NG], b[U][2][MT];
+        auto fetch_all = [&](bool whole) __attribute__((always_inline)) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int s = s0 + u * stride + h * (S / 2) + c * E;
+                for (int h = 0; h < 2; ++h) {
+                    const int s = s0 + u * stride + h * (S / 2) + c * E;
 #pragma unroll
-                for (int g = 0; g < NG; ++g) a[u][h][g] = fetch(pa, ra, p.lda, g * 16 + row, n0 + g * 16 + row < p.cols, s);
+                    for (int g = 0; g < NG; ++g) a[u][h][g] = fetch(pa, ra, p.lda, g * 16 + row, p.cols - n0, s, whole);
 #pragma unroll
-                for (int t = 0; t < MT; ++t) b[u][h][t] = fetch(pb, rb, p.ldb, t * 16 + row, t * 16 + row < p.rows, s);
-            }
+                    for (int t = 0; t < MT; ++t) b[u][h][t] = fetch(pb, rb, p.ldb, t * 16 + row, p.rows, s, whole);
+                }
+        };
+        if (!ALIGNED && s0 + (U - 1) * stride + S <= p.K) fetch_all(true);
+        else fetch_all(false);
         __builtin_amdgcn_sched_barrier(0);   // or the compiler sinks loads below products, to save registers
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -669,6 +688,30 @@ __global__ __launch_bounds__(1024) void matmul_skinny_kernel(Product p) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[k] = sum[k] + bias[k];
         finish<T, 4>(p, m, n, v);
+    }
+}
+
+// ------------------------------------------------------------------ whole pieces
+
+// Copies of two matrices [rows][K] whose rows are whole 16-byte pieces, zeros past K.
+template <typename T> struct Packed {
+    const T* from;
+    T* to;
+    long long ld, rows;
+};
+
+template <typename T>
+__global__ __launch_bounds__(256) void matmul_pack_kernel(Packed<T> a, Packed<T> b, int K) {
+    constexpr int E = kPiece<T>;
+    const int pieces = (K + E - 1) / E;
+    const long long na = a.rows * pieces, all = na + b.rows * pieces, step = (long long)gridDim.x * 256;
+#pragma unroll 2
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < all; i += step) {
+        const bool first = i < na;
+        const long long k = first ? i : i - na, r = k / pieces;
+        const int c = (int)(k - r * pieces) * E;
+        const T* const from = first ? a.from + r * a.ld + c : b.from + r * b.ld + c;
+        *reinterpret_cast<uint4*>((first ? a.to : b.to) + k * E) = load_piece<T>(from, K - c);
     }
 }
 
@@ -769,6 +812,26 @@ size_t split_bytes(int rows, int cols, int K, int es) {
     return splits > 1 ? (size_t)splits * rows * cols * 4 : 0;
 }
 
+size_t round256(size_t v) { return (v + 255) / 256 * 256; }
+
+// Elements of a row in whole 16-byte pieces.
+int whole_pieces(int n, int es) { return (n + 16 / es - 1) / (16 / es) * (16 / es); }
+
+// Whether a product is large enough for copies of its operands with whole pieces: the
+// tiles of aligned operands then save more than the copies take (bf16 with copies and
+// without: 4096 x 4095 -> 4096 148 and 230 us, 2048 x 2047 -> 2048 38 and 47, gradients of
+// 4096 x 1001 -> 2001 91 and 201; fp32 is bound by its products sooner).
+bool worth_copies(int M, int K, int N, int es) { return (double)M * N * K * (es == 4 ? 8 : 1) >= 0x1p32; }
+
+// Whether rows of K elements are copied.
+bool packs(int M, int K, int N, int es) { return (long long)K * es % 16 != 0 && worth_copies(M, K, N, es); }
+
+template <typename T> hipError_t pack(const Packed<T>& a, const Packed<T>& b, int K, hipStream_t st) {
+    const long long pieces = (a.rows + b.rows) * (whole_pieces(K, (int)sizeof(T)) / kPiece<T>), blocks = (pieces + 255) / 256;
+    matmul_pack_kernel<T><<<(unsigned)(blocks < 8 * kUnits ? blocks : 8 * kUnits), 256, 0, st>>>(a, b, K);
+    return hipGetLastError();
+}
+
 // Whole 16-byte pieces at aligned addresses; along s too where it is contiguous
 // (`padded`: with zeros, up to a whole piece).
 bool aligned_operand(const void* p, long long ld, int K, int es, bool strided, bool padded) {
@@ -790,10 +853,10 @@ hipError_t tiled(const Product& p, const Plan& q, bool aligned, float* sums, hip
     return hipGetLastError();
 }
 
-// `padded`: the rows of b end in zeros, up to a whole piece.
+// `padded`: contiguous rows end in zeros, up to a whole piece.
 template <typename T, bool TA, bool TB> hipError_t product(const Product& p, bool padded, void* ws, hipStream_t st) {
     constexpr int ES = (int)sizeof(T);
-    const bool aligned = aligned_operand(p.a, p.lda, p.K, ES, TA, false) && aligned_operand(p.b, p.ldb, p.K, ES, TB, padded);
+    const bool aligned = aligned_operand(p.a, p.lda, p.K, ES, TA, padded) && aligned_operand(p.b, p.ldb, p.K, ES, TB, padded);
     const Plan q = make_plan(p.rows, p.cols, p.K, ES, aligned);
     float* const sums = static_cast<float*>(ws);
     if (q.splits == 1) return tiled<T, TA, TB, TA ? kPlain : kEpilogue>(p, q, aligned, nullptr, st);
@@ -835,9 +898,8 @@ SkinnyShape skinny_shape(int rows, int cols, int K, int es) {
 template <typename T, int MT, int NG, int U> hipError_t skinny_instance(const Product& p, bool aligned, int waves, hipStream_t st) {
     const unsigned blocks = (unsigned)(((long long)p.cols + NG * 16 - 1) / (NG * 16));
     const int lds = waves * NG * MT * 1024;
-    // any alignment: pieces that end with their row take registers, so fewer at a time
     if (aligned) matmul_skinny_kernel<T, MT, NG, U, true><<<blocks, waves * 64, lds, st>>>(p);
-    else matmul_skinny_kernel<T, MT, NG, (MT * NG > 1 ? 1 : U), false><<<blocks, waves * 64, lds, st>>>(p);
+    else matmul_skinny_kernel<T, MT, NG, U, false><<<blocks, waves * 64, lds, st>>>(p);
     return hipGetLastError();
 }
 
@@ -848,15 +910,31 @@ template <typename T> hipError_t skinny(const Product& p, const SkinnyShape& k, 
     return k.steps > 2 ? skinny_instance<T, 1, 1, 4>(p, aligned, k.waves, st) : skinny_instance<T, 1, 1, 2>(p, aligned, k.waves, st);
 }
 
-template <typename T> hipError_t forward(const Product& p, void* ws, hipStream_t st) {
-    const SkinnyShape k = skinny_shape(p.rows, p.cols, p.K, (int)sizeof(T));
-    return k.fits ? skinny<T>(p, k, st) : product<T, false, false>(p, false, ws, st);
+template <typename T> size_t forward_workspace(int M, int K, int N) {
+    constexpr int ES = (int)sizeof(T);
+    if (skinny_shape(M, N, K, ES).fits) return 0;
+    const size_t parts = split_bytes(M, N, K, ES);
+    return packs(M, K, N, ES) ? round256(parts) + ((size_t)M + N) * whole_pieces(K, ES) * ES : parts;
 }
 
-// ---- the backward pass's workspace: dz, the parts of dbias, the parts of dx or dw
+template <typename T> hipError_t forward(Product p, char* ws, hipStream_t st) {
+    constexpr int ES = (int)sizeof(T);
+    const SkinnyShape k = skinny_shape(p.rows, p.cols, p.K, ES);
+    if (k.fits) return skinny<T>(p, k, st);
+    if (!packs(p.rows, p.K, p.cols, ES)) return product<T, false, false>(p, false, ws, st);
+    const int ld = whole_pieces(p.K, ES);
+    T* const a = reinterpret_cast<T*>(ws + round256(split_bytes(p.rows, p.cols, p.K, ES)));
+    T* const b = a + (size_t)p.cols * ld;
+    const hipError_t e = pack<T>({static_cast<const T*>(p.a), a, p.lda, p.cols}, {static_cast<const T*>(p.b), b, p.ldb, p.rows}, p.K, st);
+    if (e != hipSuccess) return e;
+    p.a = a;
+    p.b = b;
+    p.lda = p.ldb = ld;
+    return product<T, false, false>(p, true, ws, st);
+}
 
-// Rows of dz are whole 16-byte pieces.
-template <typename T> int dz_stride(int N) { return (N + kPiece<T> - 1) / kPiece<T> * kPiece<T>; }
+// ---- the backward pass's workspace: dz, the parts of dbias, the parts of dx or dw, and
+// x and w in whole pieces
 
 struct DzShape {
     int lanes, chunk, cols, chunks;
@@ -880,30 +958,35 @@ DzShape dz_shape(int M, int N, int es) {
     return d;
 }
 
-size_t round256(size_t v) { return (v + 255) / 256 * 256; }
-
 struct BwdSpace {
-    size_t dz, sums, parts;   // offsets; the end
+    size_t dz, sums, parts, x, w;   // offsets; the end
     size_t end;
 };
 
 template <typename T> BwdSpace bwd_space(int M, int K, int N) {
-    const DzShape d = dz_shape(M, N, (int)sizeof(T));
+    constexpr int ES = (int)sizeof(T);
+    const DzShape d = dz_shape(M, N, ES);
     BwdSpace b;
     b.dz = 0;
-    b.sums = round256((size_t)M * dz_stride<T>(N) * sizeof(T));
+    b.sums = round256((size_t)M * whole_pieces(N, ES) * ES);
     b.parts = b.sums + round256((size_t)d.chunks * N * 4);
-    const size_t u = split_bytes(M, K, N, (int)sizeof(T)), v = split_bytes(N, K, M, (int)sizeof(T));
-    b.end = b.parts + (u > v ? u : v);
+    const size_t u = split_bytes(M, K, N, ES), v = split_bytes(N, K, M, ES);
+    const size_t row = packs(M, K, N, ES) ? (size_t)whole_pieces(K, ES) * ES : 0;
+    b.x = b.parts + round256(u > v ? u : v);
+    b.w = b.x + round256(M * row);
+    b.end = b.w + N * row;
     return b;
 }
 
 template <typename T> hipError_t gradients(const MatmulBwdArgs& a, char* ws, hipStream_t st) {
+    constexpr int ES = (int)sizeof(T);
     const BwdSpace b = bwd_space<T>(a.M, a.K, a.N);
-    const DzShape d = dz_shape(a.M, a.N, (int)sizeof(T));
-    const int ldd = dz_stride<T>(a.N);
+    const DzShape d = dz_shape(a.M, a.N, ES);
+    const int ldd = whole_pieces(a.N, ES), ldk = whole_pieces(a.K, ES);
     const bool products = a.dx || a.dw;
-    T* const dz = a.z && products ? reinterpret_cast<T*>(ws + b.dz) : nullptr;
+    // without an activation dz is dy, read where it lies if it has whole pieces
+    const bool copy = a.z || (!aligned_operand(a.dy, a.lddy, a.N, ES, false, false) && worth_copies(a.M, a.K, a.N, ES));
+    T* const dz = copy && products ? reinterpret_cast<T*>(ws + b.dz) : nullptr;
     float* const sums = a.dbias ? reinterpret_cast<float*>(ws + b.sums) : nullptr;
     hipError_t e = hipSuccess;
     if (dz || sums) {
@@ -914,16 +997,28 @@ template <typename T> hipError_t gradients(const MatmulBwdArgs& a, char* ws, hip
         if (e == hipSuccess && sums) e = launch_join_columns(sums, a.dbias, d.chunks, a.N, st);
         if (e != hipSuccess) return e;
     }
+    const T* x = static_cast<const T*>(a.x);
+    const T* w = static_cast<const T*>(a.w);
+    long long ldx = a.ldx, ldw = a.ldw;
+    if (products && packs(a.M, a.K, a.N, ES)) {
+        T* const px = reinterpret_cast<T*>(ws + b.x);
+        T* const pw = reinterpret_cast<T*>(ws + b.w);
+        e = pack<T>({x, px, ldx, a.dw ? a.M : 0}, {w, pw, ldw, a.dx ? a.N : 0}, a.K, st);
+        if (e != hipSuccess) return e;
+        x = px;
+        w = pw;
+        ldx = ldw = ldk;
+    }
     Product p = {};
     p.b = dz ? dz : a.dy;
     p.ldb = dz ? ldd : a.lddy;
     if (a.dx) {
-        p.a = a.w; p.lda = a.ldw; p.rows = a.M; p.cols = a.K; p.K = a.N; p.y = a.dx; p.ldy = a.lddx;
+        p.a = w; p.lda = ldw; p.rows = a.M; p.cols = a.K; p.K = a.N; p.y = a.dx; p.ldy = a.lddx;
         e = product<T, true, false>(p, dz, ws + b.parts, st);
         if (e != hipSuccess) return e;
     }
     if (a.dw) {
-        p.a = a.x; p.lda = a.ldx; p.rows = a.N; p.cols = a.K; p.K = a.M; p.y = a.dw; p.ldy = a.lddw;
+        p.a = x; p.lda = ldx; p.rows = a.N; p.cols = a.K; p.K = a.M; p.y = a.dw; p.ldy = a.lddw;
         e = product<T, true, true>(p, dz, ws + b.parts, st);
     }
     return e;
@@ -939,8 +1034,7 @@ bool matmul_supports(int M, int K, int N) {
 }
 
 size_t matmul_workspace(int M, int K, int N, int dtype) {
-    const int es = dtype == 0 /* CONV2D_F32 */ ? 4 : 2;
-    return skinny_shape(M, N, K, es).fits ? 0 : split_bytes(M, N, K, es);
+    return dtype == 0 /* CONV2D_F32 */ ? forward_workspace<float>(M, K, N) : forward_workspace<bf16_t>(M, K, N);
 }
 
 size_t matmul_bwd_workspace(int M, int K, int N, int dtype) {
@@ -951,7 +1045,8 @@ hipError_t launch_matmul(const MatmulArgs& a, void* ws, hipStream_t st) {
     Product p = {};
     p.a = a.w; p.b = a.x; p.lda = a.ldw; p.ldb = a.ldx; p.rows = a.M; p.cols = a.N; p.K = a.K;
     p.bias = a.bias; p.residual = a.residual; p.z = a.z; p.y = a.y; p.ldr = a.ldr; p.ldz = a.ldz; p.ldy = a.ldy; p.act = a.act;
-    return a.dtype == 0 /* CONV2D_F32 */ ? forward<float>(p, ws, st) : forward<bf16_t>(p, ws, st);
+    char* const space = static_cast<char*>(ws);
+    return a.dtype == 0 /* CONV2D_F32 */ ? forward<float>(p, space, st) : forward<bf16_t>(p, space, st);
 }
 
 hipError_t launch_matmul_bwd(const MatmulBwdArgs& a, void* ws, hipStream_t st) {

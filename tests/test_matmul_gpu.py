@@ -124,6 +124,18 @@ def test_large_tiles(M, K, N):
     run_forward(M, K, N, "bf16", act=2)
 
 
+# rows of no whole number of 16-byte pieces, large enough to be copied first
+@pytest.mark.parametrize("M,K,N,dtype", [(2051, 1037, 2100, "bf16"), (2049, 2047, 1030, "bf16"), (801, 1001, 700, "f32")])
+def test_copied_operands(M, K, N, dtype):
+    run_forward(M, K, N, dtype, act=2)
+    run_forward(M, K, N, dtype, ints=True, act=1, padx=3, padw=1, pad=2, skip=1)
+    run_backward(M, K, N, dtype, act=2)
+    run_backward(M, K, N, dtype, act=0, ints=True, padx=3, padw=1, pad=2, skip=1)
+    run_backward(M, K, N + 1, dtype, act=0, ints=True)
+    run_backward(M, K, N, dtype, act=1, ints=True, want=("dx",))
+    run_backward(M, K, N, dtype, act=1, ints=True, want=("dw", "db"))
+
+
 @pytest.mark.parametrize("M", [1, 50, 300])
 def test_y_over_the_residual(M):
     for dtype in ("bf16", "f32"):
