@@ -320,12 +320,22 @@ __device__ __forceinline__ void write_results(const Product& p, f32x4 (&acc)[TI]
 
 // ------------------------------------------------------------------ operands of any alignment
 
-// E elements from p on, of which `left` exist (the others: 0).
-template <typename T> __device__ __forceinline__ uint4 load_piece(const T* p, long long left) {
-    if (left >= kPiece<T>) return load_bytes<16>(p);
+// 16 bytes of a row of `row` elements from p on, of which `left` > 0 exist (the others:
+// 0).  The end of a row is read with what stands before it and shifted into place, so
+// that no lane takes a path of its own.
+template <typename T> __device__ __forceinline__ uint4 load_piece(const T* p, int left, int row) {
+    constexpr int E = kPiece<T>;
+    if (row >= E) {
+        const int before = max(E - left, 0), bits = before * (int)sizeof(T) * 8;
+        const uint4 v = load_bytes<16>(p - before);
+        const uint64_t lo = (uint64_t)v.y << 32 | v.x, hi = (uint64_t)v.w << 32 | v.z;
+        const uint64_t l = bits >= 64 ? hi >> (bits - 64) : bits ? lo >> bits | hi << (64 - bits) : lo;
+        const uint64_t h = bits >= 64 ? 0 : hi >> bits;
+        return make_uint4((uint32_t)l, (uint32_t)(l >> 32), (uint32_t)h, (uint32_t)(h >> 32));
+    }
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int e = 0; e < kPiece<T>; ++e)
+    for (int e = 0; e < E; ++e)
         if (e < left) {
             if constexpr (sizeof(T) == 4) w[e] = __builtin_bit_cast(uint32_t, p[e]);
             else w[e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
@@ -338,10 +348,10 @@ template <typename T, int B, int NT, bool STRIDED> struct Staged {
     static constexpr int N = B * 8 / NT, E = kPiece<T>, S = kStageK / (int)sizeof(T);
     static_assert(N * NT == B * 8, "pieces split evenly");
     uint4 v[N];
-    // indexes i0 .. of `count`, s from s0 to `send`.  A stage whose pieces are all whole
+    // indexes i0 .. of `count`, s from s0 to `send`, rows of `row` elements.  A stage whose pieces are all whole
     // is read without conditions, contiguous rows past the last being the last again
     // (their results are not written).
-    __device__ __forceinline__ void load(const T* p, long long ld, int i0, int count, int s0, int send) {
+    __device__ __forceinline__ void load(const T* p, long long ld, int i0, int count, int s0, int send, int row) {
         const bool whole = s0 + S <= send && (!STRIDED || i0 + B <= count);
         if (whole) {
 #pragma unroll
@@ -356,8 +366,8 @@ template <typename T, int B, int NT, bool STRIDED> struct Staged {
         for (int n = 0; n < N; ++n) {
             const int e = n * NT + threadIdx.x;
             const int i = i0 + (STRIDED ? e % (B / E) * E : e / 8), s = s0 + (STRIDED ? e / (B / E) : e % 8 * E);
-            const long long left = i < count && s < send ? (STRIDED ? count - i : send - s) : 0;
-            v[n] = left > 0 ? load_piece<T>(p + (STRIDED ? s * ld + i : i * ld + s), left) : make_uint4(0, 0, 0, 0);
+            const bool in = i < count && s < send;
+            v[n] = in ? load_piece<T>(p + (STRIDED ? s * ld + i : i * ld + s), STRIDED ? count - i : send - s, row) : make_uint4(0, 0, 0, 0);
         }
     }
     __device__ __forceinline__ void store(char* stage) const {
@@ -389,8 +399,8 @@ __global__ __launch_bounds__(WM * WN * 64) void matmul_staged_kernel(Product p, 
     Staged<T, BN, NT, TA> a;
     Staged<T, BM, NT, TB> b;
     auto load = [&](int s) __attribute__((always_inline)) {
-        a.load(static_cast<const T*>(p.a), p.lda, t.n0, p.cols, s, send);
-        b.load(static_cast<const T*>(p.b), p.ldb, t.m0, p.rows, s, send);
+        a.load(static_cast<const T*>(p.a), p.lda, t.n0, p.cols, s, send, TA ? p.cols : p.K);
+        b.load(static_cast<const T*>(p.b), p.ldb, t.m0, p.rows, s, send, TB ? p.rows : p.K);
     };
     load(s0);
     for (int s = s0; s < send; s += S) {
@@ -642,7 +652,7 @@ __global__ __launch_bounds__(1024) void matmul_skinny_kernel(Product p) {
         Frag<T> f;
         if constexpr (ALIGNED) f.v = __builtin_bit_cast(decltype(f.v), load16(rs, r < left && s < p.K ? (int)(r * ld + s) * ES : kOOB));
         else if (whole) f.v = __builtin_bit_cast(decltype(f.v), load_bytes<16>(base + min(r, left - 1) * ld + s));
-        else f.v = __builtin_bit_cast(decltype(f.v), r < left && s < p.K ? load_piece<T>(base + r * ld + s, p.K - s) : make_uint4(0, 0, 0, 0));
+        else f.v = __builtin_bit_cast(decltype(f.v), r < left && s < p.K ? load_piece<T>(base + r * ld + s, p.K - s, p.K) : make_uint4(0, 0, 0, 0));
         return f;
     };
     const int stride = waves * S;
@@ -711,7 +721,7 @@ __global__ __launch_bounds__(256) void matmul_pack_kernel(Packed<T> a, Packed<T>
         const long long k = first ? i : i - na, r = k / pieces;
         const int c = (int)(k - r * pieces) * E;
         const T* const from = first ? a.from + r * a.ld + c : b.from + r * b.ld + c;
-        *reinterpret_cast<uint4*>((first ? a.to : b.to) + k * E) = load_piece<T>(from, K - c);
+        *reinterpret_cast<uint4*>((first ? a.to : b.to) + k * E) = load_piece<T>(from, K - c, K);
     }
 }
 
@@ -740,6 +750,7 @@ __global__ __launch_bounds__(256) void matmul_dz_kernel(MatmulBwdArgs a, T* dz, 
     };
     const T* const py = static_cast<const T*>(a.dy) + c;
     const T* const pz = static_cast<const T*>(a.z) + (ACT ? c : 0);
+    typedef typename Vec<T, V>::raw raw;
     if (c + V <= a.N) {
 #pragma unroll 4
         for (long long m = m0 + group; m < m1; m += groups) {
@@ -749,10 +760,11 @@ __global__ __launch_bounds__(256) void matmul_dz_kernel(MatmulBwdArgs a, T* dz, 
             row(m, v, z);
         }
     } else if (c < a.N) {
+#pragma unroll 2
         for (long long m = m0 + group; m < m1; m += groups) {
             float v[V], z[V];
-            Vec<T, V>::unpack(__builtin_bit_cast(typename Vec<T, V>::raw, load_piece<T>(py + m * a.lddy, a.N - c)), v);
-            if constexpr (ACT) Vec<T, V>::unpack(__builtin_bit_cast(typename Vec<T, V>::raw, load_piece<T>(pz + m * a.ldz, a.N - c)), z);
+            Vec<T, V>::unpack(__builtin_bit_cast(raw, load_piece<T>(py + m * a.lddy, a.N - c, a.N)), v);
+            if constexpr (ACT) Vec<T, V>::unpack(__builtin_bit_cast(raw, load_piece<T>(pz + m * a.ldz, a.N - c, a.N)), z);
             row(m, v, z);
         }
     }
