@@ -903,7 +903,8 @@ SkinnyShape skinny_shape(int rows, int cols, int K, int es) {
     k.waves = 4;
     while (k.waves < 16 && (long long)blocks * k.waves < 16 * kUnits && k.waves * 2 * kStageK <= bytes) k.waves *= 2;
     k.steps = (bytes + k.waves * kStageK - 1) / (k.waves * kStageK);
-    k.fits = rows <= 32 && !(blocks <= (rows > 8 ? 128 : 64) && k.steps >= (k.two ? 4 : 8));
+    // (a launch counts its threads in 32 bits)
+    k.fits = rows <= 32 && cols <= 1 << 27 && !(blocks <= (rows > 8 ? 128 : 64) && k.steps >= (k.two ? 4 : 8));
     return k;
 }
 

@@ -124,7 +124,7 @@ hipError_t launch_rms_norm(const RmsArgs& a, hipStream_t st);
 hipError_t launch_rms_norm_quant(const RmsArgs& a, hipStream_t st);
 hipError_t launch_rms_norm_bwd(const RmsArgs& a, void* ws, hipStream_t st);
 
-// out[c] = sum of sums[i][c] over i < count, in fp64, in a fixed order.
+// out[c] = sum of sums[i][c] over i < count, in fp64, in a fixed order; C up to 2^20.
 hipError_t launch_join_columns(const float* sums, float* out, int count, int C, hipStream_t st);
 
 // Products with an epilogue and their gradients; strides of what they read up to kMatmulMostLd.

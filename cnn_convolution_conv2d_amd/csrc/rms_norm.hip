@@ -277,7 +277,7 @@ __global__ __launch_bounds__(NT) void rms_norm_bwd_kernel(RmsArgs a, int lanes, 
 // column (with 16 of them, 777 sums of 1001 columns take 6.5 us; with 64 3.5).
 __global__ __launch_bounds__(1024) void join_columns_kernel(const float* sums, float* out, int count, int C) {
     __shared__ double part[16][65];
-    const int column = threadIdx.x % 16, c = blockIdx.x * 16 + column, k = threadIdx.x / 16;
+    const int first = blockIdx.x * 16, column = threadIdx.x % 16, c = first + column, k = threadIdx.x / 16;
     double s = 0.0;
     if (c < C) {
 #pragma unroll 8
@@ -287,7 +287,7 @@ __global__ __launch_bounds__(1024) void join_columns_kernel(const float* sums, f
     __syncthreads();
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;   // a wave adds a column
     const double t = lanes_sum(part[wave][lane], 64);
-    if (lane == 0 && blockIdx.x * 16 + wave < C) out[blockIdx.x * 16 + wave] = (float)t;
+    if (lane == 0 && first + wave < C) out[first + wave] = (float)t;
 }
 
 // ------------------------------------------------------------------ host
@@ -382,7 +382,7 @@ template <Pass P> hipError_t launch(const RmsArgs& a, float* sums, hipStream_t s
 }  // namespace
 
 hipError_t launch_join_columns(const float* sums, float* out, int count, int C, hipStream_t st) {
-    join_columns_kernel<<<(unsigned)(((long long)C + 15) / 16), 1024, 0, st>>>(sums, out, count, C);
+    join_columns_kernel<<<(C + 15) / 16, 1024, 0, st>>>(sums, out, count, C);
     return hipGetLastError();
 }
 

@@ -319,3 +319,14 @@ def test_offsets_past_32_bits():
     x.view(M, ld)[:, :N].copy_(dy)
     c2.conv2d_matmul_bwd(x, None, dx, w, y_dx := torch.empty_like(dx), None, None, ws, n, M, K, N, ld, 0, K, K, K, 0, c2.BF16, 0)
     np.testing.assert_array_equal(y_dx.double().cpu().numpy(), bf(gh @ wh))
+
+
+def test_many_columns():
+    """More columns than a launch of workgroups of 16 each has threads for."""
+    N = (1 << 28) + 5
+    w = torch.empty(N, dtype=torch.bfloat16, device="cuda").random_(-3, 4)
+    x = torch.full((1, 1), 2.0, dtype=torch.bfloat16, device="cuda")
+    y = torch.empty(N, dtype=torch.bfloat16, device="cuda")
+    n = c2.conv2d_matmul_workspace_bytes(1, 1, N, c2.BF16)
+    c2.conv2d_matmul(x, w, None, None, None, y, workspace(n), n, 1, 1, N, 1, 1, 0, 0, N, c2.BF16, 0)
+    assert torch.equal(y, 2 * w)

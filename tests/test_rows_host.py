@@ -151,6 +151,31 @@ def test_the_binding_passes_every_argument():
         assert e.value.code == code
 
 
+def test_the_calls_work_without_the_extension(tmp_path, monkeypatch):
+    """As the package loads where no extension is built for this Python: through ctypes, the same codes."""
+    import importlib.util
+    import os
+    import shutil
+    shutil.copy(os.path.join(os.path.dirname(c2.__file__), "__init__.py"), tmp_path)
+    monkeypatch.setenv("CONV2D_LIBRARY", c2.LIB_PATH)
+    spec = importlib.util.spec_from_file_location("without_extension", tmp_path / "__init__.py")
+    w = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(w)
+    for mod in (c2, w):
+        codes = []
+        for call in (lambda: mod.conv2d_rms_norm(P, None, None, None, S, None, 1, 4, 4, 4, 4, 4, -1.0, c2.F32, stream=0),
+                     lambda: mod.conv2d_rms_norm_quant(P, None, None, None, P, Q, None, 1, 4, 4, 4, 4, 4, 1e-5, c2.F32, stream=0),
+                     lambda: mod.conv2d_rms_norm_bwd(P, None, Q, None, P, S, P, None, 0, 1, 4, 4, 4, 4, 4, 9, stream=0),
+                     lambda: mod.conv2d_matmul(P, Q, None, None, None, None, None, 0, 1, 1, 1, 1, 1, 1, 1, 1, c2.F32, 0, stream=0),
+                     lambda: mod.conv2d_matmul_bwd(P, None, P, Q, S, None, None, None, 0, 1, 1, 1, 1, 1, 1, 1, 1, 1, c2.F32, 1,
+                                                   stream=0),
+                     lambda: mod.conv2d_dropout(P, None, S, Q, 1.5, 1, 1, 1, 1, 1, c2.F32, stream=0)):
+            with pytest.raises(mod.Conv2dError) as e:
+                call()
+            codes.append(e.value.code)
+        assert codes == [c2.ERR_ARG, c2.ERR_ARG, c2.ERR_DTYPE, c2.ERR_NULL, c2.ERR_NULL, c2.ERR_ARG]
+
+
 def test_workspace_sizes():
     assert c2.conv2d_rms_norm_bwd_workspace_bytes(0, 8) == 0
     assert c2.conv2d_rms_norm_bwd_workspace_bytes(8, 16385) == 0
