@@ -72,10 +72,18 @@ __global__ __launch_bounds__(256) void dropout_kernel(DropoutArgs a, int vecs, l
             drop<T, V>(v, rv, c, (int)row, seed, offset, a.threshold, a.scale);
             Vec<T, V>::store(y, v);
         } else {
+            // a row's end: shifted into place where that saves loads (65536 x 1004 bf16: 100
+            // us, element by element 110; 65536 x 1001 fp32: 176 and 158)
+            if constexpr (V > 4) {
+                typedef typename Vec<T, V>::raw raw;
+                Vec<T, V>::unpack(__builtin_bit_cast(raw, load_piece<T>(x, a.C - c, a.C)), v);
+                if constexpr (RES) Vec<T, V>::unpack(__builtin_bit_cast(raw, load_piece<T>(r, a.C - c, a.C)), rv);
+            } else {
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                v[e] = c + e < a.C ? load_f32<T>(x, e) : 0.0f;
-                if constexpr (RES) rv[e] = c + e < a.C ? load_f32<T>(r, e) : 0.0f;
+                for (int e = 0; e < V; ++e) {
+                    v[e] = c + e < a.C ? load_f32<T>(x, e) : 0.0f;
+                    if constexpr (RES) rv[e] = c + e < a.C ? load_f32<T>(r, e) : 0.0f;
+                }
             }
             drop<T, V>(v, rv, c, (int)row, seed, offset, a.threshold, a.scale);
 #pragma unroll

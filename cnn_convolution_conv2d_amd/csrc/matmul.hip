@@ -89,8 +89,6 @@ struct Product {
     int act;
 };
 
-template <typename T> constexpr int kPiece = 16 / (int)sizeof(T);   // elements of 16 bytes
-
 // ------------------------------------------------------------------ fragments
 
 // A lane's 16 bytes of s of one row of a 16x16 block.
@@ -319,29 +317,6 @@ __device__ __forceinline__ void write_results(const Product& p, f32x4 (&acc)[TI]
 }
 
 // ------------------------------------------------------------------ operands of any alignment
-
-// 16 bytes of a row of `row` elements from p on, of which `left` > 0 exist (the others:
-// 0).  The end of a row is read with what stands before it and shifted into place, so
-// that no lane takes a path of its own.
-template <typename T> __device__ __forceinline__ uint4 load_piece(const T* p, int left, int row) {
-    constexpr int E = kPiece<T>;
-    if (row >= E) {
-        const int before = max(E - left, 0), bits = before * (int)sizeof(T) * 8;
-        const uint4 v = load_bytes<16>(p - before);
-        const uint64_t lo = (uint64_t)v.y << 32 | v.x, hi = (uint64_t)v.w << 32 | v.z;
-        const uint64_t l = bits >= 64 ? hi >> (bits - 64) : bits ? lo >> bits | hi << (64 - bits) : lo;
-        const uint64_t h = bits >= 64 ? 0 : hi >> bits;
-        return make_uint4((uint32_t)l, (uint32_t)(l >> 32), (uint32_t)h, (uint32_t)(h >> 32));
-    }
-    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        if (e < left) {
-            if constexpr (sizeof(T) == 4) w[e] = __builtin_bit_cast(uint32_t, p[e]);
-            else w[e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
-        }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
 
 // A thread's pieces of an operand's stage: in registers, then in LDS.
 template <typename T, int B, int NT, bool STRIDED> struct Staged {
@@ -794,10 +769,12 @@ struct Plan {
 // is short (16384 x 1024 -> 4096 bf16 with a residual 185 us against 192, x 128 93
 // against 116; but 16384 x 2048 -> 1024 78 against 70).
 //
-// Few tiles are split along s until every compute unit has two.  A part of 128 is at
-// least 16 stages long: 256 x 4096 -> 4096 takes 27 us in 8 parts of 128 and 46 in tiles
-// of 64, but 2048 x 1024 -> 1024 18 in parts of 8 stages and 11 in tiles of 64.  A part of
-// 64 is at least 4 (dw of 100352 x 256 -> 64: 22.7 us with two a unit, 27.7 with one).
+// Few tiles are split along s until every compute unit has two, three of 64 where a
+// part is still 16 stages long.  A part of 128 is at least 16 stages: 256 x 4096 -> 4096
+// takes 27 us in 8 parts of 128 and 46 in tiles of 64, but 2048 x 1024 -> 1024 18 in parts
+// of 8 stages and 11 in tiles of 64.  A part of 64 is at least 4 (dw of 100352 x 256 -> 64:
+// 22.7 us with two a unit, 27.7 with one; 64 x 4096 -> 16384: 52 us with one, 41 with two,
+// 36 with three; but 1024 x 512 -> 1024, one a unit already, 6.9 whole and 11.2 in two).
 constexpr int kLongBytes = 2048;
 
 Plan make_plan(int rows, int cols, int K, int es, bool aligned) {
@@ -809,9 +786,11 @@ Plan make_plan(int rows, int cols, int K, int es, bool aligned) {
     p.b = large ? 256 : cols > 64 && rows > 64 && tiles(128) * parts(16) >= kUnits ? 128 : 64;
     p.tm = (rows + p.b - 1) / p.b;
     p.tn = (cols + p.b - 1) / p.b;
-    const long long t = (long long)p.tm * p.tn, want = t >= kUnits ? 1 : 2 * kUnits / t;
-    const int most = parts(p.b == 64 ? 4 : 16);
-    p.splits = (int)(want < most ? want : most);
+    const long long t = (long long)p.tm * p.tn;
+    auto split = [&](int units, int stages) { return (int)(units / t < parts(stages) ? units / t : parts(stages)); };
+    p.splits = 1;
+    if (t < kUnits) p.splits = split(2 * kUnits, p.b == 64 ? 4 : 16);
+    if (p.b == 64 && split(3 * kUnits, 16) > p.splits) p.splits = split(3 * kUnits, 16);
     p.stages = (all + p.splits - 1) / p.splits;
     p.splits = (all + p.stages - 1) / p.stages;
     return p;

@@ -1,5 +1,5 @@
-// rowvec.hpp -- device helpers shared by the group-norm and the int8 kernels:
-// vector loads of V fp32 or bf16 elements, the activations and the
+// rowvec.hpp -- device helpers shared by the norms, the products and dropout: vector
+// loads of V fp32 or bf16 elements, the activations, sums over lanes and the
 // quantisation of a row to 8 bits.
 #pragma once
 
@@ -80,6 +80,31 @@ template <int V> struct Vec<bf16_t, V> {
     }
     static __device__ __forceinline__ void store(bf16_t* p, const float (&v)[V]) { store_bytes<2 * V>(p, pack(v)); }
 };
+
+template <typename T> constexpr int kPiece = 16 / (int)sizeof(T);   // elements of 16 bytes
+
+// 16 bytes of a row of `row` elements from p on, of which `left` > 0 exist (the others:
+// 0).  The end of a row is read with what stands before it and shifted into place, so
+// that no lane takes a path of its own.
+template <typename T> __device__ __forceinline__ uint4 load_piece(const T* p, int left, int row) {
+    constexpr int E = kPiece<T>;
+    if (row >= E) {
+        const int before = max(E - left, 0), bits = before * (int)sizeof(T) * 8;
+        const uint4 v = load_bytes<16>(p - before);
+        const uint64_t lo = (uint64_t)v.y << 32 | v.x, hi = (uint64_t)v.w << 32 | v.z;
+        const uint64_t l = bits >= 64 ? hi >> (bits - 64) : bits ? lo >> bits | hi << (64 - bits) : lo;
+        const uint64_t h = bits >= 64 ? 0 : hi >> bits;
+        return make_uint4((uint32_t)l, (uint32_t)(l >> 32), (uint32_t)h, (uint32_t)(h >> 32));
+    }
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        if (e < left) {
+            if constexpr (sizeof(T) == 4) w[e] = __builtin_bit_cast(uint32_t, p[e]);
+            else w[e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
+        }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
 
 // 1 / (1 + exp(-z)) from the hardware's exp2 and reciprocal (1 ulp each).
 __device__ __forceinline__ float sigmoid(float z) {
