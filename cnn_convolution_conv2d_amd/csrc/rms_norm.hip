@@ -273,21 +273,24 @@ __global__ __launch_bounds__(NT) void rms_norm_bwd_kernel(RmsArgs a, int lanes, 
     }
 }
 
-// The workgroups' sums of each column, added: 16 columns a workgroup, 64 threads a
-// column (with 16 of them, 777 sums of 1001 columns take 6.5 us; with 64 3.5).
+// The workgroups' sums of each column, added: COLS columns a workgroup, 1024 / COLS
+// threads a column.  32 columns are whole lines, 16 leave more threads to a column (777
+// sums of 1001 columns: 4.8 us, with 16 threads a column 6.5).
+template <int COLS>
 __global__ __launch_bounds__(1024) void join_columns_kernel(const float* sums, float* out, int count, int C) {
-    __shared__ double part[16][65];
-    const int first = blockIdx.x * 16, column = threadIdx.x % 16, c = first + column, k = threadIdx.x / 16;
+    constexpr int GROUPS = 1024 / COLS;
+    __shared__ double part[COLS][GROUPS + 1];
+    const int first = blockIdx.x * COLS, column = threadIdx.x % COLS, c = first + column, k = threadIdx.x / COLS;
     double s = 0.0;
     if (c < C) {
 #pragma unroll 8
-        for (int i = k; i < count; i += 64) s += sums[(long long)i * C + c];
+        for (int i = k; i < count; i += GROUPS) s += sums[(long long)i * C + c];
     }
     part[column][k] = s;
     __syncthreads();
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;   // a wave adds a column
-    const double t = lanes_sum(part[wave][lane], 64);
-    if (lane == 0 && first + wave < C) out[first + wave] = (float)t;
+    const int row = threadIdx.x / GROUPS, lane = threadIdx.x % GROUPS;   // GROUPS lanes add a column
+    const double t = lanes_sum(part[row][lane], GROUPS);
+    if (lane == 0 && first + row < C) out[first + row] = (float)t;
 }
 
 // ------------------------------------------------------------------ host
@@ -331,11 +334,16 @@ template <typename T, int V, int J, int NT, bool QUANT> hipError_t forward(const
 // Rows that a workgroup's lanes sum in fp32 before fp64 takes over.
 constexpr int kMostRows = 512;
 
+// Workgroups of the gradients, each with sums of its own to join: two waves for every
+// vector unit, or one workgroup for every compute unit, of at least two rows (16384 x
+// 4096 bf16: 98.8 us with 512 workgroups, 104 with 768, 107 with 1024).
 long long bwd_blocks(int M, const RowShape& s) {
-    const int rows = block_of(s) / s.lanes;
-    const long long all = ((long long)M + rows - 1) / rows;
-    long long blocks = all < 1024 ? all : 1024;
-    const long long least = (all + kMostRows - 1) / kMostRows;
+    const int threads = block_of(s), rows = threads / s.lanes;
+    const long long all = ((long long)M + rows - 1) / rows, least = (all + kMostRows - 1) / kMostRows;
+    long long blocks = 2 * 4 * 64 * 256 / threads;
+    if (blocks > (all + 1) / 2) blocks = (all + 1) / 2;
+    if (blocks < 256) blocks = 256;
+    if (blocks > all) blocks = all;
     return blocks > least ? blocks : least;
 }
 
@@ -382,7 +390,8 @@ template <Pass P> hipError_t launch(const RmsArgs& a, float* sums, hipStream_t s
 }  // namespace
 
 hipError_t launch_join_columns(const float* sums, float* out, int count, int C, hipStream_t st) {
-    join_columns_kernel<<<(C + 15) / 16, 1024, 0, st>>>(sums, out, count, C);
+    if (C >= 2048) join_columns_kernel<32><<<(C + 31) / 32, 1024, 0, st>>>(sums, out, count, C);
+    else join_columns_kernel<16><<<(C + 15) / 16, 1024, 0, st>>>(sums, out, count, C);
     return hipGetLastError();
 }
 
