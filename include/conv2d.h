@@ -453,16 +453,17 @@ int conv2d_rms_norm_bwd(const void* dy, const void* dh, const void* h, const flo
  * conv2d_matmul_bwd -- the gradients from dy, z (ignored without an activation), x
  *   and w:
  *     dz = dy * act'(z),  dx = dz w,  dw = dz^T x,  dbias[n] = sum_m dz
- *   ReLU's derivative at 0 is 0.  dx [M][K], dw [N][K] of dtype, dbias fp32 [N]: written
- *   (not added to), each may be NULL when it is not wanted.  bf16: dz is rounded to bf16 before the two products, as
- *   the matrix unit takes it; dbias is the sum of the unrounded dz.  (The
- *   residual's gradient is dy.)  The outputs must not overlap the inputs.
+ *   ReLU's derivative at 0 is 0.  dx [M][K], dw [N][K] of dtype, dbias fp32 [N]:
+ *   written (not added to), each may be NULL when it is not wanted.  bf16: dz is
+ *   rounded to bf16 before the two products, as the matrix unit takes it; dbias is
+ *   the sum of the unrounded dz.  (The residual's gradient is dy.)  The outputs must
+ *   not overlap the inputs.
  *
- * K >= 1, M, N >= 1; strides of dy, z, x and w up to 2^20 elements, and of M, K and N no product of two
- * 64-wide tile counts above 2^24 (CONV2D_ERR_UNSUPPORTED).  Any stride and
- * alignment works; 16-byte aligned pointers with strides (and, of what is summed
- * along a row, lengths) that are multiples of 16 bytes are fastest.  Sums have a
- * fixed order: equal calls give equal bits.
+ * Row strides of x and w, and of dy and z in the backward pass, are at most 2^20
+ * elements; ceil(M/64) ceil(N/64), ceil(M/64) ceil(K/64) and ceil(N/64) ceil(K/64) are
+ * below 2^24 (otherwise CONV2D_ERR_UNSUPPORTED).  Any stride and alignment works;
+ * 16-byte aligned pointers with strides, and a K, that are multiples of 16 bytes are
+ * fastest.  Sums have a fixed order: equal calls give equal bits.
  *
  * workspace: as for the group norm, conv2d_matmul_workspace_bytes and
  * conv2d_matmul_bwd_workspace_bytes (0: none is needed, NULL will do).  The calls
