@@ -45,3 +45,27 @@ def test_gradients(M, C, F):
 def test_training_runs():
     losses = block.train(5)
     assert len(losses) == 5 and np.isfinite(losses).all()
+
+
+def test_two_blocks_at_once():
+    """Two blocks on two streams, each with its own workspace: the bits of each alone."""
+    import torch
+    blocks = [block.Block(600, 512, 1024, seed=s) for s in (1, 2)]
+    data = [block.inputs(600, 512, s) for s in (3, 4)]
+    want = []
+    for b, (x, r, dy) in zip(blocks, data):
+        b.forward(x, r)
+        b.backward(dy)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in (b.y, b.dx, *b.grads.values())])
+    streams = [torch.cuda.Stream() for _ in blocks]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for b, (x, r, dy), s in zip(blocks, data, streams):
+            with torch.cuda.stream(s):
+                b.forward(x, r)
+                b.backward(dy)
+    torch.cuda.synchronize()
+    for b, w in zip(blocks, want):
+        for got, t in zip((b.y, b.dx, *b.grads.values()), w):
+            assert torch.equal(got, t)
