@@ -786,8 +786,12 @@ bool aligned_operand(const void* p, long long ld, int K, int es, bool strided, b
 template <typename T, bool TA, bool TB, Output MODE>
 hipError_t tiled(const Product& p, const Plan& q, bool aligned, float* sums, hipStream_t st) {
     const unsigned blocks = (unsigned)(q.tm * q.tn * q.splits);
-    if (q.b == 256) matmul_tile_kernel<T, 256, 256, 2, 4, TA, TB, MODE><<<blocks, 512, 0, st>>>(p, q.tm, q.tn, q.stages, sums);
-    else if (q.b == 128 && aligned)
+    if constexpr (MODE != kSums)   // tiles of 256 are enough for the chip and never split
+        if (q.b == 256) {
+            matmul_tile_kernel<T, 256, 256, 2, 4, TA, TB, MODE><<<blocks, 512, 0, st>>>(p, q.tm, q.tn, q.stages, sums);
+            return hipGetLastError();
+        }
+    if (q.b == 128 && aligned)
         matmul_tile_kernel<T, 128, 128, 2, 2, TA, TB, MODE><<<blocks, 256, 0, st>>>(p, q.tm, q.tn, q.stages, sums);
     else if (q.b == 128)
         matmul_staged_kernel<T, 128, 128, 2, 2, TA, TB, MODE><<<blocks, 256, 0, st>>>(p, q.tm, q.tn, q.stages, sums);

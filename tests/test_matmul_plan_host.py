@@ -1,5 +1,6 @@
 """Which kernel form a product's sizes take (csrc/matmul_plan.hpp): the sizes that the GPU tests run by form are of the
 forms they are named for, and every form that some size takes has one."""
+import ctypes
 import itertools
 
 import pytest
@@ -35,3 +36,15 @@ def test_timed_sizes(lib):
     for kind, M, K, N, name in [("dx", 8192, 4096, 4096, "256 aligned"), ("dw", 8192, 4096, 4096, "256 aligned"),
                                 ("dx", 100352, 256, 64, "128 aligned"), ("dw", 100352, 256, 64, "64 aligned parts")]:
         assert pf.form(lib, kind, M, K, N, "bf16") == name
+
+
+def test_tiles_of_256_are_never_split(lib):
+    """No kernel is built that would write their parts."""
+    out = (ctypes.c_int * 3)()
+    sizes = [129, 256, 257, 1024, 4096, 4097, 16384, 65536, 1 << 20, 1 << 24]
+    seen = 0
+    for rows, cols, K, es in itertools.product(sizes, sizes, [513, 1025, 4096, 1 << 20, 1 << 24], (2, 4)):
+        lib.plan_tiles(rows, cols, K, es, 1, out)
+        seen += out[0] == 256
+        assert out[0] != 256 or out[1] == 1, (rows, cols, K, es)
+    assert seen
