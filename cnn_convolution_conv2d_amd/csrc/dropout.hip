@@ -67,7 +67,7 @@ __global__ __launch_bounds__(256) void dropout_kernel(DropoutArgs a, int vecs, l
         const T* r = static_cast<const T*>(a.residual) + (RES ? row * a.ldr + c : 0);
         T* y = static_cast<T*>(a.y) + row * a.ldy + c;
         float v[V], rv[V] = {};
-        if (c + V <= a.C) {
+        if (c <= a.C - V) {   // (c + V may pass 2^31)
             Vec<T, V>::unpack(Vec<T, V>::load(x), v);
             if constexpr (RES) Vec<T, V>::unpack(Vec<T, V>::load(r), rv);
             drop<T, V>(v, rv, c, (int)row, seed, offset, a.threshold, a.scale);
@@ -106,7 +106,7 @@ template <typename T, bool RES> hipError_t dropout(const DropoutArgs& a, hipStre
     if (e != hipSuccess) return e;
     constexpr int V = 16 / (int)sizeof(T);
     constexpr auto kernel = dropout_kernel<T, V, RES>;
-    const int vecs = (a.C + V - 1) / V;
+    const int vecs = a.C / V + (a.C % V != 0);
     const long long all = ((long long)a.M * vecs + 255) / 256;
     const long long most = (long long)cu_count(dev) * blocks_per_cu<kernel>(256, dev);
     const long long blocks = all < most ? all : most;
