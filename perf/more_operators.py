@@ -104,6 +104,22 @@ def _type(case):
     return torch.float32 if case["dtype"] == "f32" else torch.bfloat16
 
 
+def workspace_bytes(case):
+    """What the library's size functions ask for."""
+    import cnn_convolution_conv2d_amd as c2
+    op, m = case["op"], case["m"]
+    dt = c2.F32 if case["dtype"] == "f32" else c2.BF16
+    if op == "matmul":
+        return c2.conv2d_matmul_workspace_bytes(m, case["k"], case["n"], dt)
+    if op == "matmul_bwd":
+        return c2.conv2d_matmul_bwd_workspace_bytes(m, case["k"], case["n"], dt)
+    if op == "rms_linear":
+        return c2.conv2d_int8_matmul_workspace_bytes(m, case["c"], case["n"])
+    if op == "rms_bwd":
+        return c2.conv2d_rms_norm_bwd_workspace_bytes(m, case["c"])
+    return 0
+
+
 def prepare(case, seed):
     gen = torch.Generator(device="cuda")
     gen.manual_seed(seed)
@@ -111,10 +127,11 @@ def prepare(case, seed):
     t, m, op = _type(case), case["m"], case["op"]
     empty = lambda *s, dtype=t: torch.empty(*s, dtype=dtype, device="cuda")  # noqa: E731
     s = dict(case=case)
+    if own:
+        s["workspace"] = empty(workspace_bytes(case), dtype=torch.uint8)
     if op in ("matmul", "matmul_bwd"):
         k, n = case["k"], case["n"]
         s["x"], s["w"] = rand(m, k).to(t), (rand(n, k) / math.sqrt(k)).to(t)
-        s["workspace"] = empty(4 * m * n + (128 << 20), dtype=torch.uint8)
         if op == "matmul":
             s["bias"] = 0.1 * rand(n) if case["bias"] else None
             s["residual"] = rand(m, n).to(t) if case["residual"] else None
@@ -142,7 +159,6 @@ def prepare(case, seed):
         s["dy"] = rand(m, c).to(t)
         s["dh"] = rand(m, c).to(t) if case["dh"] else None
         s["dx"], s["dgamma"] = empty(m, c), empty(c, dtype=torch.float32)
-        s["workspace"] = empty(64 << 20, dtype=torch.uint8)
         return s
     s["h"] = empty(m, c) if case["residual"] else None   # without a residual h is x
     if op == "rms":
@@ -153,7 +169,7 @@ def prepare(case, seed):
     a = v.abs().amax(1)
     s["w"], s["w_scale"] = torch.round(v * (127.0 / a)[:, None]).to(torch.int8), a / (127.0 * math.sqrt(c))
     s["q"], s["q_scale"] = empty(m, c, dtype=torch.int8), empty(m, dtype=torch.float32)
-    s["y"], s["workspace"] = empty(m, case["n"]), empty(128 << 20, dtype=torch.uint8)
+    s["y"] = empty(m, case["n"])
     return s
 
 
