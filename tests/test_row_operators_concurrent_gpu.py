@@ -186,3 +186,38 @@ def test_norm_and_dropout_on_a_side_stream(M, C, dtype):
         step(*sets[turn % 2], side)
         side.synchronize()
         same((*outs, q), want[turn % 2], turn)
+
+
+def test_training_in_a_graph_is_the_eager_steps(monkeypatch):
+    """The example's training: its parameters and gradients after some replays are those of eager steps, bit by bit; every
+    parameter has moved and the mask's offset went up once a step."""
+    made = []
+
+    class Kept(block.Block):
+        def __init__(self, *a, **k):
+            super().__init__(*a, **k)
+            made.append(self)
+
+    M, C, F, rate, steps = 200, 128, 256, 0.005, 4
+    plain = block.Block
+    monkeypatch.setattr(block, "Block", Kept)
+    losses = block.train(steps, M, C, F, rate)
+    teacher, trained = made
+    eager = plain(M, C, F, seed=2)
+    x, r, dy = block.inputs(M, C, 6)
+    target = teacher.y   # its only pass's
+    eager.rng[1] = 1     # the step before the capture, whose update is taken back
+    for i in range(steps):
+        before = {n: getattr(eager, n).clone() for n in eager.grads}
+        eager.rng[1].add_(1)
+        dy.copy_((eager.forward(x, r).float() - target.float()) * (2 / M))
+        eager.backward(dy)
+        for n, g in eager.grads.items():
+            getattr(eager, n).sub_(g, alpha=rate)
+            assert not torch.equal(getattr(eager, n), before[n]), (i, n)
+        assert losses[i] == float((eager.y.float() - target.float()).square().sum(1).mean())
+    assert trained.rng.tolist() == [2, 1 + steps]
+    for n in eager.grads:
+        assert torch.equal(getattr(trained, n), getattr(eager, n)), n
+        assert torch.equal(trained.grads[n], eager.grads[n]), n
+    same(results(trained), results(eager), "results")
