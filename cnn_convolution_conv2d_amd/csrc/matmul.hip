@@ -716,8 +716,9 @@ __global__ __launch_bounds__(256) void matmul_pack_kernel(Packed<T> a, Packed<T>
 
 // dz = dy act'(z) (rounded to T; null: not wanted), rows padded with zeros to ldd
 // elements, and the sums of its columns over a workgroup's rows before the
-// rounding, [row chunk][N] (null: not wanted).  256 threads: `lanes` vectors of a
-// row, 256 / lanes rows at a time.
+// rounding, [row chunk][N] (null: not wanted): a thread's in fp32, the workgroup's
+// over its threads in fp64.  256 threads: `lanes` vectors of a row, 256 / lanes rows
+// at a time.
 template <typename T, bool ACT>
 __global__ __launch_bounds__(256) void matmul_dz_kernel(MatmulBwdArgs a, T* dz, int ldd, float* sums, int lanes, int chunk) {
     constexpr int V = kPiece<T>;
@@ -761,9 +762,9 @@ __global__ __launch_bounds__(256) void matmul_dz_kernel(MatmulBwdArgs a, T* dz, 
     __syncthreads();
     for (int i = threadIdx.x; i < lanes * V; i += 256) {
         const int n = blockIdx.x * lanes * V + i;
-        float t = 0.0f;
+        double t = 0.0;
         for (int g = 0; g < groups; ++g) t += part[g * lanes + i / V][i % V];
-        if (n < a.N) sums[(long long)blockIdx.y * a.N + n] = t;
+        if (n < a.N) sums[(long long)blockIdx.y * a.N + n] = (float)t;
     }
 }
 

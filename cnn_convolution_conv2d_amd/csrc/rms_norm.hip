@@ -182,7 +182,8 @@ __global__ __launch_bounds__(NT) void rms_norm_kernel(RmsArgs a, int lanes) {
     }
 }
 
-// Partial sums of dgamma: [workgroup][C], a workgroup's over its rows in fp32.
+// Partial sums of dgamma: [workgroup][C], a lane's over its rows in fp32, a workgroup's
+// over its lanes in fp64, rounded once.
 template <typename T, int V, int J, int NT>
 __global__ __launch_bounds__(NT) void rms_norm_bwd_kernel(RmsArgs a, int lanes, float* sums) {
     __shared__ float red[16];
@@ -268,9 +269,9 @@ __global__ __launch_bounds__(NT) void rms_norm_bwd_kernel(RmsArgs a, int lanes, 
     }
     __syncthreads();
     for (int c = threadIdx.x; c < a.C; c += blockDim.x) {
-        float s = 0.0f;
+        double s = 0.0;
         for (int g = 0; g < rows; ++g) s += joined[g * a.C + c];
-        sums[c] = s;
+        sums[c] = (float)s;
     }
 }
 
@@ -333,7 +334,7 @@ template <typename T, int V, int J, int NT, bool QUANT> hipError_t forward(const
     return hipGetLastError();
 }
 
-// Rows that a workgroup's lanes sum in fp32 before fp64 takes over.
+// Rows that a lane sums in fp32 before fp64 takes over.
 constexpr int kMostRows = 512;
 
 // Workgroups of the gradients, each with sums of its own to join: two waves for every
