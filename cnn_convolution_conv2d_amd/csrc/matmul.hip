@@ -41,9 +41,11 @@ enum { kGelu = 3 };   // CONV2D_ACT_GELU; the others as in rowvec.hpp
 
 // 1 - Phi(x), Phi the standard normal's distribution function, for x >= 0:
 // exp(-x^2 / 2) times a polynomial in 1 / (1 + 0.3 x), fitted by least squares of the
-// relative error, weighted towards its maximum, up to x = 15 (6e-8; 7 u in fp32 with
-// the reciprocal's and the exponential's).  So GELU keeps its digits on the negative
-// side, where 1 + erf has none left.
+// relative error, weighted towards its maximum, up to x = 15 (6e-8).  In fp32 the
+// exponential's argument is off by up to 3 u of itself (u = 2^-24), 1.5 x^2 u of the
+// value, beside some 7 u of the other steps: 7 u up to x = 1, 10 u up to 3, 23 u up to
+// 5, 125 u up to 13.  So GELU keeps most of its digits on the negative side, where
+// 1 + erf has none left, and as many as z's own rounding (x^2 u there) leaves it.
 __device__ __forceinline__ float normal_above(float x) {
     const float t = __builtin_amdgcn_rcpf(fmaf(0.3f, x, 1.0f));
     float q = 3.842540085315704e-2f;
