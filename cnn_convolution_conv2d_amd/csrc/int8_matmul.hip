@@ -141,6 +141,23 @@ __device__ __forceinline__ void products(i32x4 (&acc)[TI][TJ], const i32x4 (&w)[
         }
 }
 
+// 16 bytes of results (8 bf16, 4 fp32 or int) to channels n .. of a row, fewer
+// at the row's end.  The address is aligned to an element only (a row may have
+// any length): one store all the same.
+template <typename OUT> __device__ __forceinline__ void store_piece(OUT* row, int n, int N, const uint4& v) {
+    constexpr int E = 16 / (int)sizeof(OUT);
+    if (n + E <= N) {
+        *reinterpret_cast<u32x4_unaligned*>(row + n) = __builtin_bit_cast(u32x4, v);
+    } else {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (n + e < N)
+                row[n + e] = sizeof(OUT) == 4 ? __builtin_bit_cast(OUT, (typename RawBytes<sizeof(OUT)>::type)w[e * (int)sizeof(OUT) / 4])
+                                              : __builtin_bit_cast(OUT, (typename RawBytes<sizeof(OUT)>::type)(w[e / 2] >> (16 * (e & 1))));
+    }
+}
+
 // Four channels of a row: scaled, biased, ReLU.
 __device__ __forceinline__ float4 finish4(const Int8Args& a, const i32x4& acc, float qs, const float* sw,
                                           const float* sb) {
@@ -387,6 +404,8 @@ __device__ __forceinline__ void stream_barrier() {
     __builtin_amdgcn_s_barrier();
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
+
+constexpr int vmcnt_of(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0f70; }  // lgkmcnt, expcnt: no wait
 
 // Block j of 16 rows of a wave's results to memory, straight from registers:
 // fp32 lanes hold 16 bytes already; bf16 ones hold 8, and the exchange of

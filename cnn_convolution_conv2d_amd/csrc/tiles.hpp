@@ -1,6 +1,5 @@
 // tiles.hpp -- device helpers shared by the tiled products (8-bit integers, bf16
-// and fp32): the stages' layout in LDS, copies into it, the order of the tiles
-// and the stores of their results.
+// and fp32): the stages' layout in LDS, copies into it and the order of the tiles.
 #pragma once
 
 #include "mfma.hpp"
@@ -48,29 +47,10 @@ __device__ __forceinline__ void wave_lds_fence() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// 16 bytes of results (8 bf16, 4 fp32 or int) to channels n .. of a row, fewer
-// at the row's end.  The address is aligned to an element only (a row may have
-// any length): one store all the same.
-template <typename OUT> __device__ __forceinline__ void store_piece(OUT* row, int n, int N, const uint4& v) {
-    constexpr int E = 16 / (int)sizeof(OUT);
-    if (n + E <= N) {
-        *reinterpret_cast<u32x4_unaligned*>(row + n) = __builtin_bit_cast(u32x4, v);
-    } else {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (n + e < N)
-                row[n + e] = sizeof(OUT) == 4 ? __builtin_bit_cast(OUT, (typename RawBytes<sizeof(OUT)>::type)w[e * (int)sizeof(OUT) / 4])
-                                              : __builtin_bit_cast(OUT, (typename RawBytes<sizeof(OUT)>::type)(w[e / 2] >> (16 * (e & 1))));
-    }
-}
-
 // A wave's copy of 1 KB into LDS, 16 bytes a lane: no registers, no LDS
 // instruction; an offset outside the matrix writes zeros.
 __device__ __forceinline__ void copy_kb(__amdgpu_buffer_rsrc_t r, char* dst, int off) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)dst, 16, off, 0, 0, 0);
 }
-
-constexpr int vmcnt_of(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0f70; }  // lgkmcnt, expcnt: no wait
 
 }  // namespace conv2d
