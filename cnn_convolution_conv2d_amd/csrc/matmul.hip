@@ -19,14 +19,17 @@
 //
 //   tile    aligned operands: stages copied from memory into two LDS buffers without
 //           passing through registers, tiles of 256, 128 or 64.  8192^3 bf16 with bias, SiLU
-//           and residual: 800 us, 1375 TFLOP/s (780 without the epilogue; the matrix units
+//           and residual: 806 us, 1364 TFLOP/s (770 without the epilogue; the matrix units
 //           are busy for 71% of the cycles, at the 1.7 GHz that the socket's power leaves);
-//           both gradients of 8192 x 4096 -> 4096: 197 us each, 1400 TFLOP/s.  No bank
-//           conflicts, in transposing reads neither.
-//   staged  operands of any alignment, through registers; large ones are copied to whole
-//           pieces first and take the tiles.
+//           dx and dw of 8192 x 4096 -> 4096: 194 and 190 us, 1430 TFLOP/s.  fp32, 4096^3:
+//           938 us, 147 TFLOP/s; dx 920, dw 954, whose 256 registers leave 7 in scratch.  No
+//           bank conflicts, in transposing reads neither.
+//   staged  operands of any alignment, through registers.  Where K is no whole number of
+//           16-byte pieces, large products copy x and w to whole pieces first and take the
+//           tiles.  A whole K with other strides or addresses is not copied: 4096^3 bf16 with
+//           rows 4097 apart 217 us, 4096 apart 114.
 //   skinny  up to 32 rows of the forward product: the weights stream through registers.
-//           One row of 4096, 16384 columns: 134 MB in 26.6 us, 5.0 TB/s.
+//           One row of 4096, 16384 columns: 134 MB in 26.7 us, 5.0 TB/s.
 #include <type_traits>
 
 #include "matmul_plan.hpp"
@@ -716,11 +719,15 @@ __global__ __launch_bounds__(256) void matmul_pack_kernel(Packed<T> a, Packed<T>
 
 // ------------------------------------------------------------------ dz
 
-// dz = dy act'(z) (rounded to T; null: not wanted), rows padded with zeros to ldd
-// elements, and the sums of its columns over a workgroup's rows before the
-// rounding, [row chunk][N] (null: not wanted): a thread's in fp32, the workgroup's
-// over its threads in fp64.  256 threads: `lanes` vectors of a row, 256 / lanes rows
-// at a time.
+// dz = dy act'(z) (null: not wanted), rows padded with zeros to ldd elements, and the
+// sums of its columns over a workgroup's rows, [row chunk][N] (null: not wanted): a
+// thread's in fp32, the workgroup's over its threads in fp64.  256 threads: `lanes`
+// vectors of a row, 256 / lanes rows at a time.
+//
+// The sums are of the unrounded values; dz itself is rounded to T, as the matrix unit
+// takes bf16.  After SiLU or GELU that is half a step at most of every term of dx and dw,
+// whose error against fp64 grows from their own rounding's 0.0017 to 0.0023 (rms, 8192 x
+// 4096 -> 4096); a second bf16 part of dz would keep it, at twice the products' time.
 template <typename T, bool ACT>
 __global__ __launch_bounds__(256) void matmul_dz_kernel(MatmulBwdArgs a, T* dz, int ldd, float* sums, int lanes, int chunk) {
     constexpr int V = kPiece<T>;

@@ -61,11 +61,12 @@ inline int whole_pieces(int n, int es) { return (n + 16 / es - 1) / (16 / es) * 
 
 // Whether a product is large enough for copies of its operands with whole pieces: the
 // tiles of aligned operands then save more than the copies take (bf16 with copies and
-// without: 4096 x 4095 -> 4096 148 and 230 us, 2048 x 2047 -> 2048 38 and 47, gradients of
+// without: 4096 x 4095 -> 4096 133 and 230 us, 2048 x 2047 -> 2048 38 and 47, gradients of
 // 4096 x 1001 -> 2001 91 and 201; fp32 is bound by its products sooner).
 inline bool worth_copies(int M, int K, int N, int es) { return (double)M * N * K * (es == 4 ? 8 : 1) >= 0x1p32; }
 
-// Whether rows of K elements are copied: for two products (the gradients), or for one
+// Whether rows of K elements are copied (by K alone: a whole K at other strides or
+// addresses is read as it lies): for two products (the gradients), or for one
 // that uses an operand's elements often enough (24266 x 2092 -> 367 121 and 97 us).
 inline bool packs(int M, int K, int N, int es) { return (long long)K * es % 16 != 0 && worth_copies(M, K, N, es); }
 inline bool packs_forward(int M, int K, int N, int es) { return packs(M, K, N, es) && (double)M * N >= 500.0 * ((double)M + N); }

@@ -305,14 +305,17 @@ int vector_elements(int C, int es) {
     return v;
 }
 
-// 16 elements a lane at most: with 32 the gradients' sums leave the registers.
+// 16 elements a lane at most: with 32 the gradients' sums leave the registers (with 1024
+// threads a row and fp32 they do already: 4096 x 16384 300 us, 3.5 TB/s).
 constexpr int kMostElements = 16;
 
 RowShape row_shape(int M, int C, int es) {
     RowShape s;
     s.vec = vector_elements(C, es);
     const int vecs = (C + s.vec - 1) / s.vec;
-    // few rows: a vector a lane; many: as many as give a row to one wave
+    // few rows: a vector a lane; many: as many as give a row to one wave.  Lanes are a power
+    // of two, so a row just longer than one has half of its lanes nearly empty (3699 x 8256
+    // bf16 65 us, 8192 columns 47.6)
     s.lanes = 1;
     const int per = M >= 1024 ? kMostElements / s.vec : 1;
     while (s.lanes < 1024 && s.lanes * (s.lanes < 64 ? 1 : per) < vecs) s.lanes <<= 1;

@@ -417,10 +417,11 @@ int conv2d_int8_matmul(const void* q, const float* q_scale, const void* w, const
  *   dx is the gradient of x and of the residual alike; dgamma fp32 [C] is written
  *   (not added to), or NULL.  dx may lie over dy, dh or h (same stride).
  *
- * gamma: fp32 [C]; NULL means 1.  eps >= 0 and finite.  C <= 16384, any M, stride
- * and alignment; C, the strides and the pointers as multiples of 16 bytes are
- * fastest.  Sums have a fixed order: equal calls give equal bits.  A NaN or
- * infinity stays in its row (and its columns of dgamma).
+ * gamma: fp32 [C]; NULL means 1.  eps >= 0 and finite (with eps = 0 a row of zeros
+ * gives NaN, 0 times an infinite rstd).  C <= 16384, any M, stride and alignment;
+ * C, the strides and the pointers as multiples of 16 bytes are fastest.  Sums have a
+ * fixed order: equal calls give equal bits.  A NaN or infinity stays in its row (and
+ * its columns of dgamma).
  *
  * workspace: as for the group norm, conv2d_rms_norm_bwd_workspace_bytes(M, C)
  * bytes; not needed (NULL) when dgamma is NULL.  The calls allocate nothing and
@@ -466,8 +467,9 @@ int conv2d_rms_norm_bwd(const void* dy, const void* dh, const void* h, const flo
  * fastest.  Sums have a fixed order: equal calls give equal bits.
  *
  * workspace: as for the group norm, conv2d_matmul_workspace_bytes and
- * conv2d_matmul_bwd_workspace_bytes (0: none is needed, NULL will do).  The calls
- * allocate nothing and may be captured into a graph.
+ * conv2d_matmul_bwd_workspace_bytes (0: none is needed, NULL will do), which hold for
+ * any strides, alignment, activation and choice of outputs.  The calls allocate
+ * nothing and may be captured into a graph.
  */
 size_t conv2d_matmul_workspace_bytes(int M, int K, int N, int dtype);
 int conv2d_matmul(const void* x, const void* w, const float* bias, const void* residual, void* z, void* y,
