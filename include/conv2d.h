@@ -445,7 +445,8 @@ int conv2d_rms_norm_bwd(const void* dy, const void* dh, const void* h, const flo
  * [N][K], residual, z and y [M][N] are fp32 or bf16 (dtype), ld* elements from
  * one row to the next; bias is fp32 [N].  Products are exact, sums and everything
  * after them fp32 (fp32 operands: fp32 fused multiply-adds), each output is rounded
- * once, y from the unrounded z.
+ * once, y from the unrounded z.  Below z = -87.3, where SiLU and its slope are smaller
+ * than 1.1e-36, they may be 0.
  *
  * conv2d_matmul -- y, and z where it is not NULL (what the gradients need when
  *   there is an activation).  bias and residual may be NULL.  y may lie over the
